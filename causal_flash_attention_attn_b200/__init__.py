@@ -9,9 +9,15 @@ tensor or an integer device address). ``attention_fwd`` / ``attention_bwd`` /
 PyTorch is used for device memory and streams only; all arithmetic runs in the
 library's CUDA kernels. There is no fallback: if the shared library is missing
 or fails to load, every call raises.
+
+Packed sequences of different lengths: ``attention_varlen_fwd`` / ``_bwd`` and
+``attention_varlen`` (autograd). A paged KV cache: ``attention_decode_paged``,
+``paged_append``, ``paged_copy``, and ``PagedCache``, which keeps a pool's books
+(pages of each sequence, forks, compaction) and calls them.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import math
 import os
@@ -26,6 +32,11 @@ __all__ = [
     "forge_attn_bwd_preprocess", "forge_attn_bwd_main", "forge_attn_bwd_finalize", "forge_attn_check",
     "forge_attn_status_string", "forge_attn_selftest_timeout", "forge_attn_selftest_exp2", "forge_attn_last_cuda_error", "forge_attn_timeout_info", "forge_attn_version",
     "attention_fwd", "attention_bwd", "attention", "dtype_code",
+    "forge_attn_varlen_fwd", "forge_attn_varlen_fwd_workspace_size", "forge_attn_varlen_bwd",
+    "forge_attn_varlen_bwd_workspace_size", "forge_attn_decode_paged", "forge_attn_decode_paged_workspace_size",
+    "forge_attn_paged_append", "forge_attn_paged_copy",
+    "attention_varlen_fwd", "attention_varlen_bwd", "attention_varlen", "attention_decode_paged", "paged_append",
+    "paged_copy", "PagedCache",
 ]
 
 FORGE_OK = 0
@@ -93,6 +104,22 @@ def library():
     L.forge_attn_bwd_main.restype = i
     L.forge_attn_bwd_finalize.argtypes = [vp, i, i, i, i, i, i, vp, st, vp]
     L.forge_attn_bwd_finalize.restype = i
+    L.forge_attn_varlen_fwd_workspace_size.argtypes = [i, i, i, i, i, i]
+    L.forge_attn_varlen_fwd_workspace_size.restype = st
+    L.forge_attn_varlen_fwd.argtypes = ([vp] * 6 + [i] * 5 + [st] * 3 + [f, i, f, vp, i, i, vp, st, vp])
+    L.forge_attn_varlen_fwd.restype = i
+    L.forge_attn_varlen_bwd_workspace_size.argtypes = [i, i, i, i, i, i]
+    L.forge_attn_varlen_bwd_workspace_size.restype = st
+    L.forge_attn_varlen_bwd.argtypes = ([vp] * 10 + [i] * 5 + [st] * 3 + [f, i, f, vp, vp, i, i, vp, st, vp])
+    L.forge_attn_varlen_bwd.restype = i
+    L.forge_attn_decode_paged_workspace_size.argtypes = [i, i, i, i, i]
+    L.forge_attn_decode_paged_workspace_size.restype = st
+    L.forge_attn_decode_paged.argtypes = [vp] * 7 + [i] * 7 + [st, f, i, f, vp, i, vp, st, vp]
+    L.forge_attn_decode_paged.restype = i
+    L.forge_attn_paged_append.argtypes = [vp] * 7 + [i] * 7 + [st, st, st, i, vp]
+    L.forge_attn_paged_append.restype = i
+    L.forge_attn_paged_copy.argtypes = [vp] * 4 + [i, i, st, i, i, i, i, st, i, vp]
+    L.forge_attn_paged_copy.restype = i
     L.forge_attn_check.argtypes = [vp]
     L.forge_attn_check.restype = i
     L.forge_attn_status_string.argtypes = [i]
@@ -222,6 +249,62 @@ def forge_attn_bwd_main(q, k, v, lse, dO, dq, dk, dv, B, Hq, Hkv, T, D, scale, w
 def forge_attn_bwd_finalize(dq, B, Hq, Hkv, T, D, dtype, workspace, workspace_bytes, stream=None) -> int:
     return library().forge_attn_bwd_finalize(_ptr(dq), B, Hq, Hkv, T, D, int(dtype), _ptr(workspace),
                                              int(workspace_bytes), _stream(stream))
+
+
+def forge_attn_varlen_fwd_workspace_size(num_seqs, rows, Hq, Hkv, D, dtype) -> int:
+    return int(library().forge_attn_varlen_fwd_workspace_size(num_seqs, rows, Hq, Hkv, D, int(dtype)))
+
+
+def forge_attn_varlen_fwd(q, k, v, o, lse, cu_seqlens, num_seqs, rows, Hq, Hkv, D, q_stride, k_stride, v_stride, scale,
+                          window, softcap, sink, clear_tail, dtype, workspace, workspace_bytes, stream=None) -> int:
+    return library().forge_attn_varlen_fwd(_ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(lse), _ptr(cu_seqlens), num_seqs,
+                                           rows, Hq, Hkv, D, int(q_stride), int(k_stride), int(v_stride), float(scale),
+                                           int(window), float(softcap), _ptr(sink), int(clear_tail), int(dtype),
+                                           _ptr(workspace), int(workspace_bytes), _stream(stream))
+
+
+def forge_attn_varlen_bwd_workspace_size(num_seqs, rows, Hq, Hkv, D, dtype) -> int:
+    return int(library().forge_attn_varlen_bwd_workspace_size(num_seqs, rows, Hq, Hkv, D, int(dtype)))
+
+
+def forge_attn_varlen_bwd(q, k, v, o, lse, dO, dq, dk, dv, cu_seqlens, num_seqs, rows, Hq, Hkv, D, q_stride, k_stride,
+                          v_stride, scale, window, softcap, sink, dsink, clear_tail, dtype, workspace, workspace_bytes,
+                          stream=None) -> int:
+    return library().forge_attn_varlen_bwd(_ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(lse), _ptr(dO), _ptr(dq), _ptr(dk),
+                                           _ptr(dv), _ptr(cu_seqlens), num_seqs, rows, Hq, Hkv, D, int(q_stride),
+                                           int(k_stride), int(v_stride), float(scale), int(window), float(softcap),
+                                           _ptr(sink), _ptr(dsink), int(clear_tail), int(dtype), _ptr(workspace),
+                                           int(workspace_bytes), _stream(stream))
+
+
+def forge_attn_decode_paged_workspace_size(B, Hq, Hkv, D, dtype) -> int:
+    return int(library().forge_attn_decode_paged_workspace_size(B, Hq, Hkv, D, int(dtype)))
+
+
+def forge_attn_decode_paged(q, k_pages, v_pages, o, lse, page_table, seq_lens, B, Hq, Hkv, D, num_pages, page_size,
+                            table_width, page_stride, scale, window, softcap, sink, dtype, workspace, workspace_bytes,
+                            stream=None) -> int:
+    return library().forge_attn_decode_paged(_ptr(q), _ptr(k_pages), _ptr(v_pages), _ptr(o), _ptr(lse),
+                                             _ptr(page_table), _ptr(seq_lens), B, Hq, Hkv, D, num_pages, page_size,
+                                             table_width, int(page_stride), float(scale), int(window), float(softcap),
+                                             _ptr(sink), int(dtype), _ptr(workspace), int(workspace_bytes),
+                                             _stream(stream))
+
+
+def forge_attn_paged_append(k, v, k_pages, v_pages, page_table, starts, cu_seqlens, num_seqs, rows, Hkv, D, num_pages,
+                            page_size, table_width, k_stride, v_stride, page_stride, dtype, stream=None) -> int:
+    return library().forge_attn_paged_append(_ptr(k), _ptr(v), _ptr(k_pages), _ptr(v_pages), _ptr(page_table),
+                                             _ptr(starts), _ptr(cu_seqlens), num_seqs, rows, Hkv, D, num_pages,
+                                             page_size, table_width, int(k_stride), int(v_stride), int(page_stride),
+                                             int(dtype), _stream(stream))
+
+
+def forge_attn_paged_copy(k_pages, v_pages, src, dst, n, num_layers, layer_stride, num_pages, Hkv, page_size, D,
+                          page_stride, dtype, stream=None) -> int:
+    """src and dst: host memory (an int32 CPU tensor, or the address of n ints)."""
+    return library().forge_attn_paged_copy(_ptr(k_pages), _ptr(v_pages), _ptr(src), _ptr(dst), n, num_layers,
+                                           int(layer_stride), num_pages, Hkv, page_size, D, int(page_stride),
+                                           int(dtype), _stream(stream))
 
 
 def forge_attn_check(stream=None) -> int:
@@ -432,3 +515,266 @@ def attention(q, k, v, scale=None, window=0, softcap=0.0, sink=None):
     attention_fwd; scale defaults to 1/sqrt(head dim of q)."""
     scale = 1.0 / math.sqrt(q.shape[-1]) if scale is None else float(scale)
     return _attention_function().apply(q, k, v, sink, scale, int(window), float(softcap))
+
+
+# ------------------------------------------------------------ packed sequences
+def _scope(device, stream):
+    """Makes `device`, and the stream if one is given, current: outputs and workspaces allocated inside
+    belong to the stream that the kernels run on."""
+    import torch
+    if stream is not None:
+        return torch.cuda.stream(torch.cuda.ExternalStream(stream, device=device) if isinstance(stream, int) else stream)
+    return contextlib.nullcontext() if torch.cuda.current_device() == device.index else torch.cuda.device(device)
+
+
+def _check_dense(what, device, **specs):
+    """Each name: (tensor or None, dtype, shape). Contiguous, on `device`."""
+    _check(what, {n: d for n, (t, d, s) in specs.items()}, device, {n: s for n, (t, d, s) in specs.items()},
+           **{n: t for n, (t, d, s) in specs.items()})
+
+
+def _check_rows(what, dtype, device, **tensors):
+    """Packed [rows, H, D] tensors whose heads are dense but whose rows may lie apart (parts of one
+    projection's output). Returns their row strides in elements."""
+    import torch
+    strides = []
+    for name, t in tensors.items():
+        if not isinstance(t, torch.Tensor):
+            raise TypeError(f"{what}: {name} must be a torch tensor")
+        if t.dim() != 3:
+            raise ValueError(f"{what}: {name} must be [rows, H, D], got {tuple(t.shape)}")
+        if t.dtype != dtype:
+            raise ValueError(f"{what}: {name} has dtype {t.dtype}, expected {dtype}")
+        rows, H, D = t.shape
+        if (D > 1 and t.stride(2) != 1) or (H > 1 and t.stride(1) != D):
+            raise ValueError(f"{what}: {name}'s heads must be contiguous (strides {t.stride()})")
+        stride = t.stride(0) if rows > 1 else H * D
+        if stride < H * D or stride * t.element_size() % 16:
+            raise ValueError(f"{what}: {name}'s rows must be at least {H * D} elements and a multiple of 16 bytes "
+                             f"apart (stride {stride})")
+        strides.append(stride)
+    for name, t in tensors.items():
+        if not t.is_cuda:
+            raise ValueError(f"{what}: {name} must be a CUDA tensor")
+        if t.device != device:
+            raise ValueError(f"{what}: {name} is on {t.device}, expected {device}")
+    return strides
+
+
+def _check_packed(what, q, k, v, cu_seqlens, sink):
+    import torch
+    for name, t in (("q", q), ("k", k), ("v", v)):
+        if t.dim() != 3:
+            raise ValueError(f"{what}: {name} must be [rows, H, D], got {tuple(t.shape)}")
+    rows, Hq, D = q.shape
+    Hkv = k.shape[1]
+    for name, t in (("k", k), ("v", v)):
+        if tuple(t.shape) != (rows, Hkv, D):
+            raise ValueError(f"{what}: {name} has shape {tuple(t.shape)}, expected {(rows, Hkv, D)}")
+    if cu_seqlens.dim() != 1 or cu_seqlens.numel() < 2:
+        raise ValueError(f"{what}: cu_seqlens must be [num_seqs + 1] with num_seqs >= 1, got {tuple(cu_seqlens.shape)}")
+    strides = _check_rows(what, q.dtype, q.device, q=q, k=k, v=v)
+    _check_dense(what, q.device, cu_seqlens=(cu_seqlens, torch.int32, cu_seqlens.shape),
+                 sink=(sink, torch.float32, (Hq,)))
+    return rows, Hq, Hkv, D, strides
+
+
+def attention_varlen_fwd(q, k, v, cu_seqlens, scale=None, window=0, softcap=0.0, stream=None, *, sink=None):
+    """Causal attention over packed sequences: q [rows,Hq,D], k, v [rows,Hkv,D] (bf16 or f32; their rows
+    may lie apart), cu_seqlens int32 [num_seqs + 1] on the device, from 0. Returns (o [rows,Hq,D], lse
+    [Hq,rows]). Rows behind the last sequence get zeros, lse -inf there. Nothing synchronises; bad
+    cu_seqlens are reported by forge_attn_check."""
+    import torch
+    what = "attention_varlen_fwd"
+    rows, Hq, Hkv, D, (qs, ks, vs) = _check_packed(what, q, k, v, cu_seqlens, sink)
+    scale = 1.0 / math.sqrt(D) if scale is None else scale
+    dt, n = dtype_code(q.dtype), cu_seqlens.numel() - 1
+    with _scope(q.device, stream):
+        o = torch.empty((rows, Hq, D), dtype=q.dtype, device=q.device)
+        lse = torch.empty((Hq, rows), dtype=torch.float32, device=q.device)
+        nbytes = forge_attn_varlen_fwd_workspace_size(n, rows, Hq, Hkv, D, dt)
+        ws = torch.empty(nbytes, dtype=torch.uint8, device=q.device)
+        s = forge_attn_varlen_fwd(q, k, v, o, lse, cu_seqlens, n, rows, Hq, Hkv, D, qs, ks, vs, scale, window, softcap,
+                                  sink, True, dt, ws, nbytes)
+    if s != FORGE_OK:
+        raise ForgeError(s, "forge_attn_varlen_fwd")
+    return o, lse
+
+
+def attention_varlen_bwd(q, k, v, o, lse, dO, cu_seqlens, scale=None, window=0, softcap=0.0, stream=None, *,
+                         sink=None):
+    """Backward of attention_varlen_fwd (its o and lse; dO contiguous). Returns (dq, dk, dv), or (dq, dk,
+    dv, dsink [Hq]) with a sink; zeros in the rows behind the last sequence."""
+    import torch
+    what = "attention_varlen_bwd"
+    rows, Hq, Hkv, D, (qs, ks, vs) = _check_packed(what, q, k, v, cu_seqlens, sink)
+    _check_dense(what, q.device, o=(o, q.dtype, (rows, Hq, D)), lse=(lse, torch.float32, (Hq, rows)),
+                 dO=(dO, q.dtype, (rows, Hq, D)))
+    scale = 1.0 / math.sqrt(D) if scale is None else scale
+    dt, n = dtype_code(q.dtype), cu_seqlens.numel() - 1
+    with _scope(q.device, stream):
+        dq, dk, dv = (torch.empty(x.shape, dtype=x.dtype, device=x.device) for x in (q, k, v))
+        dsink = torch.empty((Hq,), dtype=torch.float32, device=q.device) if sink is not None else None
+        nbytes = forge_attn_varlen_bwd_workspace_size(n, rows, Hq, Hkv, D, dt)
+        ws = torch.empty(nbytes, dtype=torch.uint8, device=q.device)
+        s = forge_attn_varlen_bwd(q, k, v, o, lse, dO, dq, dk, dv, cu_seqlens, n, rows, Hq, Hkv, D, qs, ks, vs, scale,
+                                  window, softcap, sink, dsink, True, dt, ws, nbytes)
+    if s != FORGE_OK:
+        raise ForgeError(s, "forge_attn_varlen_bwd")
+    return (dq, dk, dv, dsink) if sink is not None else (dq, dk, dv)
+
+
+_attention_varlen_fn = None
+
+
+def _attention_varlen_function():
+    global _attention_varlen_fn
+    if _attention_varlen_fn is None:
+        import torch
+
+        class ForgeAttentionVarlen(torch.autograd.Function):
+            @staticmethod
+            def forward(ctx, q, k, v, cu_seqlens, sink, scale, window, softcap):
+                o, lse = attention_varlen_fwd(q, k, v, cu_seqlens, scale, window, softcap, sink=sink)
+                ctx.save_for_backward(q, k, v, o, lse, cu_seqlens, sink)
+                ctx.args = (scale, window, softcap)
+                return o
+
+            @staticmethod
+            def backward(ctx, dO):
+                q, k, v, o, lse, cu_seqlens, sink = ctx.saved_tensors
+                g = attention_varlen_bwd(q, k, v, o, lse, dO.contiguous(), cu_seqlens, *ctx.args, sink=sink)
+                return g[0], g[1], g[2], None, (g[3] if sink is not None else None), None, None, None
+
+        _attention_varlen_fn = ForgeAttentionVarlen
+    return _attention_varlen_fn
+
+
+def attention_varlen(q, k, v, cu_seqlens, scale=None, window=0, softcap=0.0, sink=None):
+    """attention_varlen_fwd with autograd: o, and gradients for q, k, v (and sink) through the
+    library's backward. The lengths must not change between the forward and its backward."""
+    scale = 1.0 / math.sqrt(q.shape[-1]) if scale is None else float(scale)
+    return _attention_varlen_function().apply(q, k, v, cu_seqlens, sink, scale, int(window), float(softcap))
+
+
+# ---------------------------------------------------------------- paged cache
+def _check_pool(what, dtype, device, k_pages, v_pages, layers=False):
+    """[num_pages, Hkv, page_size, D] pools (layers: or [layers, num_pages, ...]) whose pages are dense.
+    Returns (num_layers, layer stride, num_pages, Hkv, page_size, D, page stride), strides in elements."""
+    import torch
+    for name, t in (("k_pages", k_pages), ("v_pages", v_pages)):
+        if not isinstance(t, torch.Tensor):
+            raise TypeError(f"{what}: {name} must be a torch tensor")
+        if t.dim() != 4 and not (layers and t.dim() == 5):
+            raise ValueError(f"{what}: {name} must be [num_pages, Hkv, page_size, D]"
+                             f"{' or [layers, num_pages, Hkv, page_size, D]' if layers else ''}, got {tuple(t.shape)}")
+        if t.dtype != dtype:
+            raise ValueError(f"{what}: {name} has dtype {t.dtype}, expected {dtype}")
+        if t.shape != k_pages.shape or t.stride() != k_pages.stride():
+            raise ValueError(f"{what}: {name} has shape {tuple(t.shape)} and strides {t.stride()}, expected those of "
+                             f"k_pages, {tuple(k_pages.shape)} and {k_pages.stride()}")
+        Hkv, ps, D = t.shape[-3:]
+        if (D > 1 and t.stride(-1) != 1) or (ps > 1 and t.stride(-2) != D) or (Hkv > 1 and t.stride(-3) != ps * D):
+            raise ValueError(f"{what}: {name}'s pages must be contiguous (strides {t.stride()})")
+    for name, t in (("k_pages", k_pages), ("v_pages", v_pages)):
+        if not t.is_cuda:
+            raise ValueError(f"{what}: {name} must be a CUDA tensor")
+        if t.device != device:
+            raise ValueError(f"{what}: {name} is on {t.device}, expected {device}")
+    P, Hkv, ps, D = k_pages.shape[-4:]
+    page_stride = k_pages.stride(-4) if P > 1 else Hkv * ps * D
+    nl, ls = (k_pages.shape[0], k_pages.stride(0)) if k_pages.dim() == 5 else (1, 0)
+    return nl, ls, P, Hkv, ps, D, page_stride
+
+
+def attention_decode_paged(q, k_pages, v_pages, page_table, seq_lens, scale=None, window=0, softcap=0.0, sink=None,
+                           stream=None):
+    """One new query per sequence against a paged cache: q [B,Hq,D], pools [num_pages,Hkv,page_size,D] (bf16
+    or f32; page_size a multiple of 16), page_table int32 [B,width], seq_lens int32 [B] (0 = padded
+    entry: o = 0, lse = -inf or the sink). Returns (o [B,Hq,D], lse [B,Hq]). Nothing synchronises; bad
+    lengths and pages are reported by forge_attn_check."""
+    import torch
+    what = "attention_decode_paged"
+    if q.dim() != 3 or page_table.dim() != 2:
+        raise ValueError(f"{what}: q must be [B, Hq, D] and page_table [B, width], got {tuple(q.shape)} and "
+                         f"{tuple(page_table.shape)}")
+    B, Hq, D = q.shape
+    _, _, P, Hkv, ps, Dk, stride = _check_pool(what, q.dtype, q.device, k_pages, v_pages)
+    if Dk != D:
+        raise ValueError(f"{what}: q has head dim {D}, the pools {Dk}")
+    _check_dense(what, q.device, q=(q, q.dtype, q.shape),
+                 page_table=(page_table, torch.int32, (B, page_table.shape[1])),
+                 seq_lens=(seq_lens, torch.int32, (B,)), sink=(sink, torch.float32, (Hq,)))
+    scale = 1.0 / math.sqrt(D) if scale is None else scale
+    dt = dtype_code(q.dtype)
+    with _scope(q.device, stream):
+        o = torch.empty_like(q)
+        lse = torch.empty((B, Hq), dtype=torch.float32, device=q.device)
+        nbytes = forge_attn_decode_paged_workspace_size(B, Hq, Hkv, D, dt)
+        ws = torch.empty(nbytes, dtype=torch.uint8, device=q.device)
+        s = forge_attn_decode_paged(q, k_pages, v_pages, o, lse, page_table, seq_lens, B, Hq, Hkv, D, P, ps,
+                                    page_table.shape[1], stride, scale, window, softcap, sink, dt, ws, nbytes)
+    if s != FORGE_OK:
+        raise ForgeError(s, "forge_attn_decode_paged")
+    return o, lse
+
+
+def paged_append(k, v, k_pages, v_pages, page_table, starts, cu_seqlens=None, stream=None):
+    """Write new tokens' keys and values into their sequences' pages: k, v [rows,Hkv,D] (their rows may lie
+    apart), page_table int32 [num_seqs,width], starts int32 [num_seqs] (tokens each sequence holds
+    already), cu_seqlens int32 [num_seqs + 1] as in attention_varlen_fwd, or None: one token per sequence.
+    Rows behind the last sequence are skipped. Bad places are skipped and reported by forge_attn_check."""
+    import torch
+    what = "paged_append"
+    if k.dim() != 3 or page_table.dim() != 2:
+        raise ValueError(f"{what}: k must be [rows, Hkv, D] and page_table [num_seqs, width], got {tuple(k.shape)} and "
+                         f"{tuple(page_table.shape)}")
+    rows, Hkv, D = k.shape
+    if v.shape != k.shape:
+        raise ValueError(f"{what}: v has shape {tuple(v.shape)}, expected {tuple(k.shape)}")
+    n, width = page_table.shape
+    if cu_seqlens is None and n != rows:
+        raise ValueError(f"{what}: {rows} rows for {n} sequences need cu_seqlens")
+    ks, vs = _check_rows(what, k.dtype, k.device, k=k, v=v)
+    _check_dense(what, k.device, page_table=(page_table, torch.int32, (n, width)), starts=(starts, torch.int32, (n,)),
+                 cu_seqlens=(cu_seqlens, torch.int32, (n + 1,)))
+    _, _, P, Hp, ps, Dp, stride = _check_pool(what, k.dtype, k.device, k_pages, v_pages)
+    if (Hp, Dp) != (Hkv, D):
+        raise ValueError(f"{what}: k has {Hkv} heads of {D}, the pools {Hp} of {Dp}")
+    with _scope(k.device, stream):
+        s = forge_attn_paged_append(k, v, k_pages, v_pages, page_table, starts, cu_seqlens, n, rows, Hkv, D, P, ps,
+                                    width, ks, vs, stride, dtype_code(k.dtype))
+    if s != FORGE_OK:
+        raise ForgeError(s, "forge_attn_paged_append")
+
+
+def _host_ints(what, name, x):
+    import torch
+    if isinstance(x, torch.Tensor):
+        if x.is_cuda:
+            raise ValueError(f"{what}: {name} must be on the host")
+        if x.dim() != 1 or x.dtype not in (torch.int32, torch.int64):
+            raise ValueError(f"{what}: {name} must be a list of page numbers")
+        if x.dtype == torch.int64 and x.numel() and (int(x.min()) < 0 or int(x.max()) >= 1 << 31):
+            raise ValueError(f"{what}: {name} has a page number out of range")
+        return x.to(torch.int32).contiguous()
+    return torch.tensor(list(x), dtype=torch.int32)
+
+
+def paged_copy(k_pages, v_pages, src, dst, stream=None):
+    """Copy page src[i] onto page dst[i], i = 0, 1, .. in that order, in both pools: [num_pages,Hkv,page_size,D],
+    or [layers,num_pages,..] for every layer at once. src, dst: page numbers on the host (lists or CPU
+    tensors), read before the call returns."""
+    what = "paged_copy"
+    src, dst = _host_ints(what, "src", src), _host_ints(what, "dst", dst)
+    if src.numel() != dst.numel():
+        raise ValueError(f"{what}: {src.numel()} sources for {dst.numel()} destinations")
+    nl, ls, P, Hkv, ps, D, stride = _check_pool(what, k_pages.dtype, k_pages.device, k_pages, v_pages, layers=True)
+    with _scope(k_pages.device, stream):
+        s = forge_attn_paged_copy(k_pages, v_pages, src, dst, src.numel(), nl, ls, P, Hkv, ps, D, stride,
+                                  dtype_code(k_pages.dtype))
+    if s != FORGE_OK:
+        raise ForgeError(s, "forge_attn_paged_copy")
+
+
+from .paged_cache import PagedCache  # noqa: E402  (imports no torch)

@@ -16,10 +16,14 @@
 #include "bwd_dkv.cuh"
 #include "bwd_tc.cuh"
 #include "decode.cuh"
+#include "decode_paged.cuh"
 #include "fwd2_tc.cuh"
 #include "fwd_tc.cuh"
+#include "paged.cuh"
 #include "simt.cuh"
 #include "sm100.cuh"
+#include "varlen.cuh"
+#include "varlen_f32.cuh"
 
 namespace forge {
 namespace {
@@ -99,6 +103,22 @@ bool make_map(CUtensorMap *map, const void *base, int D, int T, long long BH, in
     if (enc == nullptr) return false;
     cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)T, (cuuint64_t)BH};
     cuuint64_t strides[2] = {(cuuint64_t)D * 2, (cuuint64_t)D * 2 * (cuuint64_t)T};
+    cuuint32_t box[3] = {64, (cuuint32_t)box_rows, 1};
+    cuuint32_t estr[3] = {1, 1, 1};
+    CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(base), dims, strides, box, estr,
+                     CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS;
+}
+
+// A packed [rows][H][D] bf16 tensor whose rows are `stride` elements apart, viewed as
+// [H][rows][D] (same box and swizzle): a head's rows are `stride` apart, so a box holds
+// box_rows consecutive tokens of one head. Rows past `rows` read as zeros.
+bool make_map_rows(CUtensorMap *map, const void *base, int D, int rows, int H, size_t stride, int box_rows) {
+    EncodeTiledFn enc = encode_fn();
+    if (enc == nullptr) return false;
+    cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)rows, (cuuint64_t)H};
+    cuuint64_t strides[2] = {(cuuint64_t)stride * 2, (cuuint64_t)D * 2};
     cuuint32_t box[3] = {64, (cuuint32_t)box_rows, 1};
     cuuint32_t estr[3] = {1, 1, 1};
     CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(base), dims, strides, box, estr,
@@ -386,6 +406,310 @@ forge_status bwd_tc_dkv(const void *q, const void *k, const void *v, const float
     bwd_dq_tc_kernel<DK, DV><<<(unsigned)(pq.num_qt * B * Hq), CQ::THREADS, CQ::SMEM, st>>>(mq, mk64, mv64, mdo, pq);
     return launch_status();
 }
+
+// ------------------------------------------------------------ packed sequences
+// Arguments of the two packed entry points that the dispatchers share.
+struct VarArgs {
+    const void *q, *k, *v;
+    const int *cu;
+    int num_seqs, rows, Hq, Hkv, D;
+    size_t q_stride, k_stride, v_stride;
+    float scale;
+    int window;
+    float softcap;
+    const float *sink;
+    forge_dtype dtype;
+    cudaStream_t st;
+};
+
+// Rows of a tile of the schedule: pairs of 128-row query tiles for the two-tile
+// forward, single ones at head dim 256, 128 keys in the backward, 64 rows in f32.
+int var_unit(int D, forge_dtype dtype, bool backward) {
+    if (dtype == FORGE_DTYPE_F32) return kVfRows;
+    return !backward && D != 256 ? 256 : 128;
+}
+// Upper bounds that need no lengths: a sequence of n > 0 rows has at most
+// n / unit + 1 tiles and n + 127 padded rows.
+int var_max_items(int rows, int num_seqs, int unit) {
+    const long long n = (long long)rows / unit + num_seqs;
+    return (int)(n < rows ? n : rows);
+}
+int var_pad_rows(int rows, int num_seqs) {
+    const long long n = rows + 127ll * (num_seqs < rows ? num_seqs : rows);
+    return (int)((n + 127) / 128 * 128);
+}
+
+forge_status check_var_sizes(int num_seqs, int rows, int Hq, int Hkv, int D, forge_dtype dtype) {
+    forge_status s = check_sizes(1, Hq, Hkv, rows, D, dtype);
+    if (s != FORGE_OK) return s;
+    if (num_seqs < 1 || num_seqs > (1 << 20)) return FORGE_ERR_INVALID_ARG;
+    if (((long long)rows / 64 + num_seqs) * Hq * 2 > 0x7fffffffll) return FORGE_ERR_INVALID_ARG;  // grids
+    return FORGE_OK;
+}
+
+forge_status check_var_args(const VarArgs &a) {
+    forge_status s = check_var_sizes(a.num_seqs, a.rows, a.Hq, a.Hkv, a.D, a.dtype);
+    if (s != FORGE_OK) return s;
+    if ((s = check_scalars(a.scale, a.window, a.softcap)) != FORGE_OK) return s;
+    if (!aligned16(a.q) || !aligned16(a.k) || !aligned16(a.v) || !aligned4(a.cu)) return FORGE_ERR_INVALID_ARG;
+    if (a.sink != nullptr && !aligned4(a.sink)) return FORGE_ERR_INVALID_ARG;
+    // rows 16 bytes apart or a multiple, under the tensor maps' 2^40 bytes, and
+    // not overlapping
+    const size_t es = a.dtype == FORGE_DTYPE_BF16 ? 2 : 4, most = (size_t)1 << 36;
+    if (a.q_stride < (size_t)a.Hq * a.D || a.k_stride < (size_t)a.Hkv * a.D || a.v_stride < (size_t)a.Hkv * a.D ||
+        a.q_stride > most || a.k_stride > most || a.v_stride > most || a.q_stride * es % 16 != 0 ||
+        a.k_stride * es % 16 != 0 || a.v_stride * es % 16 != 0)
+        return FORGE_ERR_INVALID_ARG;
+    return FORGE_OK;
+}
+
+// Workspace: [ count ][ items ][ backward: Delta [Hq][rows] f32 ][ bf16: dq accumulator [Hq][pad_rows][D] f32 ]
+struct VarLayout {
+    size_t items, delta, acc, bytes;
+};
+VarLayout var_layout(int num_seqs, int rows, int Hq, int D, forge_dtype dtype, bool backward) {
+    VarLayout l;
+    l.items = 256;
+    l.delta = l.items + round256(sizeof(VarItem) * (size_t)var_max_items(rows, num_seqs, var_unit(D, dtype, backward)));
+    l.acc = l.delta + (backward ? delta_bytes(1, Hq, rows) : 0);
+    l.bytes = l.acc;
+    if (backward && dtype == FORGE_DTYPE_BF16)
+        l.bytes += round256(sizeof(float) * (size_t)Hq * var_pad_rows(rows, num_seqs) * D);
+    return l;
+}
+
+VarSched var_sched(const VarArgs &a, void *ws, bool backward) {
+    VarSched v;
+    v.items = reinterpret_cast<const VarItem *>(static_cast<char *>(ws) +
+                                                var_layout(a.num_seqs, a.rows, a.Hq, a.D, a.dtype, backward).items);
+    v.count = static_cast<const int *>(ws);
+    v.unit = var_unit(a.D, a.dtype, backward);
+    v.rows = a.rows;
+    v.pad_rows = var_pad_rows(a.rows, a.num_seqs);
+    return v;
+}
+
+// Launches varlen_plan; tail: up to three tensors of `heads` x D elements a row
+// whose rows behind the last sequence are cleared.
+forge_status run_plan(const VarArgs &a, const VarSched &v, bool backward, void *const (&tail)[3],
+                      const int (&tail_heads)[3], float *tail_lse, bool clear) {
+    VarPlanParams p;
+    p.cu = a.cu;
+    p.num_seqs = a.num_seqs;
+    p.rows = a.rows;
+    p.unit = v.unit;
+    p.window = a.window;
+    p.backward = backward;
+    p.items = const_cast<VarItem *>(v.items);
+    p.count = const_cast<int *>(v.count);
+    p.max_items = var_max_items(a.rows, a.num_seqs, v.unit);
+    for (int i = 0; i < 3; i++) {
+        p.tail[i] = clear ? static_cast<uint4 *>(tail[i]) : nullptr;
+        p.tail_chunks[i] = tail_heads[i] * a.D * (a.dtype == FORGE_DTYPE_BF16 ? 2 : 4) / 16;
+    }
+    p.tail_lse = clear ? tail_lse : nullptr;
+    p.heads = a.Hq;
+    return launch_pdl(varlen_plan, dim3(clear ? 33 : 1), dim3(kPlanThreads), 0, a.st, p);
+}
+
+FwdParams var_fwd_params(const VarArgs &a, const VarSched &v, void *o, float *lse) {
+    FwdParams p = {};
+    p.o = static_cast<__nv_bfloat16 *>(o);
+    p.lse = lse;
+    p.B = 1; p.Hq = a.Hq; p.Hkv = a.Hkv; p.window = a.window;
+    p.scale_log2 = a.scale * kLog2e;
+    p.softcap = a.softcap;
+    p.cap_in = a.softcap > 0.0f ? a.scale / a.softcap : 0.0f;
+    p.cap_out = a.softcap * kLog2e;
+    p.sink = a.sink;
+    p.var = v;
+    return p;
+}
+
+template <int D>
+forge_status var_fwd_tc(const VarArgs &a, const VarSched &v, void *o, float *lse) {
+    CUtensorMap mq, mk, mv, mo;
+    if (!make_map_rows(&mq, a.q, D, a.rows, a.Hq, a.q_stride, 128) ||
+        !make_map_rows(&mk, a.k, D, a.rows, a.Hkv, a.k_stride, 128) ||
+        !make_map_rows(&mv, a.v, D, a.rows, a.Hkv, a.v_stride, 128) ||
+        !make_map_rows(&mo, o, D, a.rows, a.Hq, (size_t)a.Hq * D, 128)) {
+        t_last_cuda_error = "cuTensorMapEncodeTiled failed";
+        return FORGE_ERR_CUDA;
+    }
+    const FwdParams p = var_fwd_params(a, v, o, lse);
+    const long long items = (long long)var_max_items(a.rows, a.num_seqs, v.unit) * a.Hq;
+    if constexpr (D == 256) {
+        using C = FwdTc<D>;
+        if (set_smem(fwd_tc_kernel<D, D, true>, C::SMEM) != FORGE_OK) return FORGE_ERR_CUDA;
+        return launch_pdl(fwd_tc_kernel<D, D, true>, dim3((unsigned)items), dim3(C::THREADS), C::SMEM, a.st, mq, mk, mv,
+                          p);
+    } else {
+        using C = Fwd2Tc<D>;
+        if (set_smem(fwd2_tc_kernel<D, true, true>, C::SMEM) != FORGE_OK ||
+            set_smem(fwd2_tc_kernel<D, false, true>, C::SMEM) != FORGE_OK)
+            return FORGE_ERR_CUDA;
+        // as the dense forward: persistent for short sequences
+        const bool persistent = a.rows / a.num_seqs <= 1024;
+        if (persistent)
+            return launch_pdl(fwd2_tc_kernel<D, true, true>, dim3((unsigned)(items < sm_count() ? items : sm_count())),
+                              dim3(C::THREADS), C::SMEM, a.st, mq, mk, mv, mo, p);
+        return launch_pdl(fwd2_tc_kernel<D, false, true>, dim3((unsigned)items), dim3(C::THREADS), C::SMEM, a.st, mq, mk,
+                          mv, mo, p);
+    }
+}
+
+VfParams var_f32_params(const VarArgs &a, const VarSched &v) {
+    VfParams p = {};
+    p.q = static_cast<const float *>(a.q);
+    p.k = static_cast<const float *>(a.k);
+    p.v = static_cast<const float *>(a.v);
+    p.q_row = (long long)a.q_stride;
+    p.k_row = (long long)a.k_stride;
+    p.v_row = (long long)a.v_stride;
+    p.Hq = a.Hq; p.Hkv = a.Hkv; p.window = a.window;
+    p.scale = a.scale;
+    p.softcap = a.softcap;
+    p.sink = a.sink;
+    p.var = v;
+    return p;
+}
+
+template <int D>
+forge_status var_fwd_f32(const VarArgs &a, const VarSched &v, void *o, float *lse) {
+    VfParams p = var_f32_params(a, v);
+    p.o = static_cast<float *>(o);
+    p.lse = lse;
+    if (set_smem(varlen_f32_fwd<D>, vf_fwd_smem<D>()) != FORGE_OK) return FORGE_ERR_CUDA;
+    const unsigned grid = (unsigned)var_max_items(a.rows, a.num_seqs, v.unit) * (unsigned)a.Hq;
+    return launch_pdl(varlen_f32_fwd<D>, dim3(grid), dim3(kVfThreads), vf_fwd_smem<D>(), a.st, p);
+}
+
+// The backward after the schedule: Delta (and the cleared accumulator), dsink, the
+// main kernels, dq.
+template <typename T_, int D>
+forge_status var_bwd(const VarArgs &a, const VarSched &v, const void *o, const float *lse, const void *dO, void *dq,
+                     void *dk, void *dv, float *dsink, float *delta, float *acc) {
+    const int items = var_max_items(a.rows, a.num_seqs, v.unit);
+    forge_status s = launch_pdl(varlen_preprocess<T_, D>, dim3((unsigned)items * (unsigned)a.Hq), dim3(256), 0, a.st,
+                                static_cast<const T_ *>(o), static_cast<const T_ *>(dO), delta, acc, a.Hq, v);
+    if (s != FORGE_OK) return s;
+    if (dsink != nullptr) {
+        s = launch_pdl(varlen_sink_grad, dim3((unsigned)a.Hq), dim3(512), 0, a.st, lse, static_cast<const float *>(delta),
+                       a.sink, dsink, a.cu, a.num_seqs, a.rows);
+        if (s != FORGE_OK) return s;
+    }
+    if constexpr (sizeof(T_) == 4) {
+        VfParams p = var_f32_params(a, v);
+        p.dO = static_cast<const float *>(dO);
+        p.lse = const_cast<float *>(lse);
+        p.delta = delta;
+        p.dq = static_cast<float *>(dq);
+        p.dk = static_cast<float *>(dk);
+        p.dv = static_cast<float *>(dv);
+        if (set_smem(varlen_f32_bwd_dq<D>, vf_bwd_dq_smem<D>()) != FORGE_OK ||
+            set_smem(varlen_f32_bwd_dkdv<D>, vf_bwd_dkdv_smem<D>()) != FORGE_OK)
+            return FORGE_ERR_CUDA;
+        s = launch_pdl(varlen_f32_bwd_dq<D>, dim3((unsigned)items * (unsigned)a.Hq), dim3(kVfThreads),
+                       vf_bwd_dq_smem<D>(), a.st, p);
+        if (s != FORGE_OK) return s;
+        return launch_pdl(varlen_f32_bwd_dkdv<D>, dim3((unsigned)items * (unsigned)a.Hkv), dim3(kVfThreads),
+                          vf_bwd_dkdv_smem<D>(), a.st, p);
+    } else {
+        using C = BwdTc<D>;
+        CUtensorMap mq, mk, mv, mdo, macc;
+        if (!make_map_rows(&mq, a.q, D, a.rows, a.Hq, a.q_stride, C::BM) ||
+            !make_map_rows(&mk, a.k, D, a.rows, a.Hkv, a.k_stride, 128) ||
+            !make_map_rows(&mv, a.v, D, a.rows, a.Hkv, a.v_stride, 128) ||
+            !make_map_rows(&mdo, dO, D, a.rows, a.Hq, (size_t)a.Hq * D, C::BM) ||
+            !make_map_acc(&macc, acc, D, v.pad_rows, a.Hq, C::BM)) {
+            t_last_cuda_error = "cuTensorMapEncodeTiled failed";
+            return FORGE_ERR_CUDA;
+        }
+        BwdParams p = {};
+        p.lse = lse;
+        p.delta = delta;
+        p.dq_acc = acc;
+        p.dk = static_cast<__nv_bfloat16 *>(dk);
+        p.dv = static_cast<__nv_bfloat16 *>(dv);
+        p.B = 1; p.Hq = a.Hq; p.Hkv = a.Hkv; p.window = a.window;
+        p.scale = a.scale;
+        p.scale_log2 = a.scale * kLog2e;
+        p.softcap = a.softcap;
+        p.cap_in = a.softcap > 0.0f ? a.scale / a.softcap : 0.0f;
+        p.cap_out = a.softcap * kLog2e;
+        p.var = v;
+        if (set_smem(bwd_tc_kernel<D, true>, C::SMEM) != FORGE_OK) return FORGE_ERR_CUDA;
+        const long long work = (long long)items * a.Hkv * C::NSPLIT;
+        s = launch_pdl(bwd_tc_kernel<D, true>, dim3((unsigned)(work < sm_count() ? work : sm_count())), dim3(C::THREADS),
+                       C::SMEM, a.st, mq, mk, mv, mdo, macc, p);
+        if (s != FORGE_OK) return s;
+        return launch_pdl(varlen_finalize_dq<D>, dim3((unsigned)items * (unsigned)a.Hq), dim3(256), 0, a.st,
+                          static_cast<const float *>(acc), static_cast<__nv_bfloat16 *>(dq), a.Hq, v);
+    }
+}
+
+// ---------------------------------------------------------------- paged cache
+// CTAs of the split pass: one wave of what fits an SM.
+template <typename T_, int D>
+int pd_workers() {
+    return PdCfg<T_, D>::PER_SM * sm_count();
+}
+int pd_workers_of(int D, forge_dtype dtype) {
+    const bool bf = dtype == FORGE_DTYPE_BF16;
+    switch (D) {
+        case 64: return bf ? pd_workers<__nv_bfloat16, 64>() : pd_workers<float, 64>();
+        case 128: return bf ? pd_workers<__nv_bfloat16, 128>() : pd_workers<float, 128>();
+        default: return bf ? pd_workers<__nv_bfloat16, 256>() : pd_workers<float, 256>();
+    }
+}
+
+template <typename T_, int D, class W>
+forge_status pd_launch(const PdParams &p, cudaStream_t st) {
+    using C = PdCfg<T_, D>;
+    if (set_smem(decode_paged_split<T_, D, W>, C::SMEM) != FORGE_OK) return FORGE_ERR_CUDA;
+    forge_status s = launch_pdl(decode_paged_split<T_, D, W>, dim3((unsigned)p.workers), dim3(kPdThreads), C::SMEM, st, p);
+    if (s != FORGE_OK) return s;
+    return launch_pdl(decode_paged_join<T_, D>, dim3((unsigned)(p.B * p.Hq)), dim3(128), 0, st, p);
+}
+
+template <int D>
+forge_status pd_run(const PdParams &p, forge_dtype dtype, cudaStream_t st) {
+    if (dtype == FORGE_DTYPE_BF16) return pd_launch<__nv_bfloat16, D, PdWarpBf<D>>(p, st);
+    const int G = p.Hq / p.Hkv;
+    if (G <= 4) return pd_launch<float, D, PdWarpF32<D, 4>>(p, st);
+    if (G <= 8) return pd_launch<float, D, PdWarpF32<D, 8>>(p, st);
+    return pd_launch<float, D, PdWarpF32<D, 16>>(p, st);
+}
+
+// A pool of pages: [num_pages][Hkv][page_size][D], pages page_stride elements apart.
+forge_status check_pool(const void *k, const void *v, int Hkv, int D, int num_pages, int page_size, size_t page_stride,
+                        forge_dtype dtype) {
+    if (Hkv < 1 || D < 1 || num_pages < 1 || page_size < 1) return FORGE_ERR_INVALID_ARG;
+    if (dtype != FORGE_DTYPE_F32 && dtype != FORGE_DTYPE_BF16) return FORGE_ERR_INVALID_ARG;
+    if (D != 64 && D != 128 && D != 256) return D % 2 ? FORGE_ERR_INVALID_ARG : FORGE_ERR_UNSUPPORTED;
+    if (page_size % 16 != 0) return FORGE_ERR_UNSUPPORTED;
+    if (Hkv > (1 << 16) || page_size > (1 << 20)) return FORGE_ERR_INVALID_ARG;
+    const size_t es = dtype == FORGE_DTYPE_BF16 ? 2 : 4;
+    if (page_stride < (size_t)Hkv * page_size * D || page_stride * es % 16 != 0 ||
+        page_stride > ((size_t)1 << 44) / (size_t)num_pages)
+        return FORGE_ERR_INVALID_ARG;
+    if (!aligned16(k) || !aligned16(v)) return FORGE_ERR_INVALID_ARG;
+    return FORGE_OK;
+}
+
+// A set of page numbers on the stack, for the pairs of one copy launch.
+struct PageSet {
+    static constexpr int N = 2048;  // slots; at most kCopyPairs used
+    int slot[N];
+    void clear() { memset(slot, 0xff, sizeof(slot)); }
+    int find(int page) const {
+        int i = (int)((unsigned)page * 2654435761u % N);
+        while (slot[i] >= 0 && slot[i] != page) i = (i + 1) % N;
+        return i;
+    }
+    bool has(int page) const { return slot[find(page)] == page; }
+    void add(int page) { slot[find(page)] = page; }
+};
 
 // out[i] = value for i < n
 __global__ void fill_f32_kernel(float *out, long n, float value) {
@@ -853,6 +1177,200 @@ forge_status forge_attn_decode(const void *q, const void *k_cache, const void *v
         FORGE_DISPATCH_D(D, return decode_run<float, kD>(q, k_cache, v_cache, o, p, st);)
     }
     return FORGE_ERR_UNSUPPORTED;
+}
+
+size_t forge_attn_varlen_fwd_workspace_size(int num_seqs, int rows, int Hq, int Hkv, int D, forge_dtype dtype) {
+    if (check_var_sizes(num_seqs, rows, Hq, Hkv, D, dtype) != FORGE_OK) return 0;
+    return var_layout(num_seqs, rows, Hq, D, dtype, false).bytes;
+}
+
+size_t forge_attn_varlen_bwd_workspace_size(int num_seqs, int rows, int Hq, int Hkv, int D, forge_dtype dtype) {
+    if (check_var_sizes(num_seqs, rows, Hq, Hkv, D, dtype) != FORGE_OK) return 0;
+    return var_layout(num_seqs, rows, Hq, D, dtype, true).bytes;
+}
+
+forge_status forge_attn_varlen_fwd(const void *q, const void *k, const void *v, void *o, float *lse,
+                                   const int *cu_seqlens, int num_seqs, int rows, int Hq, int Hkv, int D,
+                                   size_t q_stride, size_t k_stride, size_t v_stride, float scale, int window,
+                                   float softcap, const float *sink, int clear_tail, forge_dtype dtype,
+                                   void *workspace, size_t workspace_bytes, void *stream) {
+    VarArgs a = {q, k, v, cu_seqlens, num_seqs, rows, Hq, Hkv, D, q_stride, k_stride, v_stride, scale, window, softcap,
+                 sink, dtype, static_cast<cudaStream_t>(stream)};
+    forge_status s = check_var_args(a);
+    if (s != FORGE_OK) return s;
+    if (!aligned16(o) || !aligned16(lse)) return FORGE_ERR_INVALID_ARG;
+    if (workspace == nullptr || (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0 ||
+        workspace_bytes < forge_attn_varlen_fwd_workspace_size(num_seqs, rows, Hq, Hkv, D, dtype))
+        return FORGE_ERR_WORKSPACE;
+    a.window = effective_window(window, rows);
+    const VarSched sched = var_sched(a, workspace, false);
+    void *const tail[3] = {o, nullptr, nullptr};
+    const int heads[3] = {Hq, 0, 0};
+    if ((s = run_plan(a, sched, false, tail, heads, lse, clear_tail != 0)) != FORGE_OK) return s;
+    if (dtype == FORGE_DTYPE_BF16) {
+        FORGE_DISPATCH_D(D, return var_fwd_tc<kD>(a, sched, o, lse);)
+    } else {
+        FORGE_DISPATCH_D(D, return var_fwd_f32<kD>(a, sched, o, lse);)
+    }
+    return FORGE_ERR_UNSUPPORTED;
+}
+
+forge_status forge_attn_varlen_bwd(const void *q, const void *k, const void *v, const void *o, const float *lse,
+                                   const void *dO, void *dq, void *dk, void *dv, const int *cu_seqlens, int num_seqs,
+                                   int rows, int Hq, int Hkv, int D, size_t q_stride, size_t k_stride, size_t v_stride,
+                                   float scale, int window, float softcap, const float *sink, float *dsink,
+                                   int clear_tail, forge_dtype dtype, void *workspace, size_t workspace_bytes,
+                                   void *stream) {
+    VarArgs a = {q, k, v, cu_seqlens, num_seqs, rows, Hq, Hkv, D, q_stride, k_stride, v_stride, scale, window, softcap,
+                 sink, dtype, static_cast<cudaStream_t>(stream)};
+    forge_status s = check_var_args(a);
+    if (s != FORGE_OK) return s;
+    if (!aligned16(o) || !aligned16(lse) || !aligned16(dO) || !aligned16(dq) || !aligned16(dk) || !aligned16(dv))
+        return FORGE_ERR_INVALID_ARG;
+    if (dsink != nullptr && (!aligned4(dsink) || !aligned4(sink))) return FORGE_ERR_INVALID_ARG;
+    if (workspace == nullptr || (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0 ||
+        workspace_bytes < forge_attn_varlen_bwd_workspace_size(num_seqs, rows, Hq, Hkv, D, dtype))
+        return FORGE_ERR_WORKSPACE;
+    a.window = effective_window(window, rows);
+    const VarSched sched = var_sched(a, workspace, true);
+    const VarLayout l = var_layout(num_seqs, rows, Hq, D, dtype, true);
+    float *delta = reinterpret_cast<float *>(static_cast<char *>(workspace) + l.delta);
+    float *acc = dtype == FORGE_DTYPE_BF16 ? reinterpret_cast<float *>(static_cast<char *>(workspace) + l.acc) : nullptr;
+    void *const tail[3] = {dq, dk, dv};
+    const int heads[3] = {Hq, Hkv, Hkv};
+    if ((s = run_plan(a, sched, true, tail, heads, nullptr, clear_tail != 0)) != FORGE_OK) return s;
+    if (dtype == FORGE_DTYPE_BF16) {
+        FORGE_DISPATCH_D(D, return var_bwd<__nv_bfloat16, kD>(a, sched, o, lse, dO, dq, dk, dv, dsink, delta, acc);)
+    } else {
+        FORGE_DISPATCH_D(D, return var_bwd<float, kD>(a, sched, o, lse, dO, dq, dk, dv, dsink, delta, acc);)
+    }
+    return FORGE_ERR_UNSUPPORTED;
+}
+
+size_t forge_attn_decode_paged_workspace_size(int B, int Hq, int Hkv, int D, forge_dtype dtype) {
+    if (check_sizes(B, Hq, Hkv, 1, D, dtype) != FORGE_OK || Hq / Hkv > kPdMaxG) return 0;
+    return round256((size_t)2 * pd_workers_of(D, dtype) * (Hq / Hkv) * (size_t)(D + 2) * sizeof(float));
+}
+
+forge_status forge_attn_decode_paged(const void *q, const void *k_pages, const void *v_pages, void *o, float *lse,
+                                     const int *page_table, const int *seq_lens, int B, int Hq, int Hkv, int D,
+                                     int num_pages, int page_size, int table_width, size_t page_stride, float scale,
+                                     int window, float softcap, const float *sink, forge_dtype dtype, void *workspace,
+                                     size_t workspace_bytes, void *stream) {
+    forge_status s = check_sizes(B, Hq, Hkv, 1, D, dtype);
+    if (s != FORGE_OK) return s;
+    if ((s = check_scalars(scale, window, softcap)) != FORGE_OK) return s;
+    if ((s = check_pool(k_pages, v_pages, Hkv, D, num_pages, page_size, page_stride, dtype)) != FORGE_OK) return s;
+    if (Hq / Hkv > kPdMaxG) return FORGE_ERR_UNSUPPORTED;
+    if (table_width < 1 || (long long)table_width * page_size > (1 << 30)) return FORGE_ERR_INVALID_ARG;
+    if (!aligned16(q) || !aligned16(o) || !aligned4(page_table) || !aligned4(seq_lens) || (lse && !aligned4(lse)) ||
+        (sink && !aligned4(sink)))
+        return FORGE_ERR_INVALID_ARG;
+    if (!aligned16(workspace) || workspace_bytes < forge_attn_decode_paged_workspace_size(B, Hq, Hkv, D, dtype))
+        return FORGE_ERR_WORKSPACE;
+    PdParams p;
+    p.q = q;
+    p.k = k_pages;
+    p.v = v_pages;
+    p.o = o;
+    p.lse = lse;
+    p.table = page_table;
+    p.seq_lens = seq_lens;
+    p.sink = sink;
+    p.part = static_cast<float *>(workspace);
+    p.page_stride = (long long)page_stride;
+    p.B = B; p.Hq = Hq; p.Hkv = Hkv; p.width = table_width; p.page = page_size; p.num_pages = num_pages;
+    p.window = effective_window(window, table_width * page_size);
+    p.qscale = softcap > 0.0f ? scale / softcap : scale * kLog2e;
+    p.cap_out = softcap > 0.0f ? softcap * kLog2e : 0.0f;
+    // no more CTAs than units of 32 keys that the tables could hold
+    const long long most = (long long)B * Hkv * ((long long)table_width * page_size / 32 + 1);
+    const int workers = pd_workers_of(D, dtype);
+    p.workers = most < workers ? (int)most : workers;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    FORGE_DISPATCH_D(D, return pd_run<kD>(p, dtype, st);)
+    return FORGE_ERR_UNSUPPORTED;
+}
+
+forge_status forge_attn_paged_append(const void *k, const void *v, void *k_pages, void *v_pages, const int *page_table,
+                                     const int *starts, const int *cu_seqlens, int num_seqs, int rows, int Hkv, int D,
+                                     int num_pages, int page_size, int table_width, size_t k_stride, size_t v_stride,
+                                     size_t page_stride, forge_dtype dtype, void *stream) {
+    forge_status s = check_pool(k_pages, v_pages, Hkv, D, num_pages, page_size, page_stride, dtype);
+    if (s != FORGE_OK) return s;
+    if (num_seqs < 1 || rows < 1 || rows > (1 << 30) || table_width < 1) return FORGE_ERR_INVALID_ARG;
+    if (cu_seqlens == nullptr && rows != num_seqs) return FORGE_ERR_INVALID_ARG;
+    if (!aligned16(k) || !aligned16(v) || !aligned4(page_table) || !aligned4(starts) ||
+        (cu_seqlens && !aligned4(cu_seqlens)))
+        return FORGE_ERR_INVALID_ARG;
+    const size_t es = dtype == FORGE_DTYPE_BF16 ? 2 : 4, most = (size_t)1 << 36;
+    if (k_stride < (size_t)Hkv * D || v_stride < (size_t)Hkv * D || k_stride > most || v_stride > most ||
+        k_stride * es % 16 != 0 || v_stride * es % 16 != 0)
+        return FORGE_ERR_INVALID_ARG;
+    AppendParams p;
+    p.src[0] = static_cast<const uint8_t *>(k);
+    p.src[1] = static_cast<const uint8_t *>(v);
+    p.dst[0] = static_cast<uint8_t *>(k_pages);
+    p.dst[1] = static_cast<uint8_t *>(v_pages);
+    p.src_stride[0] = (long long)(k_stride * es);
+    p.src_stride[1] = (long long)(v_stride * es);
+    p.page_stride = (long long)(page_stride * es);
+    p.table = page_table;
+    p.starts = starts;
+    p.cu = cu_seqlens;
+    p.num_seqs = num_seqs; p.rows = rows; p.width = table_width; p.page = page_size; p.num_pages = num_pages;
+    p.Hkv = Hkv;
+    p.chunks = (int)(D * es / 16);
+    // few tokens: one a block, so that they spread over the SMs
+    const int per_sm = rows / (4 * sm_count());
+    p.tokens = per_sm < 1 ? 1 : per_sm > kAppendTokens ? kAppendTokens : per_sm;
+    return launch_pdl(paged_append, dim3((unsigned)((rows + p.tokens - 1) / p.tokens)), dim3(kAppendThreads), 0,
+                      static_cast<cudaStream_t>(stream), p);
+}
+
+forge_status forge_attn_paged_copy(void *k_pages, void *v_pages, const int *src, const int *dst, int n, int num_layers,
+                                   size_t layer_stride, int num_pages, int Hkv, int page_size, int D,
+                                   size_t page_stride, forge_dtype dtype, void *stream) {
+    forge_status s = check_pool(k_pages, v_pages, Hkv, D, num_pages, page_size, page_stride, dtype);
+    if (s != FORGE_OK) return s;
+    const size_t es = dtype == FORGE_DTYPE_BF16 ? 2 : 4;
+    if (n < 0 || num_layers < 1 || num_layers > 65535 || layer_stride * es % 16 != 0 ||
+        layer_stride > ((size_t)1 << 44) / (size_t)num_layers)
+        return FORGE_ERR_INVALID_ARG;
+    if (n > 0 && (src == nullptr || dst == nullptr)) return FORGE_ERR_INVALID_ARG;
+    for (int i = 0; i < n; i++)
+        if (src[i] < 0 || src[i] >= num_pages || dst[i] < 0 || dst[i] >= num_pages) return FORGE_ERR_INVALID_ARG;
+    CopyParams p;
+    p.pool[0] = static_cast<uint8_t *>(k_pages);
+    p.pool[1] = static_cast<uint8_t *>(v_pages);
+    p.page_stride = (long long)(page_stride * es);
+    p.layer_stride = (long long)(layer_stride * es);
+    p.page_bytes = (long long)((size_t)Hkv * page_size * D * es);
+    const long long per = (long long)kCopyThreads * kCopyUnroll * 16;
+    const long long splits = (p.page_bytes + per - 1) / per;
+    p.splits = (int)(splits < 1024 ? splits : 1024);
+    PageSet read, written;
+    int at = 0;
+    while (at < n) {
+        // the longest run whose copies do not depend on one another: the next run
+        // starts at a page that this one writes, or that it would have to read first
+        read.clear();
+        written.clear();
+        p.pairs = 0;
+        for (; at < n && p.pairs < kCopyPairs; at++) {
+            if (src[at] == dst[at]) continue;
+            if (written.has(src[at]) || written.has(dst[at]) || read.has(dst[at])) break;
+            read.add(src[at]);
+            written.add(dst[at]);
+            p.src[p.pairs] = src[at];
+            p.dst[p.pairs++] = dst[at];
+        }
+        if (p.pairs == 0) continue;  // only pages copied onto themselves were left
+        s = launch_pdl(paged_copy, dim3((unsigned)(p.pairs * p.splits), (unsigned)num_layers, 2), dim3(kCopyThreads), 0,
+                       static_cast<cudaStream_t>(stream), p);
+        if (s != FORGE_OK) return s;
+    }
+    return FORGE_OK;
 }
 
 forge_status forge_attn_check(void *stream) {

@@ -49,6 +49,7 @@
 #pragma once
 
 #include "sm100.cuh"
+#include "varlen_item.cuh"
 
 namespace forge {
 
@@ -147,7 +148,12 @@ struct BwdTc {
                                                           // warps unless DV_BY_DRAIN)
     static constexpr int B_QSH_FULL = B_EPI_DONE + 1;    // the Q half for dK has landed (QSHADOW)
     static constexpr int B_QSH_EMPTY = B_QSH_FULL + 1;   // ... and dK has read it
-    static constexpr int NBAR = B_QSH_EMPTY + 1;
+    // packed sequences: the same stages with the rows past the sequence's end set
+    // to zero (two warps)
+    static constexpr int B_KV_FIX = B_QSH_EMPTY + 1;     // [NKV]
+    static constexpr int B_Q_FIX = B_KV_FIX + NKV;       // [QST]
+    static constexpr int B_QSH_FIX = B_Q_FIX + QST;
+    static constexpr int NBAR = B_QSH_FIX + 1;
     static_assert(NBAR * 8 <= (int)OFF_TMEM_SLOT, "control block");
 };
 
@@ -156,6 +162,7 @@ struct BwdTc {
 // heads of the group.
 struct BwdItem {
     int h, bkv, b, hkv, k0, m_lo, nm, steps;
+    int row0, T, pad0;  // the sequence's first row, its length, and its first padded row
 };
 
 struct BwdParams {
@@ -171,6 +178,9 @@ struct BwdParams {
     float cap_out;         // softcap * log2(e)
     int q_desc;            // step order: 0 = head by head, query tiles ascending;
                            // 1 = query tiles descending from T - 1, every head per tile
+    // packed sequences (the VAR kernels): dk, dv are [rows][Hkv][D], lse and delta
+    // [Hq][rows], dq_acc [Hq][pad_rows][D]; B = 1 and T, Tpad, num_kt unused
+    VarSched var;
 };
 
 // An item's steps in order: (query head g of the group, query tile m). Head by head,
@@ -366,11 +376,20 @@ __device__ __forceinline__ void bwd_mma_dq(uint32_t tmem, uint32_t sdS, uint32_t
     }
 }
 
-template <class C, class P>
+template <class C, bool VAR = false, class P>
 __device__ __forceinline__ BwdItem bwd_item(int w, const P &p) {
     BwdItem it;
     const int per_n = p.B * p.Hkv * C::NSPLIT;
-    const int n = w / per_n;
+    int n = w / per_n;
+    it.row0 = it.pad0 = 0;
+    it.T = p.T;
+    if constexpr (VAR) {
+        const VarItem t = var_item(p.var, n);
+        n = t.tile;
+        it.row0 = t.row0;
+        it.T = t.len;
+        it.pad0 = t.pad0;
+    }
     const int rest = w % per_n;
     it.h = rest % C::NSPLIT;
     it.bkv = rest / C::NSPLIT;  // b * Hkv + hkv
@@ -378,7 +397,7 @@ __device__ __forceinline__ BwdItem bwd_item(int w, const P &p) {
     it.hkv = it.bkv % p.Hkv;
     it.k0 = n * C::BN;
     it.m_lo = it.k0 / C::BM;
-    const int q_last = p.window > 0 ? min(p.T - 1, it.k0 + C::BN - 1 + p.window - 1) : p.T - 1;
+    const int q_last = p.window > 0 ? min(it.T - 1, it.k0 + C::BN - 1 + p.window - 1) : it.T - 1;
     it.nm = q_last / C::BM - it.m_lo + 1;
     it.steps = (p.Hq / p.Hkv) * it.nm;
     return it;
@@ -387,7 +406,12 @@ __device__ __forceinline__ BwdItem bwd_item(int w, const P &p) {
 // Persistent: gridDim.x CTAs walk the work items in the snake order above. Every
 // barrier's phase counts steps (or items) over the CTA's whole run, so the
 // pipeline carries on from one item into the next; TMEM is allocated once.
-template <int D>
+// VAR: packed sequences. Items come from the schedule and the tensor maps cover
+// [heads][rows][D] views of the packed tensors. The last tile of a sequence brings
+// rows of the next one along: warps 14 and 15 set them to zero in K, V, Q and dO
+// before the MMA warp may read the stage (it waits on their barriers), which
+// leaves the rest of the kernel the tiles it would have at a tensor's end.
+template <int D, bool VAR = false>
 __global__ void __launch_bounds__(512, 1)
     bwd_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                   const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmdO,
@@ -413,9 +437,8 @@ __global__ void __launch_bounds__(512, 1)
     }
 
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-    const int nitems = p.num_kt * p.B * p.Hkv * C::NSPLIT;
+    int nitems = p.num_kt * p.B * p.Hkv * C::NSPLIT;
     const int G = p.Hq / p.Hkv;
-    const int W = p.window;
     auto item_of = [&](int pass) -> int { return snake_item(pass, (int)blockIdx.x, (int)gridDim.x); };
 
     if (threadIdx.x == 0) {
@@ -438,6 +461,11 @@ __global__ void __launch_bounds__(512, 1)
         mbar_init(bar(C::B_EPI_DONE), C::DV_BY_DRAIN ? 4 : 12);
         mbar_init(bar(C::B_QSH_FULL), 1);
         mbar_init(bar(C::B_QSH_EMPTY), 1);
+        if constexpr (VAR) {
+            for (int s = 0; s < C::NKV; s++) mbar_init(bar(C::B_KV_FIX + s), 2);
+            for (int s = 0; s < C::QST; s++) mbar_init(bar(C::B_Q_FIX + s), 2);
+            mbar_init(bar(C::B_QSH_FIX), 1);
+        }
         *abort_flag = 0;
         fence_mbar_init();
     }
@@ -457,6 +485,7 @@ __global__ void __launch_bounds__(512, 1)
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
     griddep_wait();  // the previous kernel's outputs (lse, Delta, the zeroed accumulator) are visible
+    if constexpr (VAR) nitems = var_count(p.var) * p.Hkv * C::NSPLIT;
 
     if (warp >= C::W_LOAD) {
         setmaxnreg_dec<C::REG_CTRL>();
@@ -468,7 +497,7 @@ __global__ void __launch_bounds__(512, 1)
             for (int pass = 0; ok; pass++) {
                 const int w = item_of(pass);
                 if (w >= nitems) break;
-                const BwdItem I = bwd_item<C>(w, p);
+                const BwdItem I = bwd_item<C, VAR>(w, p);
                 // this CTA's last item: the next kernel may start launching
                 if (lane == 0 && item_of(pass + 1) >= nitems) griddep_launch_dependents();
                 // K, V of the item into buffer pass % NKV once the item that used it
@@ -482,8 +511,8 @@ __global__ void __launch_bounds__(512, 1)
                     const uint32_t sK = sK0 + (uint32_t)kvs * C::KVB, sV = sK + C::TK;
                     mbar_arrive_expect_tx(bar(C::B_KV_FULL + kvs), 2 * C::TK);
                     for (int c = 0; c < C::NCB; c++) {
-                        tma_load_3d(sK + c * C::CBK, &tmK, bar(C::B_KV_FULL + kvs), c * 64, I.k0, I.bkv);
-                        tma_load_3d(sV + c * C::CBK, &tmV, bar(C::B_KV_FULL + kvs), c * 64, I.k0, I.bkv);
+                        tma_load_3d(sK + c * C::CBK, &tmK, bar(C::B_KV_FULL + kvs), c * 64, I.row0 + I.k0, I.bkv);
+                        tma_load_3d(sV + c * C::CBK, &tmV, bar(C::B_KV_FULL + kvs), c * 64, I.row0 + I.k0, I.bkv);
                     }
                 }
                 kv_issued++;
@@ -499,9 +528,9 @@ __global__ void __launch_bounds__(512, 1)
 #pragma unroll
                     for (int r = 0; r < C::BM / 32; r++) {
                         const int q = m * C::BM + lane + 32 * r;
-                        const size_t idx = (size_t)bhq * p.T + (size_t)min(q, p.T - 1);
-                        lv[r] = q < p.T ? p.lse[idx] * kLog2e : INFINITY;
-                        dv[r] = q < p.T ? p.delta[idx] * p.scale : 0.0f;
+                        const size_t idx = (size_t)bhq * (VAR ? p.var.rows : p.T) + (size_t)(I.row0 + min(q, I.T - 1));
+                        lv[r] = q < I.T ? p.lse[idx] * kLog2e : INFINITY;
+                        dv[r] = q < I.T ? p.delta[idx] * p.scale : 0.0f;
                     }
                     if (!mbar_wait_warp(bar(C::B_Q_EMPTY + st), ph ^ 1u, abort_flag)) {
                         ok = false;
@@ -511,9 +540,9 @@ __global__ void __launch_bounds__(512, 1)
                         mbar_arrive_expect_tx(bar(C::B_Q_FULL + st), 2 * C::TQ);
                         for (int c = 0; c < C::NCB; c++) {
                             tma_load_3d(sQ0 + st * C::TQ + c * C::CBQ, &tmQ, bar(C::B_Q_FULL + st), c * 64,
-                                        m * C::BM, bhq);
+                                        I.row0 + m * C::BM, bhq);
                             tma_load_3d(sdO0 + st * C::TQ + c * C::CBQ, &tmdO, bar(C::B_Q_FULL + st), c * 64,
-                                        m * C::BM, bhq);
+                                        I.row0 + m * C::BM, bhq);
                         }
                     }
                     issued++;
@@ -534,7 +563,7 @@ __global__ void __launch_bounds__(512, 1)
                             mbar_arrive_expect_tx(bar(C::B_QSH_FULL), C::TQSH);
                             for (int c = 0; c < C::DH / 64; c++)
                                 tma_load_3d(sQsh + c * C::CBQ, &tmQ, bar(C::B_QSH_FULL), (I.h * (C::DH / 64) + c) * 64,
-                                            m * C::BM, bhq);
+                                            I.row0 + m * C::BM, bhq);
                         }
                         qsh_issued++;
                     }
@@ -557,7 +586,8 @@ __global__ void __launch_bounds__(512, 1)
             // ------------------------------------------------------ MMA issuer
             // S^T(j) = K Q(j)^T once stage j % QST holds Q(j) (j counts steps over all items)
             auto wait_q = [&](int j) -> bool {
-                if (!mbar_wait(bar(C::B_Q_FULL + j % C::QST), (uint32_t)((j / C::QST) & 1), abort_flag)) return false;
+                if (!mbar_wait(bar((VAR ? C::B_Q_FIX : C::B_Q_FULL) + j % C::QST), (uint32_t)((j / C::QST) & 1), abort_flag))
+                    return false;
                 tc_fence_after();
                 return true;
             };
@@ -567,12 +597,14 @@ __global__ void __launch_bounds__(512, 1)
             for (; ok; pass++) {
                 const int w = item_of(pass);
                 if (w >= nitems) break;
-                const BwdItem I = bwd_item<C>(w, p);
+                const BwdItem I = bwd_item<C, VAR>(w, p);
                 const int kvs = pass % C::NKV;
                 const uint32_t sK = sK0 + (uint32_t)kvs * C::KVB, sV = sK + C::TK;
                 const uint32_t h_q = (uint32_t)I.h * (C::DH / 64) * C::CBQ;  // column-block offset of half h
                 const uint32_t h_k = (uint32_t)I.h * (C::DH / 64) * C::CBK;
-                if (!(ok = mbar_wait(bar(C::B_KV_FULL + kvs), (uint32_t)((pass / C::NKV) & 1), abort_flag))) break;
+                if (!(ok = mbar_wait(bar((VAR ? C::B_KV_FIX : C::B_KV_FULL) + kvs), (uint32_t)((pass / C::NKV) & 1),
+                                     abort_flag)))
+                    break;
                 tc_fence_after();
                 if (!(ok = wait_q(gs))) break;
                 bwd_mma_kq<C>(tmem + C::COL_S, sK, sQ0 + (gs % C::QST) * C::TQ);
@@ -618,7 +650,8 @@ __global__ void __launch_bounds__(512, 1)
                     if (!(ok = mbar_wait(bar(C::B_DS_FULL), (uint32_t)(gs & 1), abort_flag))) break;
                     tc_fence_after();
                     if constexpr (C::QSHADOW) {
-                        if (!(ok = mbar_wait(bar(C::B_QSH_FULL), (uint32_t)(gs & 1), abort_flag))) break;
+                        if (!(ok = mbar_wait(bar(VAR ? C::B_QSH_FIX : C::B_QSH_FULL), (uint32_t)(gs & 1), abort_flag)))
+                            break;
                         tc_fence_after();
                         bwd_mma_dk<C>(tmem, sdS, sQsh, i == 0);
                         tc_commit(bar(C::B_QSH_EMPTY));
@@ -660,6 +693,48 @@ __global__ void __launch_bounds__(512, 1)
                 tc_commit(bar(C::B_KDONE));
                 mbar_wait_drain(bar(C::B_KDONE), (uint32_t)(pass & 1), 200000000ull);
             }
+        } else if (VAR && warp > C::W_MMA) {
+            // -------------------- packed sequences: zero the rows past the end
+            // (warp 14: K, Q and the Q shadow; warp 15: V and dO). They arrive for
+            // every stage, zeroed or not, so phases count stages as elsewhere.
+            const bool second = warp != C::W_MMA + 1;
+            bool ok = true;
+            int gs = 0;
+            for (int pass = 0; ok; pass++) {
+                const int w = item_of(pass);
+                if (w >= nitems) break;
+                const BwdItem I = bwd_item<C, VAR>(w, p);
+                const int kvs = pass % C::NKV;
+                if (!(ok = mbar_wait_warp(bar(C::B_KV_FULL + kvs), (uint32_t)((pass / C::NKV) & 1), abort_flag))) break;
+                if (I.T - I.k0 < C::BN) {
+                    zero_tail_rows<C::BN, C::NCB, 32>(sK0 + (uint32_t)kvs * C::KVB + (second ? C::TK : 0u), C::CBK,
+                                                      I.T - I.k0, lane);
+                    fence_proxy_async_smem();
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar(C::B_KV_FIX + kvs));
+                BwdStep sp(I, p.q_desc);
+                for (int i = 0; i < I.steps; i++, gs++, sp.next(I, G, p.q_desc)) {
+                    const int st = gs % C::QST;
+                    const int end = I.T - sp.m * C::BM;
+                    if (!(ok = mbar_wait_warp(bar(C::B_Q_FULL + st), (uint32_t)((gs / C::QST) & 1), abort_flag))) break;
+                    if (end < C::BM) {
+                        zero_tail_rows<C::BM, C::NCB, 32>((second ? sdO0 : sQ0) + st * C::TQ, C::CBQ, end, lane);
+                        fence_proxy_async_smem();
+                    }
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(bar(C::B_Q_FIX + st));
+                    if (C::QSHADOW && !second) {
+                        if (!(ok = mbar_wait_warp(bar(C::B_QSH_FULL), (uint32_t)(gs & 1), abort_flag))) break;
+                        if (end < C::BM) {
+                            zero_tail_rows<C::BM, C::DH / 64, 32>(sQsh, C::CBQ, end, lane);
+                            fence_proxy_async_smem();
+                        }
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(bar(C::B_QSH_FIX));
+                    }
+                }
+            }
         }
     } else if (warp < C::W_DRAIN) {
         setmaxnreg_inc<C::REG_COMPUTE>();
@@ -673,8 +748,9 @@ __global__ void __launch_bounds__(512, 1)
         for (int pass = 0; ok; pass++) {
             const int w = item_of(pass);
             if (w >= nitems) break;
-            const BwdItem I = bwd_item<C>(w, p);
+            const BwdItem I = bwd_item<C, VAR>(w, p);
             const int kj = I.k0 + kr;
+            const int W = VAR && p.window >= I.T ? 0 : p.window;  // a window that hides nothing is none
             BwdStep sp(I, p.q_desc);
             for (int i = 0; i < I.steps; i++, gs++, sp.next(I, G, p.q_desc)) {
                 const int st = gs % C::QST;
@@ -731,8 +807,10 @@ __global__ void __launch_bounds__(512, 1)
                 // epilogue of the item: dV rows, this warp's half of the columns
                 if (!(ok = mbar_wait_warp(bar(C::B_KDONE), (uint32_t)(pass & 1), abort_flag))) break;
                 tc_fence_after();
-                __nv_bfloat16 *row = p.dv + ((size_t)I.bkv * p.T + (size_t)min(kj, p.T - 1)) * D + I.h * C::DH;
-                bwd_row_out(tmem + lane_base + C::COL_DV, row, hc * (C::DH / 2), (hc + 1) * (C::DH / 2), kj < p.T);
+                const size_t kr_c = (size_t)min(kj, I.T - 1);
+                __nv_bfloat16 *row =
+                    p.dv + (VAR ? (I.row0 + kr_c) * p.Hkv + I.hkv : (size_t)I.bkv * p.T + kr_c) * D + I.h * C::DH;
+                bwd_row_out(tmem + lane_base + C::COL_DV, row, hc * (C::DH / 2), (hc + 1) * (C::DH / 2), kj < I.T);
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(bar(C::B_EPI_DONE));
@@ -748,7 +826,7 @@ __global__ void __launch_bounds__(512, 1)
         for (int pass = 0; ok; pass++) {
             const int w = item_of(pass);
             if (w >= nitems) break;
-            const BwdItem I = bwd_item<C>(w, p);
+            const BwdItem I = bwd_item<C, VAR>(w, p);
             BwdStep sp(I, p.q_desc);
             for (int i = 0; i < I.steps; i++, gs++, sp.next(I, G, p.q_desc)) {
                 const int g = sp.g, m = sp.m;
@@ -792,7 +870,7 @@ __global__ void __launch_bounds__(512, 1)
 #pragma unroll
                         for (int cb = 0; cb < C::DH / 32; cb++)
                             tma_reduce_add_3d(&tmAcc, stg + (uint32_t)cb * (uint32_t)(C::BM * 128), I.h * C::DH + 32 * cb,
-                                              m * C::BM, bhq);
+                                              I.pad0 + m * C::BM, bhq);
                         bulk_commit();
                     }
                 } else {
@@ -802,7 +880,9 @@ __global__ void __launch_bounds__(512, 1)
 
                     // evict-last: the accumulator lines are reduced into again by the
                     // other key tiles' CTAs soon, and read by the finalize
-                    float *base = p.dq_acc + ((size_t)bhq * p.Tpad + (size_t)m * C::BM) * D + I.h * C::DH + t;
+                    float *base = p.dq_acc +
+                                  ((size_t)bhq * (VAR ? p.var.pad_rows : p.Tpad) + (size_t)(I.pad0 + m * C::BM)) * D +
+                                  I.h * C::DH + t;
                     const uint64_t keep = policy_evict_last();
 #pragma unroll
                     for (int j = 0; j < NQC; j++) {
@@ -816,9 +896,10 @@ __global__ void __launch_bounds__(512, 1)
             if (!(ok = mbar_wait_warp(bar(C::B_KDONE), (uint32_t)(pass & 1), abort_flag))) break;
             tc_fence_after();
             const int kj = I.k0 + t;
-            const size_t roff = ((size_t)I.bkv * p.T + (size_t)min(kj, p.T - 1)) * D + I.h * C::DH;
-            bwd_row_out(tmem + lane_base + C::COL_DK, p.dk + roff, 0, C::DH, kj < p.T);
-            if constexpr (C::DV_BY_DRAIN) bwd_row_out(tmem + lane_base + C::COL_DV, p.dv + roff, 0, C::DH, kj < p.T);
+            const size_t kr_c = (size_t)min(kj, I.T - 1);
+            const size_t roff = (VAR ? (I.row0 + kr_c) * p.Hkv + I.hkv : (size_t)I.bkv * p.T + kr_c) * D + I.h * C::DH;
+            bwd_row_out(tmem + lane_base + C::COL_DK, p.dk + roff, 0, C::DH, kj < I.T);
+            if constexpr (C::DV_BY_DRAIN) bwd_row_out(tmem + lane_base + C::COL_DV, p.dv + roff, 0, C::DH, kj < I.T);
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(bar(C::B_EPI_DONE));

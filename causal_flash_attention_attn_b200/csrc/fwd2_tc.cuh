@@ -80,22 +80,36 @@ struct Fwd2Tc {
 // (pairs heaviest first); tile A sees KV tiles [loA, tA], tile B [loB, tB].
 struct Fwd2Item {
     int bh, hq, bkv, tA, tB, qA0, qB0, loA, loB, lo, hi;
+    int row0, T;  // the sequence's first row in the tensors and its length
     bool hasB;
 };
 
-template <class C>
+// VAR: the pair comes from the schedule of a packed batch, heads innermost.
+template <class C, bool VAR>
 __device__ __forceinline__ Fwd2Item fwd2_item(int w, const FwdParams &p) {
     Fwd2Item I;
-    const int nbh = p.B * p.Hq;
-    const int npairs = (p.num_qt + 1) / 2;
-    const int pr = npairs - 1 - w / nbh;
-    I.bh = w % nbh;
+    int pr, num_qt = p.num_qt;
+    if constexpr (VAR) {
+        const VarItem it = var_item(p.var, w / p.Hq);
+        pr = it.tile;
+        I.bh = w % p.Hq;
+        I.row0 = it.row0;
+        I.T = it.len;
+        num_qt = (it.len + C::BM - 1) / C::BM;
+    } else {
+        const int nbh = p.B * p.Hq;
+        const int npairs = (p.num_qt + 1) / 2;
+        pr = npairs - 1 - w / nbh;
+        I.bh = w % nbh;
+        I.row0 = 0;
+        I.T = p.T;
+    }
     const int b = I.bh / p.Hq;
     I.hq = I.bh % p.Hq;
     I.bkv = b * p.Hkv + I.hq / (p.Hq / p.Hkv);
     I.tA = 2 * pr;
     I.tB = 2 * pr + 1;
-    I.hasB = I.tB < p.num_qt;
+    I.hasB = I.tB < num_qt;
     I.qA0 = I.tA * C::BM;
     I.qB0 = I.tB * C::BM;
     I.loA = p.window > 0 ? max(0, I.qA0 - p.window + 1) / C::BN : 0;
@@ -152,7 +166,12 @@ __device__ __forceinline__ void exp_chunk32(const uint32_t (&s)[32], uint64_t sl
 // KV tiles (or items) over the CTA's whole run and TMEM is allocated once.
 // PERSIST = false: one CTA per item (grid = number of items), compiled without
 // the work-item loop.
-template <int D, bool PERSIST>
+// VAR: packed sequences. Items come from the schedule, the tensor maps cover
+// [heads][rows][D] views of the packed tensors, and the rows of the next sequence
+// that a sequence's last tiles bring along are kept out: K's by the causal mask,
+// V's by zeroing them in shared memory (the softmax warpgroup of the last tile,
+// before it hands its P to the MMA warp), O's by storing that tile row by row.
+template <int D, bool PERSIST, bool VAR = false>
 __global__ void __launch_bounds__(384, 1)
     fwd2_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                    const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmO,
@@ -168,8 +187,7 @@ __global__ void __launch_bounds__(384, 1)
     auto bar = [&](int i) -> uint32_t { return sbase + 8u * (uint32_t)i; };
 
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-    const int W = p.window;
-    const int nitems = ((p.num_qt + 1) / 2) * p.B * p.Hq;
+    int nitems = ((p.num_qt + 1) / 2) * p.B * p.Hq;
     auto item_of = [&](int pass) -> int {
         return PERSIST ? snake_item(pass, (int)blockIdx.x, (int)gridDim.x) : (pass == 0 ? (int)blockIdx.x : nitems);
     };
@@ -206,7 +224,8 @@ __global__ void __launch_bounds__(384, 1)
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
-    griddep_wait();  // the previous kernel's writes (q, k, v, max_logit) are visible
+    griddep_wait();  // the previous kernel's writes (q, k, v, max_logit, the schedule) are visible
+    if constexpr (VAR) nitems = var_count(p.var) * p.Hq;
 
     if (warp >= 8) {
         setmaxnreg_dec<PERSIST ? C::REG_CTRL : C::REG_CTRL_ONE>();
@@ -219,7 +238,7 @@ __global__ void __launch_bounds__(384, 1)
                 for (int pass = 0; ok && (PERSIST || pass == 0); pass++) {
                     const int w = item_of(pass);
                     if (w >= nitems) break;
-                    const Fwd2Item I = fwd2_item<C>(w, p);
+                    const Fwd2Item I = fwd2_item<C, VAR>(w, p);
                     // this CTA's last item: the next kernel may start launching
                     if (item_of(pass + 1) >= nitems) griddep_launch_dependents();
                     // the item's queries once both O stores of the item that used this
@@ -232,8 +251,10 @@ __global__ void __launch_bounds__(384, 1)
                     const uint32_t sQ = sQ0 + (uint32_t)qb * 2 * C::TILE;
                     mbar_arrive_expect_tx(bar(C::B_Q_FULL + qb), I.hasB ? 2 * C::TILE : C::TILE);
                     for (int c = 0; c < C::NCB; c++) {
-                        tma_load_3d(sQ + c * C::CB, &tmQ, bar(C::B_Q_FULL + qb), c * 64, I.qA0, I.bh);
-                        if (I.hasB) tma_load_3d(sQ + C::TILE + c * C::CB, &tmQ, bar(C::B_Q_FULL + qb), c * 64, I.qB0, I.bh);
+                        tma_load_3d(sQ + c * C::CB, &tmQ, bar(C::B_Q_FULL + qb), c * 64, I.row0 + I.qA0, I.bh);
+                        if (I.hasB)
+                            tma_load_3d(sQ + C::TILE + c * C::CB, &tmQ, bar(C::B_Q_FULL + qb), c * 64, I.row0 + I.qB0,
+                                        I.bh);
                     }
                     q_issued++;
                     // ring slots in order K(lo), V(lo), K(lo+1), V(lo+1), ...
@@ -248,7 +269,7 @@ __global__ void __launch_bounds__(384, 1)
                             mbar_arrive_expect_tx(bar(C::B_KV_FULL + st), C::TILE);
                             for (int c = 0; c < C::NCB; c++)
                                 tma_load_3d_hint(sKV + st * C::TILE + c * C::CB, kv ? &tmV : &tmK,
-                                                 bar(C::B_KV_FULL + st), c * 64, j * C::BN, I.bkv, keep);
+                                                 bar(C::B_KV_FULL + st), c * 64, I.row0 + j * C::BN, I.bkv, keep);
                             issued++;
                         }
                     }
@@ -280,7 +301,7 @@ __global__ void __launch_bounds__(384, 1)
                 for (; ok && (PERSIST || pass == 0); pass++) {
                     const int w = item_of(pass);
                     if (w >= nitems) break;
-                    const Fwd2Item I = fwd2_item<C>(w, p);
+                    const Fwd2Item I = fwd2_item<C, VAR>(w, p);
                     const int qb = pass % C::NQB;
                     const uint32_t sQ = sQ0 + (uint32_t)qb * 2 * C::TILE;
                     // KV range of each tile ([lo_x, hi_x]; empty for a missing tile B)
@@ -368,13 +389,15 @@ __global__ void __launch_bounds__(384, 1)
         const bool cap = p.softcap > 0.0f;
         const uint64_t sl2x2 = f2_make(p.scale_log2, p.scale_log2);
         int cnt = 0;  // KV tiles of this tile slot over the whole run (S_FULL phases)
+        int slot0 = 0;  // ring slot of the current item's K(lo)
         bool ok = true;
         for (int pass = 0; ok && (PERSIST || pass == 0); pass++) {
             const int w = item_of(pass);
             if (w >= nitems) break;
-            const Fwd2Item I = fwd2_item<C>(w, p);
+            const Fwd2Item I = fwd2_item<C, VAR>(w, p);
             const int qb = pass % C::NQB;
             const bool has = (x == 0) || I.hasB;
+            const int W = VAR && p.window >= I.T ? 0 : p.window;  // a window that hides nothing is none
             const int q0 = x ? I.qB0 : I.qA0;
             const int lox = x ? I.loB : I.loA, hix = x ? I.tB : I.tA;
             const int qi = q0 + row;
@@ -486,6 +509,20 @@ __global__ void __launch_bounds__(384, 1)
                     }
                 }
                 tmem_st_wait();
+                if constexpr (VAR) {
+                    // the sequence's last V tile: thread r zeroes row r if it lies past
+                    // the end. Only this tile slot (the pair's last tile) reads it, and
+                    // it is not released before the PV that waits for this warp.
+                    const int end = I.T - k0;
+                    if (end < C::BN) {
+                        const int slotV = slot0 + 2 * (j - I.lo) + 1;
+                        if (!(ok = mbar_wait_warp(bar(C::B_KV_FULL + slotV % C::NSTAGE),
+                                                  (uint32_t)((slotV / C::NSTAGE) & 1), abort_flag)))
+                            break;
+                        zero_tail_rows<128, C::NCB, 128>(sKV + (uint32_t)(slotV % C::NSTAGE) * C::TILE, C::CB, end, row);
+                        fence_proxy_async_smem();
+                    }
+                }
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(bar(C::B_P_FULL + x));
@@ -532,19 +569,34 @@ __global__ void __launch_bounds__(384, 1)
             if (has) {
                 fence_proxy_async_smem();
                 named_barrier_sync(1 + x, 128);
-                if (row == 0) {
-                    for (int cb = 0; cb < C::NCB; cb++) tma_store_3d(&tmO, sO + cb * C::CB, cb * 64, q0, I.bh);
+                if (VAR && q0 + C::BM > I.T) {
+                    // a box would write into the next sequence: the rows up to the end,
+                    // D / 8 chunks of 16 bytes each, one chunk a thread at a time
+                    for (int i = row; i < (I.T - q0) * (D / 8); i += 128) {
+                        const int r = i / (D / 8), ch = i % (D / 8);
+                        uint4 w4;
+                        asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                                     : "=r"(w4.x), "=r"(w4.y), "=r"(w4.z), "=r"(w4.w)
+                                     : "r"(sO + (uint32_t)(ch / 8) * C::CB + (uint32_t)r * 128u +
+                                           (((uint32_t)(ch % 8) ^ (uint32_t)(r & 7)) << 4)));
+                        *reinterpret_cast<uint4 *>(p.o + ((size_t)(I.row0 + q0 + r) * p.Hq + I.bh) * D + ch * 8) = w4;
+                    }
+                    named_barrier_sync(1 + x, 128);  // the buffer is read before it is released below
+                } else if (row == 0) {
+                    for (int cb = 0; cb < C::NCB; cb++)
+                        tma_store_3d(&tmO, sO + cb * C::CB, cb * 64, I.row0 + q0, I.bh);
                     bulk_commit();
                     bulk_wait_read<0>();
                 }
-                if (qi < p.T) p.lse[(size_t)I.bh * p.T + qi] = (m + __log2f(l)) * kLn2;
-                if (p.max_logit) {
+                if (qi < I.T) p.lse[(size_t)I.bh * (VAR ? p.var.rows : p.T) + I.row0 + qi] = (m + __log2f(l)) * kLn2;
+                if (!VAR && p.max_logit) {
                     const float r = warp_max_f32(qi < p.T ? mraw * kLn2 : -INFINITY);
                     if (lane == 0) atomic_max_f32(p.max_logit + I.bh, r);
                 }
             }
             // the Q buffer is free for the item NQB ahead once both tiles' stores read it
             if (row == 0) mbar_arrive(bar(C::B_Q_EMPTY + qb));
+            slot0 += 2 * (I.hi - I.lo + 1);
         }
     }
 

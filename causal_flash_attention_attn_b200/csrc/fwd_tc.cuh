@@ -27,6 +27,7 @@
 #pragma once
 
 #include "sm100.cuh"
+#include "varlen_item.cuh"
 
 namespace forge {
 
@@ -184,9 +185,17 @@ struct FwdParams {
     // not included (QK-Clip's monitor, "Vague 3" item 12); nullptr = not wanted.
     // Must hold -inf (or a lower bound) before the launch: kernels atomic-max it.
     float *max_logit;
+    // packed sequences (the VAR kernels): o is [rows][Hq][D], lse [Hq][rows], B = 1
+    // and T, num_qt unused (each item carries its sequence's length)
+    VarSched var;
 };
 
-template <int DK, int DV = DK>
+// VAR: packed sequences. The CTA's tile comes from the schedule (heads innermost),
+// the tensor maps cover [heads][rows][D] views of the packed tensors, and rows of
+// the next sequence that the last K/V tile of a sequence brings along are kept
+// out: K's by the causal mask, V's by zeroing them in shared memory before the
+// last P is handed to the MMA warp (the softmax warps do it).
+template <int DK, int DV = DK, bool VAR = false>
 __global__ void __launch_bounds__(320, 1)
     fwd_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                   const __grid_constant__ CUtensorMap tmV, const FwdParams p) {
@@ -203,9 +212,22 @@ __global__ void __launch_bounds__(320, 1)
     auto bar = [&](int i) -> uint32_t { return sbase + 8u * (uint32_t)i; };
 
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-    int qt_heavy, bh;
-    grouped_block((int)blockIdx.x, p.num_qt, p.B * p.Hq, qt_heavy, bh);
-    const int qt = p.num_qt - 1 - qt_heavy;
+    int qt, bh, row0 = 0, T = p.T;
+    if constexpr (VAR) {
+        griddep_launch_dependents();
+        griddep_wait();  // the schedule (and, behind it, q, k and v) is visible
+        const int w = (int)blockIdx.x;
+        if (w / p.Hq >= var_count(p.var)) return;  // the grid is an upper bound; uniform over the CTA
+        const VarItem it = var_item(p.var, w / p.Hq);
+        bh = w % p.Hq;
+        qt = it.tile;
+        row0 = it.row0;
+        T = it.len;
+    } else {
+        int qt_heavy;
+        grouped_block((int)blockIdx.x, p.num_qt, p.B * p.Hq, qt_heavy, bh);
+        qt = p.num_qt - 1 - qt_heavy;
+    }
     const int b = bh / p.Hq, hq = bh % p.Hq;
     const int bkv = b * p.Hkv + hq / (p.Hq / p.Hkv);
     const int q0 = qt * C::BM;
@@ -246,7 +268,7 @@ __global__ void __launch_bounds__(320, 1)
         if (lane == 0) {
             const uint64_t keep = policy_evict_last();
             mbar_arrive_expect_tx(bar(C::B_Q), C::TILEK);
-            for (int c = 0; c < C::NCBK; c++) tma_load_3d(sQ + c * C::CB, &tmQ, bar(C::B_Q), c * 64, q0, bh);
+            for (int c = 0; c < C::NCBK; c++) tma_load_3d(sQ + c * C::CB, &tmQ, bar(C::B_Q), c * 64, row0 + q0, bh);
             int stage = 0;
             uint32_t ph = 0;
             int issued = 0;
@@ -257,7 +279,7 @@ __global__ void __launch_bounds__(320, 1)
                 mbar_arrive_expect_tx(bar(C::B_KV_FULL + stage), is_v ? C::TILEV : C::TILEK);
                 for (int c = 0; c < (is_v ? C::NCBV : C::NCBK); c++)
                     tma_load_3d_hint(sKV + stage * C::SLOT + c * C::CB, m, bar(C::B_KV_FULL + stage), c * 64,
-                                     j * C::BN, bkv, keep);
+                                     row0 + j * C::BN, bkv, keep);
                 issued++;
                 if (++stage == C::NSTAGE) {
                     stage = 0;
@@ -354,7 +376,7 @@ __global__ void __launch_bounds__(320, 1)
         const int qi = q0 + row;
         const uint32_t lane_base = (uint32_t)(quad * 32) << 16;
         const uint32_t pair_bar = 1 + (uint32_t)quad;  // named barrier of warps quad, quad + 4
-        const int W = p.window;
+        const int W = VAR && p.window >= T ? 0 : p.window;  // a window that hides nothing is none
         float m = p.sink ? p.sink[hq] * kLog2e : -INFINITY;
         // the sink's 1 in the sum is counted once, by half 0
         float l = (p.sink && hf == 0) ? 1.0f : 0.0f;
@@ -449,6 +471,23 @@ __global__ void __launch_bounds__(320, 1)
                 tmem_st32(tS + 64 + hf * 32, pk);
             }
             tmem_st_wait();
+            if constexpr (VAR) {
+                // the sequence's last V tile: rows past its end become zeros. V(u) is
+                // the ring's load 2 (K 0, K 1), 4, ... (n > 1), or 1 (n = 1), and is
+                // not released before PV(u), which waits for this warp's arrival.
+                const int end = T - (lo + u) * C::BN;
+                if (end < C::BN) {
+                    const int load = n > 1 ? min(2 * u + 2, n + u) : 1;
+                    if (!mbar_wait_warp(bar(C::B_KV_FULL + load % C::NSTAGE), (uint32_t)((load / C::NSTAGE) & 1),
+                                        abort_flag)) {
+                        ok = false;
+                        break;
+                    }
+                    zero_tail_rows<C::BN, C::NCBV, 256>(sKV + (uint32_t)(load % C::NSTAGE) * C::SLOT, C::CB, end,
+                                                        (int)threadIdx.x);
+                    fence_proxy_async_smem();
+                }
+            }
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(bar(C::B_P_FULL + buf));
@@ -462,7 +501,8 @@ __global__ void __launch_bounds__(320, 1)
             named_barrier_sync(pair_bar, 64);
             const float lt = l + xsum[(hf ^ 1) * 128 + row];
             const float inv_l = 1.0f / lt;
-            __nv_bfloat16 *orow = p.o + ((size_t)bh * p.T + (size_t)min(qi, p.T - 1)) * DV;
+            const int qc = min(qi, T - 1);
+            __nv_bfloat16 *orow = p.o + (VAR ? (size_t)(row0 + qc) * p.Hq + bh : (size_t)bh * p.T + (size_t)qc) * DV;
 #pragma unroll 1
             for (int c0 = hf * (DV / 2); c0 < (hf + 1) * (DV / 2); c0 += 32) {
                 uint32_t o[32];
@@ -472,15 +512,15 @@ __global__ void __launch_bounds__(320, 1)
 #pragma unroll
                 for (int i = 0; i < 16; i++)
                     w[i] = pack_bf16x2(__uint_as_float(o[2 * i]) * inv_l, __uint_as_float(o[2 * i + 1]) * inv_l);
-                if (qi < p.T) {
+                if (qi < T) {
                     uint4 *dst = reinterpret_cast<uint4 *>(orow + c0);
 #pragma unroll
                     for (int i = 0; i < 4; i++) dst[i] = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
                 }
             }
             if (hf == 0) {
-                if (qi < p.T) p.lse[(size_t)bh * p.T + qi] = (m + __log2f(lt)) * kLn2;
-                if (p.max_logit) {
+                if (qi < T) p.lse[(size_t)bh * (VAR ? p.var.rows : p.T) + row0 + qi] = (m + __log2f(lt)) * kLn2;
+                if (!VAR && p.max_logit) {
                     const float r = warp_max_f32(qi < p.T ? mraw * kLn2 : -INFINITY);
                     if (lane == 0) atomic_max_f32(p.max_logit + bh, r);
                 }

@@ -1,0 +1,243 @@
+// varlen.cuh -- attention over packed sequences: the schedule, and the HBM-bound
+// stages around the backward.
+//
+// Sequences of different lengths lie one after the other along the row axis of
+// [rows][heads][D] tensors; cu_seqlens[b] is the first row of sequence b and
+// cu_seqlens[num_seqs] the first row behind the last one. Query and key tiles
+// start at their sequence's first row, so a tile never mixes two sequences and
+// one sequence's values (an infinity, a NaN) never reach another's results.
+//
+// The lengths are read on the device: varlen_plan writes the list of tiles that
+// the attention kernels walk, heaviest first (a tile's weight is the span of keys,
+// or of queries in the backward, that it has to visit), with the number of tiles
+// in front. Launches are sized by an upper bound that needs only `rows` and
+// `num_seqs`.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+#include <math.h>
+#include <stdint.h>
+
+#include "bwd_aux.cuh"
+#include "simt.cuh"
+#include "sm100.cuh"
+#include "varlen_item.cuh"
+
+namespace forge {
+
+constexpr int kPlanThreads = 1024;  // also the weight classes, and the sequences held in shared memory at once
+
+struct VarPlanParams {
+    const int *cu;  // [num_seqs + 1]
+    int num_seqs, rows;
+    int unit;      // rows of a tile
+    int window;    // 0 = none
+    int backward;  // weights: 0 = keys a query tile sees, 1 = queries that see a key tile
+    VarItem *items;
+    int *count;
+    int max_items;
+    // tensors whose rows behind the last sequence are set to zero (nullptr = none):
+    // [rows][row_chunks * 16 bytes]
+    uint4 *tail[3];
+    int tail_chunks[3];
+    float *tail_lse;  // [heads][rows], set to -inf there
+    int heads;
+};
+
+// Exclusive prefix sum over the block's 1024 threads; `total` gets the sum.
+__device__ __forceinline__ int plan_scan(int x, int &total, int *warp_sums) {
+    const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+    int s = x;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, s, o);
+        if (lane >= o) s += y;
+    }
+    __syncthreads();  // the previous scan's warp_sums have been read
+    if (lane == 31) warp_sums[warp] = s;
+    __syncthreads();
+    int w = warp_sums[lane];
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, w, o);
+        if (lane >= o) w += y;
+    }
+    total = __shfl_sync(0xffffffffu, w, 31);
+    const int before = __shfl_sync(0xffffffffu, w, (warp + 31) % 32);
+    return (warp ? before : 0) + s - x;
+}
+
+// Block 0 writes the schedule: a counting sort of the tiles by weight class, one
+// warp per sequence, one lane per tile. The other blocks clear the rows behind the
+// last sequence. Lengths that do not ascend from 0 or that leave the tensors are
+// reported as FORGE_ERR_INVALID_ARG, and no tile is scheduled.
+__global__ void __launch_bounds__(kPlanThreads) varlen_plan(const VarPlanParams p) {
+    griddep_launch_dependents();
+    griddep_wait();
+    if (blockIdx.x > 0) {
+        const int end = min(max(p.cu[p.num_seqs], 0), p.rows);
+        const size_t t0 = (size_t)(blockIdx.x - 1) * blockDim.x + threadIdx.x;
+        const size_t nt = (size_t)(gridDim.x - 1) * blockDim.x;
+#pragma unroll
+        for (int i = 0; i < 3; i++) {
+            if (p.tail[i] == nullptr) continue;
+            const size_t c = (size_t)p.tail_chunks[i];
+            for (size_t j = (size_t)end * c + t0; j < (size_t)p.rows * c; j += nt) p.tail[i][j] = make_uint4(0, 0, 0, 0);
+        }
+        const size_t left = (size_t)(p.rows - end);
+        if (p.tail_lse != nullptr)
+            for (size_t j = t0; j < left * p.heads; j += nt)
+                p.tail_lse[(j / left) * p.rows + end + j % left] = -INFINITY;
+        return;
+    }
+    __shared__ int cls[kPlanThreads], first[kPlanThreads], length[kPlanThreads], padded[kPlanThreads], sums[32];
+    const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
+    const int gran = max(128, (p.rows + kPlanThreads - 1) / kPlanThreads);
+    const int most = p.window > 0 ? (int)min((long long)p.window + p.unit, (long long)p.rows) : p.rows;
+    auto klass = [&](int len, int t) -> int {
+        const int span = p.backward ? len - t * p.unit : min(len, (t + 1) * p.unit);
+        return min(min(span, most) / gran, kPlanThreads - 1);
+    };
+    bool bad = tid == 0 && p.cu[0] != 0;
+    cls[tid] = 0;
+    int total = 0;
+    for (int pass = 0; pass < 2; pass++) {
+        int pad = 0;
+        for (int c0 = 0; c0 < p.num_seqs; c0 += kPlanThreads) {
+            if (pass == 0 || p.num_seqs > kPlanThreads) {
+                const int b = c0 + tid;
+                int s = 0, len = 0;
+                if (b < p.num_seqs) {
+                    s = p.cu[b];
+                    const int e = p.cu[b + 1];
+                    if (s >= 0 && s <= e && e <= p.rows) len = e - s;
+                    else bad = true;
+                }
+                int sum;
+                __syncthreads();  // the previous chunk has been read
+                const int at = plan_scan((len + 127) / 128 * 128, sum, sums);
+                first[tid] = s;
+                length[tid] = len;
+                padded[tid] = pad + at;
+                pad += sum;
+            }
+            __syncthreads();
+            for (int i = warp; i < min(kPlanThreads, p.num_seqs - c0); i += 32) {
+                const int len = length[i];
+                for (int t = lane; t * p.unit < len; t += 32) {
+                    const int at = atomicAdd(&cls[klass(len, t)], 1);
+                    if (pass == 1 && at < p.max_items) p.items[at] = VarItem{first[i], len, t, padded[i]};
+                }
+            }
+        }
+        __syncthreads();
+        if (pass == 0) {
+            // lengths that do not add up could overlap: nothing is scheduled then
+            if (__syncthreads_or(bad)) {
+                if (tid == 0) {
+                    *p.count = 0;
+                    record_status(kStatusInvalidArg);
+                }
+                return;
+            }
+            // class sizes -> first place of each class, the heaviest class first
+            const int n = cls[kPlanThreads - 1 - tid];
+            const int at = plan_scan(n, total, sums);
+            __syncthreads();
+            cls[kPlanThreads - 1 - tid] = at;
+            __syncthreads();
+        }
+    }
+    if (tid == 0) *p.count = min(total, p.max_items);
+}
+
+// Delta_i = rowsum(dO_i * o_i) of a tile of one head, and (acc != nullptr)
+// the tile's rows of the padded dq accumulator set to zero. One block per (tile,
+// head), heads innermost; LPR lanes a row as in bwd_preprocess.
+template <typename T, int D>
+__global__ void __launch_bounds__(256) varlen_preprocess(const T *__restrict__ o, const T *__restrict__ dO,
+                                                         float *__restrict__ delta, float *__restrict__ acc, int Hq,
+                                                         const VarSched var) {
+    constexpr int LPR = D / 8 < 32 ? D / 8 : 32;  // lanes per row
+    constexpr int RPB = 256 / LPR;                // rows per pass of the block
+    griddep_launch_dependents();
+    griddep_wait();
+    const int item = blockIdx.x / Hq, h = blockIdx.x % Hq;
+    if (item >= var_count(var)) return;
+    const VarItem it = var_item(var, item);
+    const int sub = threadIdx.x % LPR, n = min(var.unit, it.len - it.tile * var.unit);
+    const size_t row0 = (size_t)it.row0 + (size_t)it.tile * var.unit;
+    float *arow0 = acc == nullptr ? nullptr : acc + ((size_t)h * var.pad_rows + it.pad0 + (size_t)it.tile * var.unit) * D;
+    for (int r0 = 0; r0 < n; r0 += RPB) {
+        const int r = r0 + threadIdx.x / LPR;
+        const bool live = r < n;
+        const size_t at = ((row0 + (live ? r : 0)) * Hq + h) * D;  // every lane takes part in the shuffles
+        if (acc != nullptr && live)
+            for (int c = sub * 4; c < D; c += 4 * LPR)
+                *reinterpret_cast<float4 *>(arow0 + (size_t)r * D + c) = make_float4(0.f, 0.f, 0.f, 0.f);
+        float sum = 0.0f;
+#pragma unroll
+        for (int c = sub * 8; c < D; c += 8 * LPR) {
+            float a[8], b[8];
+            load8(o + at + c, a);
+            load8(dO + at + c, b);
+#pragma unroll
+            for (int i = 0; i < 8; i++) sum = fmaf(a[i], b[i], sum);
+        }
+#pragma unroll
+        for (int off = LPR / 2; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
+        if (sub == 0 && live) delta[(size_t)h * var.rows + row0 + r] = sum;
+    }
+}
+
+// dq rows of a 128-row tile of one head from the padded accumulator.
+template <int D>
+__global__ void __launch_bounds__(256) varlen_finalize_dq(const float *__restrict__ acc, __nv_bfloat16 *__restrict__ dq,
+                                                          int Hq, const VarSched var) {
+    constexpr int CH = D / 8;  // 8-element chunks per row
+    griddep_launch_dependents();
+    griddep_wait();
+    const int item = blockIdx.x / Hq, h = blockIdx.x % Hq;
+    if (item >= var_count(var)) return;
+    const VarItem it = var_item(var, item);
+    const int n = min(var.unit, it.len - it.tile * var.unit);
+    const size_t row0 = (size_t)it.row0 + (size_t)it.tile * var.unit;
+    const float *arow0 = acc + ((size_t)h * var.pad_rows + it.pad0 + (size_t)it.tile * var.unit) * D;
+    for (int i = threadIdx.x; i < n * CH; i += 256) {
+        const int r = i / CH, c = i % CH;
+        float f[8];
+        load8(arow0 + (size_t)r * D + c * 8, f);
+        uint4 u;
+        uint32_t *w = reinterpret_cast<uint32_t *>(&u);
+#pragma unroll
+        for (int e = 0; e < 4; e++) w[e] = pack_bf16x2(f[2 * e], f[2 * e + 1]);
+        *reinterpret_cast<uint4 *>(dq + ((row0 + r) * Hq + h) * D + c * 8) = u;
+    }
+}
+
+// dsink[h] = -sum over the rows of all sequences of exp(sink[h] - lse) * Delta. One
+// block per head, in a fixed order.
+__global__ void __launch_bounds__(512) varlen_sink_grad(const float *lse, const float *delta, const float *sink,
+                                                        float *dsink, const int *cu, int num_seqs, int rows) {
+    __shared__ float part[16];
+    griddep_launch_dependents();
+    griddep_wait();
+    const int h = blockIdx.x, end = min(max(cu[num_seqs], 0), rows);
+    const float sg = sink[h];
+    float acc = 0.0f;
+    for (int t = threadIdx.x; t < end; t += 512) {
+        const size_t at = (size_t)h * rows + t;
+        acc -= expf(sg - lse[at]) * delta[at];
+    }
+    acc = warp_sum(acc);
+    if (threadIdx.x % 32 == 0) part[threadIdx.x / 32] = acc;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        float sum = 0.0f;
+        for (int w = 0; w < 16; w++) sum += part[w];
+        dsink[h] = sum;
+    }
+}
+
+}  // namespace forge

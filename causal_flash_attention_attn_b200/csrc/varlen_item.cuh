@@ -1,0 +1,60 @@
+// varlen_item.cuh -- one tile of a packed batch, as the kernels for packed
+// sequences read it from the schedule that varlen_plan (varlen.cuh) writes.
+#pragma once
+
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+namespace forge {
+
+struct alignas(16) VarItem {
+    int row0;  // first row of the sequence in the packed tensors
+    int len;   // rows of the sequence
+    int tile;  // tile index within the sequence
+    int pad0;  // first row of the sequence in tensors whose sequences are padded to 128 rows
+};
+
+// The schedule of one call, in device memory. Both are written by an earlier
+// kernel of the same stream, so they are read with plain (not read-only-cache)
+// loads, after griddep_wait.
+struct VarSched {
+    const VarItem *items;
+    const int *count;  // tiles in `items`
+    int unit;          // rows of a tile
+    int rows;          // rows of the packed tensors
+    int pad_rows;      // rows of the padded tensors (an upper bound)
+};
+
+__device__ __forceinline__ VarItem var_item(const VarSched &v, int i) {
+    VarItem t;
+    asm volatile("ld.global.v4.b32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(t.row0), "=r"(t.len), "=r"(t.tile), "=r"(t.pad0)
+                 : "l"(v.items + i)
+                 : "memory");
+    return t;
+}
+__device__ __forceinline__ int var_count(const VarSched &v) {
+    int n;
+    asm volatile("ld.global.b32 %0, [%1];" : "=r"(n) : "l"(v.count) : "memory");
+    return n;
+}
+
+// Rows [valid, ROWS) of a tile of NCB swizzled column blocks (128 bytes a row, `cb`
+// bytes a block) set to zero by NT threads, t = 0 .. NT - 1. A TMA box that runs past a sequence's
+// end brings rows of the next sequence: they are replaced by the zeros that a
+// box past the tensor's end would have brought, so that a product summed over
+// the tile's rows never multiplies them (zero times an infinity is NaN). Zeros
+// are the same under the swizzle, which permutes the 16-byte chunks of a row.
+template <int ROWS, int NCB, int NT>
+__device__ __forceinline__ void zero_tail_rows(uint32_t tile, uint32_t cb, int valid, int t) {
+    for (int r = valid + t / 8; r < ROWS; r += NT / 8) {
+#pragma unroll
+        for (int c = 0; c < NCB; c++)
+            asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(tile + c * cb + (uint32_t)r * 128u +
+                                                                         (uint32_t)(t % 8) * 16u),
+                         "r"(0)
+                         : "memory");
+    }
+}
+
+}  // namespace forge

@@ -1,0 +1,172 @@
+"""The books of a paged KV cache: which pages each sequence holds, how many sequences share a
+page, which are free. Bookkeeping is host work on plain integers; the pages themselves move
+through the library's kernels (paged_append, paged_copy, attention_decode_paged)."""
+from __future__ import annotations
+
+import heapq
+
+
+class PagedCache:
+    """Pools of `num_pages` pages for `num_layers` layers, and the sequences in them.
+
+        cache = PagedCache(num_pages=512, num_kv_heads=8, head_dim=128, num_layers=2)
+        a = cache.new()
+        starts = cache.extend([a], [100])             # room for 100 tokens; positions to append at
+        for layer in range(2):
+            cache.append(layer, k[layer], v[layer], [a], starts, cu_seqlens)
+        b = cache.fork(a)                             # shares a's pages
+        ...
+        o, lse = cache.decode(layer, q, [a, b])
+
+    A page is shared by the forks of a sequence until one of them writes into it: extend() then
+    gives that sequence a copy (its last, partly filled page only, in every layer). free() and compact()
+    return pages and close the gaps. Page tables are built on the host; tables() copies them
+    to the device.
+
+    k_pages, v_pages: [num_layers, num_pages, num_kv_heads, page_size, head_dim]; they may be given
+    (pages=(k, v)) instead of being allocated.
+    """
+
+    def __init__(self, num_pages, num_kv_heads, head_dim, page_size=64, num_layers=1, dtype=None, device="cuda",
+                 pages=None):
+        if min(num_pages, num_kv_heads, head_dim, page_size, num_layers) < 1:
+            raise ValueError("PagedCache: every size must be at least 1")
+        if page_size % 16:
+            raise ValueError(f"PagedCache: page_size must be a multiple of 16, got {page_size}")
+        shape = (num_layers, num_pages, num_kv_heads, page_size, head_dim)
+        if pages is None:
+            import torch
+            dtype = torch.bfloat16 if dtype is None else dtype
+            pages = tuple(torch.empty(shape, dtype=dtype, device=device) for _ in range(2))
+        for t in pages:
+            if tuple(t.shape) != shape:
+                raise ValueError(f"PagedCache: pages of shape {tuple(t.shape)}, expected {shape}")
+        self.k_pages, self.v_pages = pages
+        self.num_pages, self.page_size, self.num_layers = num_pages, page_size, num_layers
+        self._free = list(range(num_pages))   # a heap: the lowest page first
+        self._refs = [0] * num_pages
+        self._pages = {}                      # sequence -> its pages in order
+        self._lens = {}                       # sequence -> tokens
+        self._next = 0
+
+    # ------------------------------------------------------------------ the books
+    @property
+    def free_pages(self):
+        return len(self._free)
+
+    def length(self, seq):
+        return self._lens[seq]
+
+    def pages(self, seq):
+        return list(self._pages[seq])
+
+    def new(self):
+        """A new, empty sequence's handle."""
+        seq = self._next
+        self._next += 1
+        self._pages[seq], self._lens[seq] = [], 0
+        return seq
+
+    def fork(self, seq):
+        """A new sequence with the same tokens. Shares seq's pages; nothing is copied yet."""
+        new = self.new()
+        self._pages[new], self._lens[new] = list(self._pages[seq]), self._lens[seq]
+        for p in self._pages[new]:
+            self._refs[p] += 1
+        return new
+
+    def free(self, seq):
+        """Forget a sequence; pages that no other sequence holds become free."""
+        for p in self._pages.pop(seq):
+            self._drop(p)
+        del self._lens[seq]
+
+    def _drop(self, page):
+        self._refs[page] -= 1
+        if self._refs[page] == 0:
+            heapq.heappush(self._free, page)
+
+    def _take(self):
+        page = heapq.heappop(self._free)
+        self._refs[page] = 1
+        return page
+
+    def extend(self, seqs, counts, stream=None):
+        """Make room for counts[i] more tokens of seqs[i] (each sequence once). A partly filled last page
+        that is shared is copied first, in every layer. Returns the old lengths: the positions to append
+        at. All or nothing: MemoryError if the free pages do not suffice."""
+        seqs, counts = list(seqs), list(counts)
+        if len(seqs) != len(counts) or len(set(seqs)) != len(seqs):
+            raise ValueError("PagedCache.extend: one count for each sequence, each sequence once")
+        if any(n < 0 for n in counts):
+            raise ValueError("PagedCache.extend: a negative count")
+        ps = self.page_size
+        need, shared, refs = 0, [], {}
+        for s, n in zip(seqs, counts):
+            held = self._lens[s]
+            need += -(-(held + n) // ps) - len(self._pages[s])
+            if n and held % ps:
+                # the last sequence left on a page writes into it as it is
+                last = self._pages[s][-1]
+                if refs.setdefault(last, self._refs[last]) > 1:
+                    refs[last] -= 1
+                    shared.append(s)
+        if need + len(shared) > len(self._free):
+            raise MemoryError(f"PagedCache: {need + len(shared)} pages needed, {len(self._free)} free")
+        moves = []
+        for s in shared:
+            old, page = self._pages[s][-1], self._take()
+            self._pages[s][-1] = page
+            self._drop(old)
+            moves.append((old, page))
+        starts = []
+        for s, n in zip(seqs, counts):
+            starts.append(self._lens[s])
+            self._lens[s] += n
+            while len(self._pages[s]) * ps < self._lens[s]:
+                self._pages[s].append(self._take())
+        self._copy(moves, stream)
+        return starts
+
+    def compact(self, stream=None):
+        """Move pages down until the held ones are 0 .. n - 1, in every layer. Returns the moves
+        [(from, to), ..]; tables made before are stale after it."""
+        held = sorted(p for p in range(self.num_pages) if self._refs[p])
+        holes = [p for p in range(len(held)) if not self._refs[p]]
+        moves = list(zip(reversed(held[len(held) - len(holes):]), holes)) if holes else []
+        to = dict(moves)
+        for old, new in moves:
+            self._refs[new], self._refs[old] = self._refs[old], 0
+        for s, pages in self._pages.items():
+            self._pages[s] = [to.get(p, p) for p in pages]
+        self._free = list(range(len(held), self.num_pages))
+        self._copy(moves, stream)
+        return moves
+
+    def _copy(self, moves, stream):
+        if moves:
+            from . import paged_copy
+            paged_copy(self.k_pages, self.v_pages, [a for a, _ in moves], [b for _, b in moves], stream=stream)
+
+    # ------------------------------------------------------------------ on the device
+    def tables(self, seqs):
+        """(page_table int32 [len(seqs), width], seq_lens int32 [len(seqs)]) on the pools' device."""
+        import torch
+        width = max([1] + [len(self._pages[s]) for s in seqs])
+        rows = [self._pages[s] + [0] * (width - len(self._pages[s])) for s in seqs]
+        device = self.k_pages.device
+        return (torch.tensor(rows, dtype=torch.int32).to(device),
+                torch.tensor([self._lens[s] for s in seqs], dtype=torch.int32).to(device))
+
+    def append(self, layer, k, v, seqs, starts, cu_seqlens=None, stream=None):
+        """Write new tokens of one layer at the positions that extend() returned (paged_append)."""
+        import torch
+        from . import paged_append
+        starts = torch.tensor(list(starts), dtype=torch.int32).to(self.k_pages.device)
+        paged_append(k, v, self.k_pages[layer], self.v_pages[layer], self.tables(seqs)[0], starts, cu_seqlens, stream)
+
+    def decode(self, layer, q, seqs, stream=None, **options):
+        """attention_decode_paged of one new query per sequence; options: scale, window, softcap, sink."""
+        from . import attention_decode_paged
+        table, lens = self.tables(seqs)
+        return attention_decode_paged(q, self.k_pages[layer], self.v_pages[layer], table, lens, stream=stream, **options)

@@ -239,10 +239,105 @@ forge_status forge_attn_decode(const void *q, const void *k_cache, const void *v
                                size_t workspace_bytes, void *stream);
 
 /*
+ * Attention over packed sequences (no counterpart on the Forge pages): causal
+ * attention of num_seqs sequences of different lengths that lie one after the other
+ * along the rows of
+ *   q, o, dO, dq : [rows][Hq][D]      k, v, dk, dv : [rows][Hkv][D]
+ *   lse          : [Hq][rows] f32
+ *   cu_seqlens   : [num_seqs + 1] int32 (device): sequence b has the rows
+ *                  [cu_seqlens[b], cu_seqlens[b + 1]); cu_seqlens[0] = 0; a length may be 0.
+ * A row sees the rows of its own sequence only, by the rules at the top of this file
+ * (position = row - cu_seqlens[b]); no value of one sequence, an infinity or a NaN
+ * included, reaches another's results.
+ *  - q_stride, k_stride, v_stride: elements between two rows (>= heads * D, a multiple
+ *    of 16 bytes), so that q, k and v may be parts of one projection's output. o, dO,
+ *    dq, dk, dv and lse are dense.
+ *  - Rows at or behind cu_seqlens[num_seqs] are not read. Outputs there are left as they
+ *    were (clear_tail = 0), or set to zero, lse to -inf (clear_tail != 0).
+ *  - The lengths are read on the device: nothing synchronises, and a captured call
+ *    follows the lengths that cu_seqlens holds at each replay. Lengths that do not ascend from
+ *    0, or that pass `rows`, are reported as FORGE_ERR_INVALID_ARG by the next
+ *    forge_attn_check; nothing is computed then.
+ *  - sink, dsink: as in forge_attn_fwd_ext / forge_attn_bwd_ext. scale, window, softcap
+ *    as in forge_attn_fwd (a window >= rows acts as off).
+ *  - rows and num_seqs >= 1, num_seqs <= 2^20, (rows / 64 + num_seqs) * Hq < 2^30; the limits
+ *    of the dense calls with B = 1, T = rows.
+ * workspace: 256-byte aligned device memory of at least the given size, overwritten:
+ * the schedule, and in the backward Delta and (bf16) an f32 dq accumulator whose sequences
+ * are padded to 128 rows. dq (bf16) is summed with f32 atomics whose order differs
+ * between calls; o, lse, dk, dv and everything in f32 are the same on every call. The backward
+ * takes o and lse as forge_attn_varlen_fwd wrote them.
+ */
+size_t forge_attn_varlen_fwd_workspace_size(int num_seqs, int rows, int Hq, int Hkv, int D, forge_dtype dtype);
+forge_status forge_attn_varlen_fwd(const void *q, const void *k, const void *v, void *o, float *lse,
+                                   const int *cu_seqlens, int num_seqs, int rows, int Hq, int Hkv, int D,
+                                   size_t q_stride, size_t k_stride, size_t v_stride, float scale, int window,
+                                   float softcap, const float *sink, int clear_tail, forge_dtype dtype,
+                                   void *workspace, size_t workspace_bytes, void *stream);
+size_t forge_attn_varlen_bwd_workspace_size(int num_seqs, int rows, int Hq, int Hkv, int D, forge_dtype dtype);
+forge_status forge_attn_varlen_bwd(const void *q, const void *k, const void *v, const void *o, const float *lse,
+                                   const void *dO, void *dq, void *dk, void *dv, const int *cu_seqlens, int num_seqs,
+                                   int rows, int Hq, int Hkv, int D, size_t q_stride, size_t k_stride, size_t v_stride,
+                                   float scale, int window, float softcap, const float *sink, float *dsink,
+                                   int clear_tail, forge_dtype dtype, void *workspace, size_t workspace_bytes,
+                                   void *stream);
+
+/*
+ * A paged KV cache (no counterpart on the Forge pages, which keep the cache
+ * contiguous): one layer's pool of pages for K and one for V,
+ *   k_pages, v_pages : [num_pages][Hkv][page_size][D], pages page_stride elements apart
+ *                      (>= Hkv * page_size * D, a multiple of 16 bytes; 16-byte aligned)
+ *   page_table       : [B or num_seqs][table_width] int32 (device): position t of sequence b
+ *                      is row t % page_size of page page_table[b][t / page_size]
+ * page_size is a multiple of 16 (FORGE_ERR_UNSUPPORTED otherwise); D in {64, 128, 256};
+ * dtype bf16 or f32. Table entries past a sequence's length are not read. A page outside
+ * [0, num_pages), or a length or position outside the table, is reported as
+ * FORGE_ERR_INVALID_ARG by the next forge_attn_check; no memory outside the pool is touched.
+ *
+ * forge_attn_decode_paged: one new query per (sequence, query head), as forge_attn_decode.
+ *   q, o : [B][Hq][D]; lse : [B][Hq] f32 (may be NULL); seq_lens : [B] int32 (device), 0 <=
+ *   seq_lens[b] <= table_width * page_size. Sequence b's query sits at position len - 1. Length
+ *   0 (a padded batch entry): o = 0 and lse = -inf, or the sink. An entry with a bad
+ *   length is taken as empty, a bad page as holding no visible key. Hq / Hkv <= 16. Rows of
+ *   the pool that no query sees are not read: what they hold (NaN included) does not matter.
+ *   workspace: 16-byte aligned, overwritten, of at least the given size, which does
+ *   not depend on the lengths. Two kernels: the split pass (the batch's visible keys in
+ *   equal shares over the SMs) and the join.
+ *
+ * forge_attn_paged_append: writes the new tokens k, v [rows][Hkv][D] (k_stride, v_stride
+ *   elements between rows, a multiple of 16 bytes) at positions starts[b], starts[b] + 1, ...
+ *   of their sequences. cu_seqlens [num_seqs + 1] as above (rows at or behind the last
+ *   entry are skipped), or NULL: rows = num_seqs, one token each. A token whose place is bad
+ *   is skipped and reported. Two sequences' tables must not share a page that is written.
+ *
+ * forge_attn_paged_copy: page src[i] onto page dst[i] for i = 0 .. n - 1, for K and V, in
+ *   each of num_layers layers whose pools lie layer_stride elements apart. src and dst are
+ *   HOST arrays, read before the call returns. The result is that of copying one after
+ *   the other in the order given (an index may come again, a page may be a source and a
+ *   destination); copies that do not depend on one another share a launch. Page numbers
+ *   outside [0, num_pages) are refused before anything is launched; n = 0 does nothing.
+ */
+size_t forge_attn_decode_paged_workspace_size(int B, int Hq, int Hkv, int D, forge_dtype dtype);
+forge_status forge_attn_decode_paged(const void *q, const void *k_pages, const void *v_pages, void *o, float *lse,
+                                     const int *page_table, const int *seq_lens, int B, int Hq, int Hkv, int D,
+                                     int num_pages, int page_size, int table_width, size_t page_stride, float scale,
+                                     int window, float softcap, const float *sink, forge_dtype dtype, void *workspace,
+                                     size_t workspace_bytes, void *stream);
+forge_status forge_attn_paged_append(const void *k, const void *v, void *k_pages, void *v_pages,
+                                     const int *page_table, const int *starts, const int *cu_seqlens, int num_seqs,
+                                     int rows, int Hkv, int D, int num_pages, int page_size, int table_width,
+                                     size_t k_stride, size_t v_stride, size_t page_stride, forge_dtype dtype,
+                                     void *stream);
+forge_status forge_attn_paged_copy(void *k_pages, void *v_pages, const int *src, const int *dst, int n,
+                                   int num_layers, size_t layer_stride, int num_pages, int Hkv, int page_size, int D,
+                                   size_t page_stride, forge_dtype dtype, void *stream);
+
+/*
  * Synchronises `stream`, then reports (and clears) the error a kernel of this
  * library recorded on the current device since the last check, or FORGE_OK:
  *   FORGE_ERR_TIMEOUT      a bounded wait inside a kernel ran out;
- *   FORGE_ERR_INVALID_ARG  a decode length outside [1, T] (forge_attn_decode);
+ *   FORGE_ERR_INVALID_ARG  a decode length outside [1, T] (forge_attn_decode), or bad
+ *                          lengths, positions or pages of a packed or paged call;
  *   FORGE_ERR_UNSUPPORTED  the backward's shared-memory layout did not fit the
  *                          dynamic shared-memory base it was given (nothing written);
  *   FORGE_ERR_CUDA         an asynchronous CUDA error (forge_attn_last_cuda_error).

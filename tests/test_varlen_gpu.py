@@ -1,0 +1,352 @@
+"""Attention over packed sequences on the GPU, forward and backward, against the f64 oracle run on
+each sequence by itself (the definition of the packed call). Tolerances are those of the other
+parity tests (parity_util): 1e-4 for f32, 2e-2 + 1e-2 |ref| for bf16 with Delta from the bf16 o; where
+many terms add up, the bf16 bar gives way to the sum of the roundings themselves (`roundings`)."""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import causal_flash_attention_attn_b200 as fa
+import oracle
+from parity_util import check_close
+
+pytestmark = pytest.mark.gpu
+DEV = torch.device("cuda:0")
+TDT = {"bf16": torch.bfloat16, "f32": torch.float32}
+
+EDGES = [0, 1, 127, 128, 129, 0, 255, 256, 257, 2, 385]
+CASES = [
+    # name, dtype, lens, pad, Hq, Hkv, D, window, softcap, sink, fused
+    ("d128_edges", "bf16", EDGES, 0, 4, 2, 128, 0, 0.0, False, False),
+    ("d128_fused_pad", "bf16", [300, 45, 130], 70, 14, 2, 128, 0, 0.0, False, True),
+    ("d128_win_cap_sink", "bf16", [385, 3, 0, 260], 1, 4, 1, 128, 100, 5.0, True, True),
+    ("d128_win1", "bf16", [130, 7], 0, 2, 2, 128, 1, 0.0, False, False),
+    ("d128_long", "bf16", [2500, 60], 0, 2, 1, 128, 0, 0.0, False, False),
+    ("d64_edges", "bf16", EDGES, 5, 3, 3, 64, 0, 0.0, True, False),
+    ("d64_many_short", "bf16", [1 + 7 * i % 61 for i in range(150)], 0, 2, 1, 64, 0, 0.0, False, True),
+    ("d64_win", "bf16", [700, 512, 90], 0, 6, 6, 64, 200, 0.0, False, False),
+    ("d256_edges", "bf16", EDGES, 0, 2, 1, 256, 0, 0.0, False, False),
+    ("d256_win_cap_sink", "bf16", [333, 64, 65], 9, 4, 2, 256, 150, 50.0, True, True),
+    ("one_row", "bf16", [1], 0, 1, 1, 128, 0, 0.0, False, False),
+    ("f32_d64_edges", "f32", [0, 1, 63, 64, 65, 130], 3, 4, 2, 64, 0, 0.0, True, True),
+    ("f32_d128_win", "f32", [200, 31], 0, 4, 1, 128, 40, 0.0, False, False),
+    ("f32_d256_cap", "f32", [100, 0, 33], 0, 2, 2, 256, 0, 5.0, False, False),
+]
+
+
+def make(dtype, lens, pad, Hq, Hkv, D, softcap, sink, fused, seed=0):
+    g = torch.Generator().manual_seed(seed)
+    rows, dt, sig = sum(lens) + pad, TDT[dtype], 2.0 if softcap else 1.0
+    qkv = torch.randn(rows, Hq + 2 * Hkv, D, generator=g)
+    qkv[:, :Hq + Hkv] *= sig
+    qkv = qkv.to(dt).to(DEV)
+    q, k, v = qkv[:, :Hq], qkv[:, Hq:Hq + Hkv], qkv[:, Hq + Hkv:]
+    if not fused:
+        q, k, v = q.contiguous(), k.contiguous(), v.contiguous()
+    dO = torch.randn(rows, Hq, D, generator=g).to(dt).to(DEV)
+    sk = torch.tensor(np.linspace(-0.5, 3.0, Hq), dtype=torch.float32, device=DEV) if sink else None
+    cu = torch.tensor([0] + list(np.cumsum(lens)), dtype=torch.int32, device=DEV)
+    return q, k, v, dO, sk, cu
+
+
+def raw(q, k, v, dO, sk, cu, W, C, clear, fill=float("nan")):
+    """Both calls through the C ABI, outputs pre-filled, workspaces full of 0xFF."""
+    rows, Hq, D = q.shape
+    Hkv, n, dt, sc = k.shape[1], cu.numel() - 1, fa.dtype_code(q.dtype), 1.0 / math.sqrt(q.shape[2])
+
+    def filled(*shape, dtype=q.dtype):
+        return torch.full(shape, fill, dtype=dtype, device=DEV)
+    o, lse = filled(rows, Hq, D), filled(Hq, rows, dtype=torch.float32)
+    dq, dk, dv = filled(rows, Hq, D), filled(rows, Hkv, D), filled(rows, Hkv, D)
+    ds = filled(Hq, dtype=torch.float32) if sk is not None else None
+    st = (q.stride(0) if rows > 1 else Hq * D, *(x.stride(0) if rows > 1 else Hkv * D for x in (k, v)))
+    for back in (False, True):
+        size = fa.forge_attn_varlen_bwd_workspace_size if back else fa.forge_attn_varlen_fwd_workspace_size
+        ws = torch.full((size(n, rows, Hq, Hkv, D, dt),), 255, dtype=torch.uint8, device=DEV)
+        if back:
+            s = fa.forge_attn_varlen_bwd(q, k, v, o, lse, dO, dq, dk, dv, cu, n, rows, Hq, Hkv, D, *st, sc, W, C, sk,
+                                         ds, clear, dt, ws, ws.numel())
+        else:
+            s = fa.forge_attn_varlen_fwd(q, k, v, o, lse, cu, n, rows, Hq, Hkv, D, *st, sc, W, C, sk, clear, dt, ws,
+                                         ws.numel())
+        assert s == fa.FORGE_OK, fa.forge_attn_status_string(s)
+    torch.cuda.synchronize()
+    assert fa.forge_attn_check() == fa.FORGE_OK
+    return o, lse, dq, dk, dv, ds
+
+
+def roundings(q, k, v, dO, sk, W, C):
+    """Element-wise bounds on the bf16 call's error for one sequence ([T, H, D] tensors): a bf16 rounding
+    is off by at most u = 2^-8 of the value, and the kernels round P and dS (scale included) before
+    their products and each output once. With |.| the terms' absolute values,
+      |err o|  <= u |o| + u sum_j P_ij |v_j|                                     (P)
+      |err dv| <= u |dv| + u sum_i P_ij |dO_i|                                   (P)
+      |err Delta_i| <= u sum_d |dO_id o_id|     (the reference's Delta is taken from o rounded to bf16; the
+                       call's o is a rounding of a value that differs by the P term above)
+                       + sum_d |dO_id| (u sum_j P_ij |v_jd| + u |o_id|)
+      |err dS_ij| <= u |dS_ij| + scale P_ij t'_ij |err Delta_i|,  and dq, dk sum those against |k|, |q|,
+    plus u of the output. f32 accumulation and the exponential (4e-6) are smaller by 2^-9 and are
+    covered by the factor 1.05. Returns bounds for o, dq, dk, dv."""
+    u, (T, Hq, D), Hkv = 2.0 ** -8, q.shape, k.shape[1]
+    qh, kh, vh, dh = (x.double().transpose(0, 1) for x in (q, k, v, dO))
+    kh, vh = (x.repeat_interleave(Hq // Hkv, 0) for x in (kh, vh))
+    s = qh @ kh.transpose(1, 2) / math.sqrt(D)
+    slope = torch.ones_like(s)
+    if C:
+        s = C * torch.tanh(s / C)
+        slope = 1 - (s / C) ** 2
+    i = torch.arange(T, device=q.device)
+    see = (i[None] <= i[:, None]) & ((i[None] > i[:, None] - W) if W else True)
+    s = s.masked_fill(~see, -math.inf)
+    if sk is not None:
+        s = torch.cat([s, sk.double()[:, None, None].expand(Hq, T, 1)], 2)
+    p = torch.softmax(s, 2)[:, :, :T]
+    o, pv = p @ vh, p @ vh.abs()
+    ds = p * (dh @ vh.transpose(1, 2) - (dh * o).sum(2, keepdim=True)) * slope / math.sqrt(D)
+    edelta = (dh.abs() * (2 * u * o.abs() + u * pv)).sum(2, keepdim=True)
+    eds = u * ds.abs() + p * slope * edelta / math.sqrt(D)
+
+    def group(x):
+        return x.view(Hkv, Hq // Hkv, T, D).sum(1)
+    bound = (u * o.abs() + u * pv, u * (ds @ kh).abs() + eds @ kh.abs(),
+             u * group(ds.transpose(1, 2) @ qh).abs() + group(eds.transpose(1, 2) @ qh.abs()),
+             u * group(p.transpose(1, 2) @ dh).abs() + u * group(p.transpose(1, 2) @ dh.abs()))
+    return [1.05 * x.cpu().numpy() for x in bound]
+
+
+def close(name, got, ref, dtype, bound):
+    if dtype == "f32":
+        return check_close(name, got, ref, dtype)
+    got = got.double().cpu().numpy()
+    assert np.all(np.isfinite(got)), name
+    err, tol = np.abs(got - ref), np.maximum(2e-2 + 1e-2 * np.abs(ref), bound)
+    assert np.all(err <= tol), (name, float((err / tol).max()))
+
+
+def compare(dtype, lens, q, k, v, dO, sk, W, C, got):
+    o, lse, dq, dk, dv, ds = got
+    Hq, D = q.shape[1:]
+    sc, row = 1.0 / math.sqrt(D), 0
+    rds, mag = np.zeros(Hq), np.zeros(Hq)
+    host = None if sk is None else sk.cpu()
+    for n in lens:
+        if n == 0:
+            continue
+        at = slice(row, row + n)
+        row += n
+        qs, ks, vs, ds_ = (x[at].transpose(0, 1)[None].cpu() for x in (q, k, v, dO))
+        ro, rl, _ = oracle.attn_fwd_ext(qs, ks, vs, sc, W, C, sink=host)
+        rdq, rdk, rdv, rs, delta, rlse = oracle.attn_bwd_ext(qs, ks, vs, ds_, sc, W, C, sink=host, o_round=dtype)
+        bounds = roundings(q[at], k[at], v[at], dO[at], sk, W, C) if dtype == "bf16" else [None] * 4
+        for name, x, r, bound in zip(("o", "dq", "dk", "dv"), (o, dq, dk, dv), (ro, rdq, rdk, rdv), bounds):
+            close(f"{name}[{at}]", x[at].transpose(0, 1), r[0], dtype, bound)
+        check_close(f"lse[{at}]", lse[:, at][None].cpu(), rl, dtype)
+        if sk is not None:
+            rds += rs
+            mag += np.abs(np.exp(host.double().numpy()[None, :, None] - rlse) * delta).sum(axis=(0, 2))
+    if sk is not None:  # a sum of terms of both signs: the bar applies to their magnitude (test_ext_gpu.py)
+        err = np.abs(ds.double().cpu().numpy() - rds)
+        assert np.all(err <= (1e-4 * (1 + mag) if dtype == "f32" else 2e-2 + 1e-2 * mag)), (err, mag)
+
+
+@pytest.mark.parametrize("case", CASES, ids=[c[0] for c in CASES])
+def test_matches_oracle_per_sequence(case):
+    _, dtype, lens, pad, Hq, Hkv, D, W, C, sink, fused = case
+    q, k, v, dO, sk, cu = make(dtype, lens, pad, Hq, Hkv, D, C, sink, fused)
+    total = sum(lens)
+    if pad:  # rows behind the last sequence are not read
+        for x in (q, k, v, dO):
+            x[total:] = float("nan")
+    got = raw(q, k, v, dO, sk, cu, W, C, clear=0)
+    compare(dtype, lens, q, k, v, dO, sk, W, C, got)
+    o, lse, dq, dk, dv, _ = got
+    for x in (o, dq, dk, dv, lse.t()):  # ... and their outputs left as they were
+        assert bool(torch.isnan(x[total:]).all())
+    o, lse, dq, dk, dv, _ = raw(q, k, v, dO, sk, cu, W, C, clear=1)
+    assert torch.equal(o[:total], got[0][:total]) and torch.equal(lse[:, :total], got[1][:, :total])
+    assert torch.equal(dk[:total], got[3][:total]) and torch.equal(dv[:total], got[4][:total])
+    for x in (o, dq, dk, dv):
+        assert not bool(x[total:].any())
+    assert bool((lse[:, total:] == -math.inf).all())
+
+
+@pytest.mark.parametrize("dtype,D,Hq,Hkv", [("bf16", 128, 4, 2), ("bf16", 64, 3, 3), ("bf16", 256, 2, 1),
+                                             ("f32", 64, 2, 1)])
+@pytest.mark.parametrize("poison", [float("nan"), float("inf"), -3.0e38])
+def test_one_sequences_values_stay_in_it(dtype, D, Hq, Hkv, poison):
+    lens = [100, 200, 61, 300, 5]
+    q, k, v, dO, _, cu = make(dtype, lens, 0, Hq, Hkv, D, 0.0, False, False)
+    clean = raw(q, k, v, dO, None, cu, 0, 0.0, 0)
+    rest = torch.ones(sum(lens), dtype=torch.bool, device=DEV)
+    for b in (1, 3):  # between clean sequences whose tiles run into them
+        rest[int(cu[b]):int(cu[b + 1])] = False
+        for x in (q, k, v, dO):
+            x[int(cu[b]):int(cu[b + 1])] = poison
+    o, lse, dq, dk, dv, _ = raw(q, k, v, dO, None, cu, 0, 0.0, 0)
+    assert torch.equal(o[rest], clean[0][rest]) and torch.equal(lse[:, rest], clean[1][:, rest])
+    assert torch.equal(dk[rest], clean[3][rest]) and torch.equal(dv[rest], clean[4][rest])
+    if dtype == "f32":
+        assert torch.equal(dq[rest], clean[2][rest])
+    else:  # f32 atomics in any order, then one rounding
+        check_close("dq", dq[rest], clean[2][rest].double().cpu().numpy(), dtype)
+
+
+@pytest.mark.parametrize("D,T", [(128, 700), (64, 512), (256, 300)])
+def test_equal_lengths_give_the_dense_call(D, T):
+    B, Hq, Hkv = 3, 4, 2
+    q, k, v, dO, _, cu = make("bf16", [T] * B, 0, Hq, Hkv, D, 0.0, False, False)
+    o, lse, dq, dk, dv, _ = raw(q, k, v, dO, None, cu, 0, 0.0, 0)
+
+    def dense(x):
+        return x.view(B, T, -1, D).transpose(1, 2).contiguous()
+    do, dl = fa.attention_fwd(dense(q), dense(k), dense(v))
+    ddq, ddk, ddv = fa.attention_bwd(dense(q), dense(k), dense(v), do, dl, dense(dO))
+    # the same kernels on the same tiles in the same order
+    assert torch.equal(dense(o), do) and torch.equal(lse.view(Hq, B, T).transpose(0, 1), dl)
+    if not (D == 128 and T > 512):
+        assert torch.equal(dense(dk), ddk) and torch.equal(dense(dv), ddv)
+    check_close("dk", dense(dk), ddk.double().cpu().numpy(), "bf16")
+    check_close("dq", dense(dq), ddq.double().cpu().numpy(), "bf16")
+
+
+def test_window_of_the_longest_sequence_is_no_window():
+    lens = [200, 90]
+    q, k, v, dO, _, cu = make("bf16", lens, 0, 2, 1, 128, 0.0, False, False)
+    a, b = raw(q, k, v, dO, None, cu, 0, 0.0, 0), raw(q, k, v, dO, None, cu, 1 << 30, 0.0, 0)
+    c = raw(q, k, v, dO, None, cu, 200, 0.0, 0)
+    for i in (0, 1, 3, 4):
+        assert torch.equal(a[i], b[i]) and torch.equal(a[i], c[i])
+
+
+@pytest.mark.parametrize("cu", [[1, 5, 10], [0, 6, 4, 10], [0, 5, 11], [0, -1, 10], [0, 10, 0, 10]])
+def test_bad_lengths_are_reported_and_nothing_is_computed(cu):
+    q, k, v, dO, _, _ = make("bf16", [10], 0, 2, 1, 128, 0.0, False, False)
+    bad = torch.tensor(cu, dtype=torch.int32, device=DEV)
+    n, sc, dt = len(cu) - 1, 0.1, fa.FORGE_DTYPE_BF16
+    o, lse = torch.full_like(q, 7.0), torch.full((2, 10), 7.0, device=DEV)
+    ws = torch.empty(fa.forge_attn_varlen_fwd_workspace_size(n, 10, 2, 1, 128, dt), dtype=torch.uint8, device=DEV)
+    assert fa.forge_attn_varlen_fwd(q, k, v, o, lse, bad, n, 10, 2, 1, 128, 256, 128, 128, sc, 0, 0.0, None, 0, dt, ws,
+                                    ws.numel()) == fa.FORGE_OK
+    assert fa.forge_attn_check() == fa.FORGE_ERR_INVALID_ARG and fa.forge_attn_check() == fa.FORGE_OK
+    assert bool((o == 7.0).all()) and bool((lse == 7.0).all())
+    dq, dk, dv = (torch.full_like(x, 7.0) for x in (q, k, v))
+    ws = torch.empty(fa.forge_attn_varlen_bwd_workspace_size(n, 10, 2, 1, 128, dt), dtype=torch.uint8, device=DEV)
+    assert fa.forge_attn_varlen_bwd(q, k, v, o, lse, dO, dq, dk, dv, bad, n, 10, 2, 1, 128, 256, 128, 128, sc, 0, 0.0,
+                                    None, None, 0, dt, ws, ws.numel()) == fa.FORGE_OK
+    assert fa.forge_attn_check() == fa.FORGE_ERR_INVALID_ARG
+    assert all(bool((x == 7.0).all()) for x in (dq, dk, dv))
+
+
+def test_all_lengths_zero():
+    q, k, v, dO, _, _ = make("bf16", [4], 0, 2, 1, 64, 0.0, False, False)
+    cu = torch.zeros(4, dtype=torch.int32, device=DEV)
+    o, lse = fa.attention_varlen_fwd(q, k, v, cu)
+    assert not bool(o.any()) and bool((lse == -math.inf).all())
+    assert all(not bool(x.any()) for x in fa.attention_varlen_bwd(q, k, v, o, lse, dO, cu))
+    assert fa.forge_attn_check() == fa.FORGE_OK
+
+
+def test_more_sequences_than_the_schedule_holds_at_once():
+    lens = [(i * 7) % 5 for i in range(2500)]
+    q, k, v, dO, _, cu = make("bf16", lens, 0, 2, 1, 64, 0.0, False, False)
+    compare("bf16", lens, q, k, v, dO, None, 0, 0.0, raw(q, k, v, dO, None, cu, 0, 0.0, 0))
+
+
+def test_autograd_gradients_match_the_formula_and_differences():
+    # f32: the library's gradient of sum(o * c) against f64 autograd of the definition and against
+    # central differences; a step h has a truncation error ~h^2 and a rounding error ~eps |f| / h
+    lens, Hq, Hkv, D, W, C = [30, 0, 70], 4, 2, 64, 20, 5.0
+    q, k, v, c, sk, cu = make("f32", lens, 2, Hq, Hkv, D, 0.0, True, True)
+    leaves = [x.clone().requires_grad_() for x in (q, k, v, sk)]
+    o = fa.attention_varlen(*leaves[:3], cu, window=W, softcap=C, sink=leaves[3])
+    grads = torch.autograd.grad(o, leaves, c.transpose(0, 1).contiguous().transpose(0, 1))  # a strided dO
+
+    def definition(q, k, v, sk):
+        out, row = torch.zeros_like(q), 0
+        for n in lens:
+            i = torch.arange(n, device=DEV)
+            see = (i[None] <= i[:, None]) & (i[None] > i[:, None] - W)
+            for h in range(Hq):
+                s = C * torch.tanh(q[row:row + n, h] @ k[row:row + n, h // 2].T / math.sqrt(D) / C)
+                s = torch.cat([s.masked_fill(~see, -math.inf), sk[h].expand(n, 1)], 1)
+                out[row:row + n, h] = torch.softmax(s, 1)[:, :n] @ v[row:row + n, h // 2]
+            row += n
+        return out
+    wide = [x.detach().double().requires_grad_() for x in leaves]
+    for name, a, b in zip(("q", "k", "v", "sink"), grads, torch.autograd.grad(definition(*wide), wide, c.double())):
+        check_close("d" + name, a, b.cpu().numpy(), "f32")
+    h, g = 1e-4, torch.Generator(device=DEV).manual_seed(1)
+    with torch.no_grad():
+        for i, a in enumerate(grads):
+            d = torch.randn(a.shape, generator=g, device=DEV, dtype=torch.float64)
+            up, down = ([x + (s * h * d if j == i else 0) for j, x in enumerate(wide)] for s in (1, -1))
+            diff = float(((definition(*up) - definition(*down)) * c.double()).sum() / (2 * h))
+            got, size = float((a.double() * d).sum()), float((a.double().abs() * d.abs()).sum())
+            assert abs(got - diff) <= 1e-4 * size + 1e-4, (i, got, diff)
+
+
+def test_gradients_of_shared_heads_and_repeated_inputs():
+    # k and v the same tensor, broadcast over query heads: both gradients land in one leaf
+    q, k, _, dO, _, cu = make("f32", [50, 21], 0, 4, 1, 64, 0.0, False, False)
+    x = k.clone().requires_grad_()
+    (g,) = torch.autograd.grad(fa.attention_varlen(q, x, x, cu), x, dO)
+    o, lse = fa.attention_varlen_fwd(q, k, k, cu)
+    _, dk, dv = fa.attention_varlen_bwd(q, k, k, o, lse, dO, cu)
+    assert torch.equal(g, dk + dv)
+
+
+def test_captured_calls_follow_the_lengths():
+    lens_a, lens_b = [100, 300, 112], [257, 1, 200]
+    q, k, v, dO, _, cu = make("bf16", lens_a, 0, 4, 2, 128, 0.0, False, False)
+    rows = 512
+
+    def step():
+        o, lse = fa.attention_varlen_fwd(q, k, v, cu)
+        return (o, lse, *fa.attention_varlen_bwd(q, k, v, o, lse, dO, cu))
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step()
+    torch.cuda.current_stream().wait_stream(side)
+    graphs = []
+    for _ in range(2):  # two graphs, each with workspaces of its own pool
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            out = step()
+        graphs.append((graph, out))
+    for lens in (lens_a, lens_b):
+        cu.copy_(torch.tensor([0] + list(np.cumsum(lens)), dtype=torch.int32))
+        want = step()
+        for graph, out in graphs:
+            graph.replay()
+        torch.cuda.synchronize()
+        total = sum(lens)
+        for graph, out in graphs:
+            for i in (0, 3, 4):
+                assert torch.equal(out[i], want[i]), i
+            assert torch.equal(out[1], want[1])
+            check_close("dq", out[2][:total], want[2][:total].double().cpu().numpy(), "bf16")
+        assert total <= rows
+    assert fa.forge_attn_check() == fa.FORGE_OK
+
+
+def test_calls_on_two_streams_at_once():
+    sets = [make("bf16", lens, 0, 4, 2, 128, 0.0, False, False, seed=i)
+            for i, lens in enumerate(([900, 100], [33] * 20, [1200], [400, 1, 400]))]
+    want = [fa.attention_varlen_fwd(q, k, v, cu) for q, k, v, dO, _, cu in sets]
+    grads = [fa.attention_varlen_bwd(q, k, v, o, lse, dO, cu) for (q, k, v, dO, _, cu), (o, lse) in zip(sets, want)]
+    torch.cuda.synchronize()
+    streams, got = [torch.cuda.Stream() for _ in sets], []
+    for _ in range(3):
+        for s, (q, k, v, dO, _, cu) in zip(streams, sets):
+            # one by the argument, one by the current stream, one by the raw handle
+            o, lse = fa.attention_varlen_fwd(q, k, v, cu, stream=s)
+            with torch.cuda.stream(s):
+                got.append((o, lse, *fa.attention_varlen_bwd(q, k, v, o, lse, dO, cu, stream=s.cuda_stream)))
+    torch.cuda.synchronize()
+    for i, x in enumerate(got):
+        (o, lse), (dq, dk, dv) = want[i % 4], grads[i % 4]
+        assert torch.equal(x[0], o) and torch.equal(x[1], lse) and torch.equal(x[3], dk) and torch.equal(x[4], dv)
+    assert fa.forge_attn_check() == fa.FORGE_OK
