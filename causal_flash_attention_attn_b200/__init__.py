@@ -106,11 +106,11 @@ def library():
     L.forge_attn_bwd_finalize.restype = i
     L.forge_attn_varlen_fwd_workspace_size.argtypes = [i, i, i, i, i, i]
     L.forge_attn_varlen_fwd_workspace_size.restype = st
-    L.forge_attn_varlen_fwd.argtypes = ([vp] * 6 + [i] * 5 + [st] * 3 + [f, i, f, vp, i, i, vp, st, vp])
+    L.forge_attn_varlen_fwd.argtypes = ([vp] * 7 + [i] * 5 + [st] * 3 + [f, i, f, vp, i, i, vp, st, vp])
     L.forge_attn_varlen_fwd.restype = i
     L.forge_attn_varlen_bwd_workspace_size.argtypes = [i, i, i, i, i, i]
     L.forge_attn_varlen_bwd_workspace_size.restype = st
-    L.forge_attn_varlen_bwd.argtypes = ([vp] * 10 + [i] * 5 + [st] * 3 + [f, i, f, vp, vp, i, i, vp, st, vp])
+    L.forge_attn_varlen_bwd.argtypes = ([vp] * 11 + [i] * 5 + [st] * 3 + [f, i, f, vp, vp, i, i, vp, st, vp])
     L.forge_attn_varlen_bwd.restype = i
     L.forge_attn_decode_paged_workspace_size.argtypes = [i, i, i, i, i]
     L.forge_attn_decode_paged_workspace_size.restype = st
@@ -255,10 +255,11 @@ def forge_attn_varlen_fwd_workspace_size(num_seqs, rows, Hq, Hkv, D, dtype) -> i
     return int(library().forge_attn_varlen_fwd_workspace_size(num_seqs, rows, Hq, Hkv, D, int(dtype)))
 
 
-def forge_attn_varlen_fwd(q, k, v, o, lse, cu_seqlens, num_seqs, rows, Hq, Hkv, D, q_stride, k_stride, v_stride, scale,
-                          window, softcap, sink, clear_tail, dtype, workspace, workspace_bytes, stream=None) -> int:
-    return library().forge_attn_varlen_fwd(_ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(lse), _ptr(cu_seqlens), num_seqs,
-                                           rows, Hq, Hkv, D, int(q_stride), int(k_stride), int(v_stride), float(scale),
+def forge_attn_varlen_fwd(q, k, v, o, o_res, lse, cu_seqlens, num_seqs, rows, Hq, Hkv, D, q_stride, k_stride, v_stride,
+                          scale, window, softcap, sink, clear_tail, dtype, workspace, workspace_bytes,
+                          stream=None) -> int:
+    return library().forge_attn_varlen_fwd(_ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(o_res), _ptr(lse),
+                                           _ptr(cu_seqlens), num_seqs, rows, Hq, Hkv, D, int(q_stride), int(k_stride), int(v_stride), float(scale),
                                            int(window), float(softcap), _ptr(sink), int(clear_tail), int(dtype),
                                            _ptr(workspace), int(workspace_bytes), _stream(stream))
 
@@ -267,10 +268,10 @@ def forge_attn_varlen_bwd_workspace_size(num_seqs, rows, Hq, Hkv, D, dtype) -> i
     return int(library().forge_attn_varlen_bwd_workspace_size(num_seqs, rows, Hq, Hkv, D, int(dtype)))
 
 
-def forge_attn_varlen_bwd(q, k, v, o, lse, dO, dq, dk, dv, cu_seqlens, num_seqs, rows, Hq, Hkv, D, q_stride, k_stride,
+def forge_attn_varlen_bwd(q, k, v, o, o_res, lse, dO, dq, dk, dv, cu_seqlens, num_seqs, rows, Hq, Hkv, D, q_stride, k_stride,
                           v_stride, scale, window, softcap, sink, dsink, clear_tail, dtype, workspace, workspace_bytes,
                           stream=None) -> int:
-    return library().forge_attn_varlen_bwd(_ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(lse), _ptr(dO), _ptr(dq), _ptr(dk),
+    return library().forge_attn_varlen_bwd(_ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(o_res), _ptr(lse), _ptr(dO), _ptr(dq), _ptr(dk),
                                            _ptr(dv), _ptr(cu_seqlens), num_seqs, rows, Hq, Hkv, D, int(q_stride),
                                            int(k_stride), int(v_stride), float(scale), int(window), float(softcap),
                                            _ptr(sink), _ptr(dsink), int(clear_tail), int(dtype), _ptr(workspace),
@@ -579,11 +580,13 @@ def _check_packed(what, q, k, v, cu_seqlens, sink):
     return rows, Hq, Hkv, D, strides
 
 
-def attention_varlen_fwd(q, k, v, cu_seqlens, scale=None, window=0, softcap=0.0, stream=None, *, sink=None):
+def attention_varlen_fwd(q, k, v, cu_seqlens, scale=None, window=0, softcap=0.0, stream=None, *, sink=None,
+                         return_residual=False):
     """Causal attention over packed sequences: q [rows,Hq,D], k, v [rows,Hkv,D] (bf16 or f32; their rows
     may lie apart), cu_seqlens int32 [num_seqs + 1] on the device, from 0. Returns (o [rows,Hq,D], lse
-    [Hq,rows]). Rows behind the last sequence get zeros, lse -inf there. Nothing synchronises; bad
-    cu_seqlens are reported by forge_attn_check."""
+    [Hq,rows]), or (o, lse, o_res) with return_residual: o's rounding residual for the backward (None in
+    f32). Rows behind the last sequence get zeros, lse -inf there. Nothing synchronises; bad cu_seqlens
+    are reported by forge_attn_check."""
     import torch
     what = "attention_varlen_fwd"
     rows, Hq, Hkv, D, (qs, ks, vs) = _check_packed(what, q, k, v, cu_seqlens, sink)
@@ -591,25 +594,27 @@ def attention_varlen_fwd(q, k, v, cu_seqlens, scale=None, window=0, softcap=0.0,
     dt, n = dtype_code(q.dtype), cu_seqlens.numel() - 1
     with _scope(q.device, stream):
         o = torch.empty((rows, Hq, D), dtype=q.dtype, device=q.device)
+        o_res = torch.empty_like(o) if return_residual and dt == FORGE_DTYPE_BF16 else None
         lse = torch.empty((Hq, rows), dtype=torch.float32, device=q.device)
         nbytes = forge_attn_varlen_fwd_workspace_size(n, rows, Hq, Hkv, D, dt)
         ws = torch.empty(nbytes, dtype=torch.uint8, device=q.device)
-        s = forge_attn_varlen_fwd(q, k, v, o, lse, cu_seqlens, n, rows, Hq, Hkv, D, qs, ks, vs, scale, window, softcap,
-                                  sink, True, dt, ws, nbytes)
+        s = forge_attn_varlen_fwd(q, k, v, o, o_res, lse, cu_seqlens, n, rows, Hq, Hkv, D, qs, ks, vs, scale, window,
+                                  softcap, sink, True, dt, ws, nbytes)
     if s != FORGE_OK:
         raise ForgeError(s, "forge_attn_varlen_fwd")
-    return o, lse
+    return (o, lse, o_res) if return_residual else (o, lse)
 
 
 def attention_varlen_bwd(q, k, v, o, lse, dO, cu_seqlens, scale=None, window=0, softcap=0.0, stream=None, *,
-                         sink=None):
-    """Backward of attention_varlen_fwd (its o and lse; dO contiguous). Returns (dq, dk, dv), or (dq, dk,
-    dv, dsink [Hq]) with a sink; zeros in the rows behind the last sequence."""
+                         sink=None, o_res=None):
+    """Backward of attention_varlen_fwd (its o and lse, and o_res if it returned one; dO contiguous).
+    Returns (dq, dk, dv), or (dq, dk, dv, dsink [Hq]) with a sink; zeros in the rows behind the last
+    sequence."""
     import torch
     what = "attention_varlen_bwd"
     rows, Hq, Hkv, D, (qs, ks, vs) = _check_packed(what, q, k, v, cu_seqlens, sink)
     _check_dense(what, q.device, o=(o, q.dtype, (rows, Hq, D)), lse=(lse, torch.float32, (Hq, rows)),
-                 dO=(dO, q.dtype, (rows, Hq, D)))
+                 o_res=(o_res, q.dtype, (rows, Hq, D)), dO=(dO, q.dtype, (rows, Hq, D)))
     scale = 1.0 / math.sqrt(D) if scale is None else scale
     dt, n = dtype_code(q.dtype), cu_seqlens.numel() - 1
     with _scope(q.device, stream):
@@ -617,8 +622,8 @@ def attention_varlen_bwd(q, k, v, o, lse, dO, cu_seqlens, scale=None, window=0, 
         dsink = torch.empty((Hq,), dtype=torch.float32, device=q.device) if sink is not None else None
         nbytes = forge_attn_varlen_bwd_workspace_size(n, rows, Hq, Hkv, D, dt)
         ws = torch.empty(nbytes, dtype=torch.uint8, device=q.device)
-        s = forge_attn_varlen_bwd(q, k, v, o, lse, dO, dq, dk, dv, cu_seqlens, n, rows, Hq, Hkv, D, qs, ks, vs, scale,
-                                  window, softcap, sink, dsink, True, dt, ws, nbytes)
+        s = forge_attn_varlen_bwd(q, k, v, o, o_res, lse, dO, dq, dk, dv, cu_seqlens, n, rows, Hq, Hkv, D, qs, ks, vs,
+                                  scale, window, softcap, sink, dsink, True, dt, ws, nbytes)
     if s != FORGE_OK:
         raise ForgeError(s, "forge_attn_varlen_bwd")
     return (dq, dk, dv, dsink) if sink is not None else (dq, dk, dv)
@@ -635,15 +640,18 @@ def _attention_varlen_function():
         class ForgeAttentionVarlen(torch.autograd.Function):
             @staticmethod
             def forward(ctx, q, k, v, cu_seqlens, sink, scale, window, softcap):
-                o, lse = attention_varlen_fwd(q, k, v, cu_seqlens, scale, window, softcap, sink=sink)
-                ctx.save_for_backward(q, k, v, o, lse, cu_seqlens, sink)
+                if not any(ctx.needs_input_grad):
+                    return attention_varlen_fwd(q, k, v, cu_seqlens, scale, window, softcap, sink=sink)[0]
+                o, lse, o_res = attention_varlen_fwd(q, k, v, cu_seqlens, scale, window, softcap, sink=sink,
+                                                     return_residual=True)
+                ctx.save_for_backward(q, k, v, o, o_res, lse, cu_seqlens, sink)
                 ctx.args = (scale, window, softcap)
                 return o
 
             @staticmethod
             def backward(ctx, dO):
-                q, k, v, o, lse, cu_seqlens, sink = ctx.saved_tensors
-                g = attention_varlen_bwd(q, k, v, o, lse, dO.contiguous(), cu_seqlens, *ctx.args, sink=sink)
+                q, k, v, o, o_res, lse, cu_seqlens, sink = ctx.saved_tensors
+                g = attention_varlen_bwd(q, k, v, o, lse, dO.contiguous(), cu_seqlens, *ctx.args, sink=sink, o_res=o_res)
                 return g[0], g[1], g[2], None, (g[3] if sink is not None else None), None, None, None
 
         _attention_varlen_fn = ForgeAttentionVarlen

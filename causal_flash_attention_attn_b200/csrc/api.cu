@@ -512,7 +512,7 @@ forge_status run_plan(const VarArgs &a, const VarSched &v, bool backward, void *
     return launch_pdl(varlen_plan, dim3(clear ? 33 : 1), dim3(kPlanThreads), 0, a.st, p);
 }
 
-FwdParams var_fwd_params(const VarArgs &a, const VarSched &v, void *o, float *lse) {
+FwdParams var_fwd_params(const VarArgs &a, const VarSched &v, void *o, void *o_res, float *lse) {
     FwdParams p = {};
     p.o = static_cast<__nv_bfloat16 *>(o);
     p.lse = lse;
@@ -523,11 +523,12 @@ FwdParams var_fwd_params(const VarArgs &a, const VarSched &v, void *o, float *ls
     p.cap_out = a.softcap * kLog2e;
     p.sink = a.sink;
     p.var = v;
+    p.o_res = static_cast<__nv_bfloat16 *>(o_res);
     return p;
 }
 
 template <int D>
-forge_status var_fwd_tc(const VarArgs &a, const VarSched &v, void *o, float *lse) {
+forge_status var_fwd_tc(const VarArgs &a, const VarSched &v, void *o, void *o_res, float *lse) {
     CUtensorMap mq, mk, mv, mo;
     if (!make_map_rows(&mq, a.q, D, a.rows, a.Hq, a.q_stride, 128) ||
         !make_map_rows(&mk, a.k, D, a.rows, a.Hkv, a.k_stride, 128) ||
@@ -536,7 +537,7 @@ forge_status var_fwd_tc(const VarArgs &a, const VarSched &v, void *o, float *lse
         t_last_cuda_error = "cuTensorMapEncodeTiled failed";
         return FORGE_ERR_CUDA;
     }
-    const FwdParams p = var_fwd_params(a, v, o, lse);
+    const FwdParams p = var_fwd_params(a, v, o, o_res, lse);
     const long long items = (long long)var_max_items(a.rows, a.num_seqs, v.unit) * a.Hq;
     if constexpr (D == 256) {
         using C = FwdTc<D>;
@@ -587,11 +588,12 @@ forge_status var_fwd_f32(const VarArgs &a, const VarSched &v, void *o, float *ls
 // The backward after the schedule: Delta (and the cleared accumulator), dsink, the
 // main kernels, dq.
 template <typename T_, int D>
-forge_status var_bwd(const VarArgs &a, const VarSched &v, const void *o, const float *lse, const void *dO, void *dq,
+forge_status var_bwd(const VarArgs &a, const VarSched &v, const void *o, const void *o_res, const float *lse, const void *dO, void *dq,
                      void *dk, void *dv, float *dsink, float *delta, float *acc) {
     const int items = var_max_items(a.rows, a.num_seqs, v.unit);
     forge_status s = launch_pdl(varlen_preprocess<T_, D>, dim3((unsigned)items * (unsigned)a.Hq), dim3(256), 0, a.st,
-                                static_cast<const T_ *>(o), static_cast<const T_ *>(dO), delta, acc, a.Hq, v);
+                                static_cast<const T_ *>(o), static_cast<const T_ *>(o_res), static_cast<const T_ *>(dO),
+                                delta, acc, a.Hq, v);
     if (s != FORGE_OK) return s;
     if (dsink != nullptr) {
         s = launch_pdl(varlen_sink_grad, dim3((unsigned)a.Hq), dim3(512), 0, a.st, lse, static_cast<const float *>(delta),
@@ -1189,7 +1191,7 @@ size_t forge_attn_varlen_bwd_workspace_size(int num_seqs, int rows, int Hq, int 
     return var_layout(num_seqs, rows, Hq, D, dtype, true).bytes;
 }
 
-forge_status forge_attn_varlen_fwd(const void *q, const void *k, const void *v, void *o, float *lse,
+forge_status forge_attn_varlen_fwd(const void *q, const void *k, const void *v, void *o, void *o_res, float *lse,
                                    const int *cu_seqlens, int num_seqs, int rows, int Hq, int Hkv, int D,
                                    size_t q_stride, size_t k_stride, size_t v_stride, float scale, int window,
                                    float softcap, const float *sink, int clear_tail, forge_dtype dtype,
@@ -1198,7 +1200,7 @@ forge_status forge_attn_varlen_fwd(const void *q, const void *k, const void *v, 
                  sink, dtype, static_cast<cudaStream_t>(stream)};
     forge_status s = check_var_args(a);
     if (s != FORGE_OK) return s;
-    if (!aligned16(o) || !aligned16(lse)) return FORGE_ERR_INVALID_ARG;
+    if (!aligned16(o) || !aligned16(lse) || (o_res != nullptr && !aligned16(o_res))) return FORGE_ERR_INVALID_ARG;
     if (workspace == nullptr || (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0 ||
         workspace_bytes < forge_attn_varlen_fwd_workspace_size(num_seqs, rows, Hq, Hkv, D, dtype))
         return FORGE_ERR_WORKSPACE;
@@ -1208,15 +1210,15 @@ forge_status forge_attn_varlen_fwd(const void *q, const void *k, const void *v, 
     const int heads[3] = {Hq, 0, 0};
     if ((s = run_plan(a, sched, false, tail, heads, lse, clear_tail != 0)) != FORGE_OK) return s;
     if (dtype == FORGE_DTYPE_BF16) {
-        FORGE_DISPATCH_D(D, return var_fwd_tc<kD>(a, sched, o, lse);)
+        FORGE_DISPATCH_D(D, return var_fwd_tc<kD>(a, sched, o, o_res, lse);)
     } else {
         FORGE_DISPATCH_D(D, return var_fwd_f32<kD>(a, sched, o, lse);)
     }
     return FORGE_ERR_UNSUPPORTED;
 }
 
-forge_status forge_attn_varlen_bwd(const void *q, const void *k, const void *v, const void *o, const float *lse,
-                                   const void *dO, void *dq, void *dk, void *dv, const int *cu_seqlens, int num_seqs,
+forge_status forge_attn_varlen_bwd(const void *q, const void *k, const void *v, const void *o, const void *o_res,
+                                   const float *lse, const void *dO, void *dq, void *dk, void *dv, const int *cu_seqlens, int num_seqs,
                                    int rows, int Hq, int Hkv, int D, size_t q_stride, size_t k_stride, size_t v_stride,
                                    float scale, int window, float softcap, const float *sink, float *dsink,
                                    int clear_tail, forge_dtype dtype, void *workspace, size_t workspace_bytes,
@@ -1227,7 +1229,9 @@ forge_status forge_attn_varlen_bwd(const void *q, const void *k, const void *v, 
     if (s != FORGE_OK) return s;
     if (!aligned16(o) || !aligned16(lse) || !aligned16(dO) || !aligned16(dq) || !aligned16(dk) || !aligned16(dv))
         return FORGE_ERR_INVALID_ARG;
+    if (o_res != nullptr && !aligned16(o_res)) return FORGE_ERR_INVALID_ARG;
     if (dsink != nullptr && (!aligned4(dsink) || !aligned4(sink))) return FORGE_ERR_INVALID_ARG;
+    if (dtype == FORGE_DTYPE_F32) o_res = nullptr;  // an f32 o has no residual
     if (workspace == nullptr || (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0 ||
         workspace_bytes < forge_attn_varlen_bwd_workspace_size(num_seqs, rows, Hq, Hkv, D, dtype))
         return FORGE_ERR_WORKSPACE;
@@ -1240,9 +1244,9 @@ forge_status forge_attn_varlen_bwd(const void *q, const void *k, const void *v, 
     const int heads[3] = {Hq, Hkv, Hkv};
     if ((s = run_plan(a, sched, true, tail, heads, nullptr, clear_tail != 0)) != FORGE_OK) return s;
     if (dtype == FORGE_DTYPE_BF16) {
-        FORGE_DISPATCH_D(D, return var_bwd<__nv_bfloat16, kD>(a, sched, o, lse, dO, dq, dk, dv, dsink, delta, acc);)
+        FORGE_DISPATCH_D(D, return var_bwd<__nv_bfloat16, kD>(a, sched, o, o_res, lse, dO, dq, dk, dv, dsink, delta, acc);)
     } else {
-        FORGE_DISPATCH_D(D, return var_bwd<float, kD>(a, sched, o, lse, dO, dq, dk, dv, dsink, delta, acc);)
+        FORGE_DISPATCH_D(D, return var_bwd<float, kD>(a, sched, o, o_res, lse, dO, dq, dk, dv, dsink, delta, acc);)
     }
     return FORGE_ERR_UNSUPPORTED;
 }

@@ -548,11 +548,23 @@ __global__ void __launch_bounds__(384, 1)
                     tmem_ld32(tO + c0, o);
                     tmem_ld_wait(o);
                     uint32_t w16[16];
+                    if (VAR && p.o_res != nullptr) {
+                        uint32_t lo16[16];
+                        o_pairs32(o, inv_l, w16, lo16);
+                        if (qi < I.T) {
+                            uint4 *dst = reinterpret_cast<uint4 *>(p.o_res + ((size_t)(I.row0 + qi) * p.Hq + I.bh) * D + c0);
 #pragma unroll
-                    for (int i = 0; i < 16; i++) {
-                        float a, bb;
-                        f2_split(f2_mul(f2_make(__uint_as_float(o[2 * i]), __uint_as_float(o[2 * i + 1])), inv2), a, bb);
-                        w16[i] = pack_bf16x2(a, bb);
+                            for (int i = 0; i < 4; i++)
+                                dst[i] = make_uint4(lo16[4 * i], lo16[4 * i + 1], lo16[4 * i + 2], lo16[4 * i + 3]);
+                        }
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < 16; i++) {
+                            float a, bb;
+                            f2_split(f2_mul(f2_make(__uint_as_float(o[2 * i]), __uint_as_float(o[2 * i + 1])), inv2), a,
+                                     bb);
+                            w16[i] = pack_bf16x2(a, bb);
+                        }
                     }
                     const uint32_t rowaddr = sO + (uint32_t)(c0 / 64) * C::CB + (uint32_t)row * 128u;
                     const uint32_t ch0 = (uint32_t)((c0 % 64) / 8);

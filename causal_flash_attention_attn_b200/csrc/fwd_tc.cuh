@@ -188,7 +188,24 @@ struct FwdParams {
     // packed sequences (the VAR kernels): o is [rows][Hq][D], lse [Hq][rows], B = 1
     // and T, num_qt unused (each item carries its sequence's length)
     VarSched var;
+    // VAR, may be nullptr: the rounding residual of o, bf16(o - bf16(o)), same layout.
+    // The backward's Delta = rowsum(dO * o) takes o + residual: with o's rounding
+    // alone it would carry an error of 2^-9 sum |dO o|, which exceeds dP - Delta where a
+    // row's softmax is peaked (simulated on 16 capped keys at sigma 2: dq and dk off by
+    // 0.0042 instead of 0.0024, of which 0.0023 are the roundings of dS and of dq, dk).
+    __nv_bfloat16 *o_res;
 };
+
+// 32 f32 values of o times f, as bf16 pairs (hi), and the residuals' pairs (lo)
+__device__ __forceinline__ void o_pairs32(const uint32_t (&o)[32], float f, uint32_t (&hi)[16], uint32_t (&lo)[16]) {
+#pragma unroll
+    for (int i = 0; i < 16; i++) {
+        const float a = __uint_as_float(o[2 * i]) * f, b = __uint_as_float(o[2 * i + 1]) * f;
+        hi[i] = pack_bf16x2(a, b);
+        const float2 h = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&hi[i]));
+        lo[i] = pack_bf16x2(a - h.x, b - h.y);
+    }
+}
 
 // VAR: packed sequences. The CTA's tile comes from the schedule (heads innermost),
 // the tensor maps cover [heads][rows][D] views of the packed tensors, and rows of
@@ -509,9 +526,20 @@ __global__ void __launch_bounds__(320, 1)
                 tmem_ld32(tmem + lane_base + C::COL_O + c0, o);
                 tmem_ld_wait(o);
                 uint32_t w[16];
+                if constexpr (VAR) {
+                    uint32_t lo16[16];
+                    o_pairs32(o, inv_l, w, lo16);
+                    if (p.o_res != nullptr && qi < T) {
+                        uint4 *dst = reinterpret_cast<uint4 *>(p.o_res + ((size_t)(row0 + qi) * p.Hq + bh) * DV + c0);
 #pragma unroll
-                for (int i = 0; i < 16; i++)
-                    w[i] = pack_bf16x2(__uint_as_float(o[2 * i]) * inv_l, __uint_as_float(o[2 * i + 1]) * inv_l);
+                        for (int i = 0; i < 4; i++)
+                            dst[i] = make_uint4(lo16[4 * i], lo16[4 * i + 1], lo16[4 * i + 2], lo16[4 * i + 3]);
+                    }
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 16; i++)
+                        w[i] = pack_bf16x2(__uint_as_float(o[2 * i]) * inv_l, __uint_as_float(o[2 * i + 1]) * inv_l);
+                }
                 if (qi < T) {
                     uint4 *dst = reinterpret_cast<uint4 *>(orow + c0);
 #pragma unroll

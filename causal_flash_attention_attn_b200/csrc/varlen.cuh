@@ -152,12 +152,13 @@ __global__ void __launch_bounds__(kPlanThreads) varlen_plan(const VarPlanParams 
     if (tid == 0) *p.count = min(total, p.max_items);
 }
 
-// Delta_i = rowsum(dO_i * o_i) of a tile of one head, and (acc != nullptr)
+// Delta_i = rowsum(dO_i * o_i) of a tile of one head (o + o_res, where the forward
+// wrote o's rounding residual), and (acc != nullptr)
 // the tile's rows of the padded dq accumulator set to zero. One block per (tile,
 // head), heads innermost; LPR lanes a row as in bwd_preprocess.
 template <typename T, int D>
-__global__ void __launch_bounds__(256) varlen_preprocess(const T *__restrict__ o, const T *__restrict__ dO,
-                                                         float *__restrict__ delta, float *__restrict__ acc, int Hq,
+__global__ void __launch_bounds__(256) varlen_preprocess(const T *__restrict__ o, const T *__restrict__ o_res,
+                                                         const T *__restrict__ dO, float *__restrict__ delta, float *__restrict__ acc, int Hq,
                                                          const VarSched var) {
     constexpr int LPR = D / 8 < 32 ? D / 8 : 32;  // lanes per row
     constexpr int RPB = 256 / LPR;                // rows per pass of the block
@@ -182,6 +183,12 @@ __global__ void __launch_bounds__(256) varlen_preprocess(const T *__restrict__ o
             float a[8], b[8];
             load8(o + at + c, a);
             load8(dO + at + c, b);
+            if (o_res != nullptr) {
+                float r[8];
+                load8(o_res + at + c, r);
+#pragma unroll
+                for (int i = 0; i < 8; i++) a[i] += r[i];
+            }
 #pragma unroll
             for (int i = 0; i < 8; i++) sum = fmaf(a[i], b[i], sum);
         }

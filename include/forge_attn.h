@@ -258,6 +258,10 @@ forge_status forge_attn_decode(const void *q, const void *k_cache, const void *v
  *    follows the lengths that cu_seqlens holds at each replay. Lengths that do not ascend from
  *    0, or that pass `rows`, are reported as FORGE_ERR_INVALID_ARG by the next
  *    forge_attn_check; nothing is computed then.
+ *  - o_res [rows][Hq][D] (dtype; may be NULL): the forward writes o's rounding residual,
+ *    o - bf16(o) as bf16, there, and the backward, given it, takes Delta from o + o_res. Without it
+ *    (NULL in the backward) Delta carries o's rounding, which shows in dq, dk and dsink where
+ *    rows attend to few keys. f32: neither written nor read.
  *  - sink, dsink: as in forge_attn_fwd_ext / forge_attn_bwd_ext. scale, window, softcap
  *    as in forge_attn_fwd (a window >= rows acts as off).
  *  - rows and num_seqs >= 1, num_seqs <= 2^20, (rows / 64 + num_seqs) * Hq < 2^30; the limits
@@ -269,14 +273,14 @@ forge_status forge_attn_decode(const void *q, const void *k_cache, const void *v
  * takes o and lse as forge_attn_varlen_fwd wrote them.
  */
 size_t forge_attn_varlen_fwd_workspace_size(int num_seqs, int rows, int Hq, int Hkv, int D, forge_dtype dtype);
-forge_status forge_attn_varlen_fwd(const void *q, const void *k, const void *v, void *o, float *lse,
+forge_status forge_attn_varlen_fwd(const void *q, const void *k, const void *v, void *o, void *o_res, float *lse,
                                    const int *cu_seqlens, int num_seqs, int rows, int Hq, int Hkv, int D,
                                    size_t q_stride, size_t k_stride, size_t v_stride, float scale, int window,
                                    float softcap, const float *sink, int clear_tail, forge_dtype dtype,
                                    void *workspace, size_t workspace_bytes, void *stream);
 size_t forge_attn_varlen_bwd_workspace_size(int num_seqs, int rows, int Hq, int Hkv, int D, forge_dtype dtype);
-forge_status forge_attn_varlen_bwd(const void *q, const void *k, const void *v, const void *o, const float *lse,
-                                   const void *dO, void *dq, void *dk, void *dv, const int *cu_seqlens, int num_seqs,
+forge_status forge_attn_varlen_bwd(const void *q, const void *k, const void *v, const void *o, const void *o_res,
+                                   const float *lse, const void *dO, void *dq, void *dk, void *dv, const int *cu_seqlens, int num_seqs,
                                    int rows, int Hq, int Hkv, int D, size_t q_stride, size_t k_stride, size_t v_stride,
                                    float scale, int window, float softcap, const float *sink, float *dsink,
                                    int clear_tail, forge_dtype dtype, void *workspace, size_t workspace_bytes,

@@ -16,7 +16,7 @@ INVALID, UNSUPPORTED, WORKSPACE = fa.FORGE_ERR_INVALID_ARG, fa.FORGE_ERR_UNSUPPO
 
 # ------------------------------------------------------------------ C ABI
 def varlen(backward, **kw):
-    a = dict(q=A, k=A, v=A, o=A, lse=A, dO=A, dq=A, dk=A, dv=A, cu=A, n=3, rows=500, Hq=4, Hkv=2, D=128, qs=None,
+    a = dict(q=A, k=A, v=A, o=A, res=None, lse=A, dO=A, dq=A, dk=A, dv=A, cu=A, n=3, rows=500, Hq=4, Hkv=2, D=128, qs=None,
              ks=None, vs=None, scale=0.1, window=0, softcap=0.0, sink=None, dsink=None, dtype=BF, ws=A, nbytes=None)
     a.update(kw)
     H, K, D = a["Hq"], a["Hkv"], a["D"]
@@ -24,10 +24,10 @@ def varlen(backward, **kw):
     size = fa.forge_attn_varlen_bwd_workspace_size if backward else fa.forge_attn_varlen_fwd_workspace_size
     nbytes = size(3, 500, 4, 2, 128, BF) if a["nbytes"] is None else a["nbytes"]
     if backward:
-        return fa.forge_attn_varlen_bwd(a["q"], a["k"], a["v"], a["o"], a["lse"], a["dO"], a["dq"], a["dk"], a["dv"],
-                                        a["cu"], a["n"], a["rows"], H, K, D, qs, ks, vs, a["scale"], a["window"],
+        return fa.forge_attn_varlen_bwd(a["q"], a["k"], a["v"], a["o"], a["res"], a["lse"], a["dO"], a["dq"], a["dk"],
+                                        a["dv"], a["cu"], a["n"], a["rows"], H, K, D, qs, ks, vs, a["scale"], a["window"],
                                         a["softcap"], a["sink"], a["dsink"], 1, a["dtype"], a["ws"], nbytes, 0)
-    return fa.forge_attn_varlen_fwd(a["q"], a["k"], a["v"], a["o"], a["lse"], a["cu"], a["n"], a["rows"], H, K, D, qs,
+    return fa.forge_attn_varlen_fwd(a["q"], a["k"], a["v"], a["o"], a["res"], a["lse"], a["cu"], a["n"], a["rows"], H, K, D, qs,
                                     ks, vs, a["scale"], a["window"], a["softcap"], a["sink"], 1, a["dtype"], a["ws"],
                                     nbytes, 0)
 
@@ -40,6 +40,7 @@ def varlen(backward, **kw):
     (dict(window=-1), INVALID), (dict(scale=0.0), INVALID), (dict(softcap=float("nan")), INVALID),
     (dict(q=0), INVALID), (dict(k=A + 8), INVALID), (dict(cu=0), INVALID), (dict(cu=A + 2), INVALID),
     (dict(o=A + 4), INVALID), (dict(lse=A + 4), INVALID), (dict(sink=A + 1), INVALID), (dict(dtype=7), INVALID),
+    (dict(res=A + 8), INVALID),
     (dict(qs=4 * 128 - 8), INVALID),                               # rows would overlap
     (dict(ks=2 * 128 + 4), INVALID),                               # not a multiple of 16 bytes
     (dict(vs=1 << 37), INVALID),

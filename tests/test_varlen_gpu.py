@@ -51,14 +51,15 @@ def make(dtype, lens, pad, Hq, Hkv, D, softcap, sink, fused, seed=0):
     return q, k, v, dO, sk, cu
 
 
-def raw(q, k, v, dO, sk, cu, W, C, clear, fill=float("nan")):
-    """Both calls through the C ABI, outputs pre-filled, workspaces full of 0xFF."""
+def raw(q, k, v, dO, sk, cu, W, C, clear, fill=float("nan"), res=False):
+    """Both calls through the C ABI, outputs pre-filled, workspaces full of 0xFF; res: with o's residual."""
     rows, Hq, D = q.shape
     Hkv, n, dt, sc = k.shape[1], cu.numel() - 1, fa.dtype_code(q.dtype), 1.0 / math.sqrt(q.shape[2])
 
     def filled(*shape, dtype=q.dtype):
         return torch.full(shape, fill, dtype=dtype, device=DEV)
     o, lse = filled(rows, Hq, D), filled(Hq, rows, dtype=torch.float32)
+    o_res = filled(rows, Hq, D) if res else None
     dq, dk, dv = filled(rows, Hq, D), filled(rows, Hkv, D), filled(rows, Hkv, D)
     ds = filled(Hq, dtype=torch.float32) if sk is not None else None
     st = (q.stride(0) if rows > 1 else Hq * D, *(x.stride(0) if rows > 1 else Hkv * D for x in (k, v)))
@@ -66,15 +67,22 @@ def raw(q, k, v, dO, sk, cu, W, C, clear, fill=float("nan")):
         size = fa.forge_attn_varlen_bwd_workspace_size if back else fa.forge_attn_varlen_fwd_workspace_size
         ws = torch.full((size(n, rows, Hq, Hkv, D, dt),), 255, dtype=torch.uint8, device=DEV)
         if back:
-            s = fa.forge_attn_varlen_bwd(q, k, v, o, lse, dO, dq, dk, dv, cu, n, rows, Hq, Hkv, D, *st, sc, W, C, sk,
-                                         ds, clear, dt, ws, ws.numel())
+            s = fa.forge_attn_varlen_bwd(q, k, v, o, o_res, lse, dO, dq, dk, dv, cu, n, rows, Hq, Hkv, D, *st, sc, W, C,
+                                         sk, ds, clear, dt, ws, ws.numel())
         else:
-            s = fa.forge_attn_varlen_fwd(q, k, v, o, lse, cu, n, rows, Hq, Hkv, D, *st, sc, W, C, sk, clear, dt, ws,
+            s = fa.forge_attn_varlen_fwd(q, k, v, o, o_res, lse, cu, n, rows, Hq, Hkv, D, *st, sc, W, C, sk, clear, dt, ws,
                                          ws.numel())
         assert s == fa.FORGE_OK, fa.forge_attn_status_string(s)
     torch.cuda.synchronize()
     assert fa.forge_attn_check() == fa.FORGE_OK
+    if res and dtype_is_bf16(q):  # hi + lo: what o's rounding lost is below half a unit of its last place
+        total = int(cu[-1])
+        assert bool((o_res[:total].float().abs() <= 2.0 ** -8 * o[:total].float().abs() + 1e-37).all())
     return o, lse, dq, dk, dv, ds
+
+
+def dtype_is_bf16(x):
+    return x.dtype == torch.bfloat16
 
 
 def roundings(q, k, v, dO, sk, W, C):
@@ -172,6 +180,37 @@ def test_matches_oracle_per_sequence(case):
     assert bool((lse[:, total:] == -math.inf).all())
 
 
+@pytest.mark.parametrize("case", [c for c in CASES if c[1] == "bf16"], ids=[c[0] for c in CASES if c[1] == "bf16"])
+def test_the_residual_of_o_takes_its_rounding_out_of_the_gradients(case):
+    """With o_res, Delta lacks o's rounding: dq and dk against the exact gradient, in the 2-norm. What is left is
+    the rounding of dS (at most u = 2^-8 of each term: u |dS| |K| in the 2-norm of independent roundings) and of
+    the outputs (u): 2 u relative, where the plain Delta may exceed it many times over (peaked rows). The
+    residual's own rounding leaves |err Delta_i| <= u^2 sum_d |dO_id o_id|, which reaches dq_i times
+    scale max |k| and dk times scale max |q| (`floor`, summed over the rows: all there is where the exact
+    gradient is 0, as in rows that see one key)."""
+    _, dtype, lens, pad, Hq, Hkv, D, W, C, sink, fused = case
+    q, k, v, dO, sk, cu = make(dtype, lens, pad, Hq, Hkv, D, C, sink, fused)
+    got = raw(q, k, v, dO, sk, cu, W, C, clear=0, res=True)
+    plain = raw(q, k, v, dO, sk, cu, W, C, clear=0)
+    assert torch.equal(got[0][:sum(lens)], plain[0][:sum(lens)]) and torch.equal(got[1][:, :sum(lens)], plain[1][:, :sum(lens)])
+    host, row, off, floor = None if sk is None else sk.cpu(), 0, np.zeros((2, 2)), np.zeros(2)
+    for n in lens:
+        at = slice(row, row + n)
+        row += n
+        if n == 0:
+            continue
+        ref = oracle.attn_bwd_ext(*(x[at].transpose(0, 1)[None].cpu() for x in (q, k, v, dO)), 1.0 / math.sqrt(D), W, C,
+                                  sink=host, o_round=None)
+        part = 2.0 ** -16 / math.sqrt(D) * float((dO[at].double() * got[0][at].double()).abs().sum())
+        floor += [part * float(x[at].double().norm(dim=2).max()) for x in (k, q)]
+        for i in (0, 1):
+            x = got[2 + i][at].transpose(0, 1).double().cpu().numpy()
+            off[i] += ((x - ref[i][0]) ** 2).sum(), (ref[i][0] ** 2).sum()
+    for i in (0, 1):
+        err, size = np.sqrt(off[i])
+        assert err <= 2 * 2.0 ** -8 * size + floor[i], (i, err, size, floor[i])
+
+
 @pytest.mark.parametrize("dtype,D,Hq,Hkv", [("bf16", 128, 4, 2), ("bf16", 64, 3, 3), ("bf16", 256, 2, 1),
                                              ("f32", 64, 2, 1)])
 @pytest.mark.parametrize("poison", [float("nan"), float("inf"), -3.0e38])
@@ -227,14 +266,14 @@ def test_bad_lengths_are_reported_and_nothing_is_computed(cu):
     n, sc, dt = len(cu) - 1, 0.1, fa.FORGE_DTYPE_BF16
     o, lse = torch.full_like(q, 7.0), torch.full((2, 10), 7.0, device=DEV)
     ws = torch.empty(fa.forge_attn_varlen_fwd_workspace_size(n, 10, 2, 1, 128, dt), dtype=torch.uint8, device=DEV)
-    assert fa.forge_attn_varlen_fwd(q, k, v, o, lse, bad, n, 10, 2, 1, 128, 256, 128, 128, sc, 0, 0.0, None, 0, dt, ws,
+    assert fa.forge_attn_varlen_fwd(q, k, v, o, None, lse, bad, n, 10, 2, 1, 128, 256, 128, 128, sc, 0, 0.0, None, 0, dt, ws,
                                     ws.numel()) == fa.FORGE_OK
     assert fa.forge_attn_check() == fa.FORGE_ERR_INVALID_ARG and fa.forge_attn_check() == fa.FORGE_OK
     assert bool((o == 7.0).all()) and bool((lse == 7.0).all())
     dq, dk, dv = (torch.full_like(x, 7.0) for x in (q, k, v))
     ws = torch.empty(fa.forge_attn_varlen_bwd_workspace_size(n, 10, 2, 1, 128, dt), dtype=torch.uint8, device=DEV)
-    assert fa.forge_attn_varlen_bwd(q, k, v, o, lse, dO, dq, dk, dv, bad, n, 10, 2, 1, 128, 256, 128, 128, sc, 0, 0.0,
-                                    None, None, 0, dt, ws, ws.numel()) == fa.FORGE_OK
+    assert fa.forge_attn_varlen_bwd(q, k, v, o, None, lse, dO, dq, dk, dv, bad, n, 10, 2, 1, 128, 256, 128, 128, sc, 0,
+                                    0.0, None, None, 0, dt, ws, ws.numel()) == fa.FORGE_OK
     assert fa.forge_attn_check() == fa.FORGE_ERR_INVALID_ARG
     assert all(bool((x == 7.0).all()) for x in (dq, dk, dv))
 
