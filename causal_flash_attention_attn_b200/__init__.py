@@ -519,13 +519,72 @@ def attention(q, k, v, scale=None, window=0, softcap=0.0, sink=None):
 
 
 # ------------------------------------------------------------ packed sequences
+_NOTHING = contextlib.nullcontext()
+
+
 def _scope(device, stream):
     """Makes `device`, and the stream if one is given, current: outputs and workspaces allocated inside
     belong to the stream that the kernels run on."""
     import torch
     if stream is not None:
         return torch.cuda.stream(torch.cuda.ExternalStream(stream, device=device) if isinstance(stream, int) else stream)
-    return contextlib.nullcontext() if torch.cuda.current_device() == device.index else torch.cuda.device(device)
+    return _NOTHING if torch.cuda.current_device() == device.index else torch.cuda.device(device)
+
+
+def _here(device):
+    """Handle of the current stream of `device`."""
+    import torch
+    try:  # without a Stream object: 0.2 instead of 3 us of a short call's host time
+        return torch._C._cuda_getCurrentRawStream(device.index)
+    except AttributeError:
+        return torch.cuda.current_stream(device).cuda_stream
+
+
+# The helpers below are called once per layer and token, so that their host time counts. Each takes
+# arguments that are as they should be through one test (_is, _is_packed, _is_pool) and leaves the
+# explanation of what is not to the _check functions, which test the same things one by one.
+# They call the library without the raw binding in between for the same reason.
+def _at(t):
+    return None if t is None else t.data_ptr()
+
+
+def _is(t, dtype, shape, index):
+    return t is None or t.dtype is dtype and t.shape == shape and t.get_device() == index and t.is_contiguous()
+
+
+def _is_packed(q, k, v, cu_seqlens, sink):
+    """(rows, Hq, Hkv, D, row strides) of packed arguments, or None: ask _check_packed."""
+    import torch
+    try:
+        sq, sk, sv, dtype, index = q.stride(), k.stride(), v.stride(), q.dtype, q.get_device()
+        rows, Hq, D = q.shape
+        Hkv = k.shape[1]
+        if (index >= 0 and rows > 1 and k.shape == v.shape == (rows, Hkv, D) and dtype is k.dtype is v.dtype and
+                k.get_device() == v.get_device() == index and sq[1:] == sk[1:] == sv[1:] == (D, 1) and
+                sq[0] >= Hq * D and sk[0] >= Hkv * D and sv[0] >= Hkv * D and not (sq[0] | sk[0] | sv[0]) % 8 and
+                cu_seqlens.dim() == 1 and cu_seqlens.numel() > 1 and
+                _is(cu_seqlens, torch.int32, cu_seqlens.shape, index) and _is(sink, torch.float32, (Hq,), index)):
+            return rows, Hq, Hkv, D, (sq[0], sk[0], sv[0])
+    except (AttributeError, TypeError, ValueError, IndexError):
+        pass
+    return None
+
+
+def _is_pool(k_pages, v_pages, dtype, index, layers=False):
+    """As _check_pool, or None: ask it."""
+    try:
+        st, shape = k_pages.stride(), k_pages.shape
+        nl, ls = 1, 0
+        if layers and len(shape) == 5:
+            nl, ls, st, shape = shape[0], st[0], st[1:], shape[1:]
+        P, Hkv, ps, D = shape
+        if (index >= 0 and P > 1 and st[1:] == (ps * D, D, 1) and k_pages.shape == v_pages.shape and
+                k_pages.stride() == v_pages.stride() and k_pages.dtype is dtype is v_pages.dtype and
+                k_pages.get_device() == v_pages.get_device() == index):
+            return nl, ls, P, Hkv, ps, D, st[0]
+    except (AttributeError, TypeError, ValueError, IndexError):
+        pass
+    return None
 
 
 def _check_dense(what, device, **specs):
@@ -589,17 +648,20 @@ def attention_varlen_fwd(q, k, v, cu_seqlens, scale=None, window=0, softcap=0.0,
     are reported by forge_attn_check."""
     import torch
     what = "attention_varlen_fwd"
-    rows, Hq, Hkv, D, (qs, ks, vs) = _check_packed(what, q, k, v, cu_seqlens, sink)
+    rows, Hq, Hkv, D, (qs, ks, vs) = (_is_packed(q, k, v, cu_seqlens, sink) or
+                                      _check_packed(what, q, k, v, cu_seqlens, sink))
     scale = 1.0 / math.sqrt(D) if scale is None else scale
     dt, n = dtype_code(q.dtype), cu_seqlens.numel() - 1
     with _scope(q.device, stream):
         o = torch.empty((rows, Hq, D), dtype=q.dtype, device=q.device)
         o_res = torch.empty_like(o) if return_residual and dt == FORGE_DTYPE_BF16 else None
         lse = torch.empty((Hq, rows), dtype=torch.float32, device=q.device)
-        nbytes = forge_attn_varlen_fwd_workspace_size(n, rows, Hq, Hkv, D, dt)
+        L = library()
+        nbytes = L.forge_attn_varlen_fwd_workspace_size(n, rows, Hq, Hkv, D, dt)
         ws = torch.empty(nbytes, dtype=torch.uint8, device=q.device)
-        s = forge_attn_varlen_fwd(q, k, v, o, o_res, lse, cu_seqlens, n, rows, Hq, Hkv, D, qs, ks, vs, scale, window,
-                                  softcap, sink, True, dt, ws, nbytes)
+        s = L.forge_attn_varlen_fwd(q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), _at(o_res), lse.data_ptr(),
+                                    cu_seqlens.data_ptr(), n, rows, Hq, Hkv, D, qs, ks, vs, scale, window, softcap,
+                                    _at(sink), 1, dt, ws.data_ptr(), nbytes, _here(q.device))
     if s != FORGE_OK:
         raise ForgeError(s, "forge_attn_varlen_fwd")
     return (o, lse, o_res) if return_residual else (o, lse)
@@ -612,18 +674,25 @@ def attention_varlen_bwd(q, k, v, o, lse, dO, cu_seqlens, scale=None, window=0, 
     sequence."""
     import torch
     what = "attention_varlen_bwd"
-    rows, Hq, Hkv, D, (qs, ks, vs) = _check_packed(what, q, k, v, cu_seqlens, sink)
-    _check_dense(what, q.device, o=(o, q.dtype, (rows, Hq, D)), lse=(lse, torch.float32, (Hq, rows)),
-                 o_res=(o_res, q.dtype, (rows, Hq, D)), dO=(dO, q.dtype, (rows, Hq, D)))
+    rows, Hq, Hkv, D, (qs, ks, vs) = (_is_packed(q, k, v, cu_seqlens, sink) or
+                                      _check_packed(what, q, k, v, cu_seqlens, sink))
+    shape, dev = (rows, Hq, D), q.get_device()
+    if not (_is(o, q.dtype, shape, dev) and _is(o_res, q.dtype, shape, dev) and _is(dO, q.dtype, shape, dev) and
+            _is(lse, torch.float32, (Hq, rows), dev)):
+        _check_dense(what, q.device, o=(o, q.dtype, shape), lse=(lse, torch.float32, (Hq, rows)),
+                     o_res=(o_res, q.dtype, shape), dO=(dO, q.dtype, shape))
     scale = 1.0 / math.sqrt(D) if scale is None else scale
     dt, n = dtype_code(q.dtype), cu_seqlens.numel() - 1
     with _scope(q.device, stream):
         dq, dk, dv = (torch.empty(x.shape, dtype=x.dtype, device=x.device) for x in (q, k, v))
         dsink = torch.empty((Hq,), dtype=torch.float32, device=q.device) if sink is not None else None
-        nbytes = forge_attn_varlen_bwd_workspace_size(n, rows, Hq, Hkv, D, dt)
+        L = library()
+        nbytes = L.forge_attn_varlen_bwd_workspace_size(n, rows, Hq, Hkv, D, dt)
         ws = torch.empty(nbytes, dtype=torch.uint8, device=q.device)
-        s = forge_attn_varlen_bwd(q, k, v, o, o_res, lse, dO, dq, dk, dv, cu_seqlens, n, rows, Hq, Hkv, D, qs, ks, vs,
-                                  scale, window, softcap, sink, dsink, True, dt, ws, nbytes)
+        s = L.forge_attn_varlen_bwd(q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), _at(o_res), lse.data_ptr(),
+                                    dO.data_ptr(), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), cu_seqlens.data_ptr(),
+                                    n, rows, Hq, Hkv, D, qs, ks, vs, scale, window, softcap, _at(sink), _at(dsink), 1,
+                                    dt, ws.data_ptr(), nbytes, _here(q.device))
     if s != FORGE_OK:
         raise ForgeError(s, "forge_attn_varlen_bwd")
     return (dq, dk, dv, dsink) if sink is not None else (dq, dk, dv)
@@ -707,21 +776,27 @@ def attention_decode_paged(q, k_pages, v_pages, page_table, seq_lens, scale=None
         raise ValueError(f"{what}: q must be [B, Hq, D] and page_table [B, width], got {tuple(q.shape)} and "
                          f"{tuple(page_table.shape)}")
     B, Hq, D = q.shape
-    _, _, P, Hkv, ps, Dk, stride = _check_pool(what, q.dtype, q.device, k_pages, v_pages)
+    width, dev = page_table.shape[1], q.get_device()
+    _, _, P, Hkv, ps, Dk, stride = (_is_pool(k_pages, v_pages, q.dtype, dev) or
+                                    _check_pool(what, q.dtype, q.device, k_pages, v_pages))
     if Dk != D:
         raise ValueError(f"{what}: q has head dim {D}, the pools {Dk}")
-    _check_dense(what, q.device, q=(q, q.dtype, q.shape),
-                 page_table=(page_table, torch.int32, (B, page_table.shape[1])),
-                 seq_lens=(seq_lens, torch.int32, (B,)), sink=(sink, torch.float32, (Hq,)))
+    if not (_is(q, q.dtype, q.shape, dev) and _is(page_table, torch.int32, (B, width), dev) and
+            _is(seq_lens, torch.int32, (B,), dev) and _is(sink, torch.float32, (Hq,), dev)):
+        _check_dense(what, q.device, q=(q, q.dtype, q.shape), page_table=(page_table, torch.int32, (B, width)),
+                     seq_lens=(seq_lens, torch.int32, (B,)), sink=(sink, torch.float32, (Hq,)))
     scale = 1.0 / math.sqrt(D) if scale is None else scale
     dt = dtype_code(q.dtype)
     with _scope(q.device, stream):
         o = torch.empty_like(q)
         lse = torch.empty((B, Hq), dtype=torch.float32, device=q.device)
-        nbytes = forge_attn_decode_paged_workspace_size(B, Hq, Hkv, D, dt)
+        L = library()
+        nbytes = L.forge_attn_decode_paged_workspace_size(B, Hq, Hkv, D, dt)
         ws = torch.empty(nbytes, dtype=torch.uint8, device=q.device)
-        s = forge_attn_decode_paged(q, k_pages, v_pages, o, lse, page_table, seq_lens, B, Hq, Hkv, D, P, ps,
-                                    page_table.shape[1], stride, scale, window, softcap, sink, dt, ws, nbytes)
+        s = L.forge_attn_decode_paged(q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), o.data_ptr(),
+                                      lse.data_ptr(), page_table.data_ptr(), seq_lens.data_ptr(), B, Hq, Hkv, D, P, ps,
+                                      width, stride, scale, window, softcap, _at(sink), dt, ws.data_ptr(), nbytes,
+                                      _here(q.device))
     if s != FORGE_OK:
         raise ForgeError(s, "forge_attn_decode_paged")
     return o, lse
@@ -743,15 +818,24 @@ def paged_append(k, v, k_pages, v_pages, page_table, starts, cu_seqlens=None, st
     n, width = page_table.shape
     if cu_seqlens is None and n != rows:
         raise ValueError(f"{what}: {rows} rows for {n} sequences need cu_seqlens")
-    ks, vs = _check_rows(what, k.dtype, k.device, k=k, v=v)
-    _check_dense(what, k.device, page_table=(page_table, torch.int32, (n, width)), starts=(starts, torch.int32, (n,)),
-                 cu_seqlens=(cu_seqlens, torch.int32, (n + 1,)))
-    _, _, P, Hp, ps, Dp, stride = _check_pool(what, k.dtype, k.device, k_pages, v_pages)
+    dev, sk, sv = k.get_device(), k.stride(), v.stride()
+    if (rows > 1 and sk[1:] == sv[1:] == (D, 1) and k.dtype is v.dtype and v.get_device() == dev >= 0 and
+            sk[0] >= Hkv * D and sv[0] >= Hkv * D and not (sk[0] | sv[0]) % 8):
+        ks, vs = sk[0], sv[0]
+    else:
+        ks, vs = _check_rows(what, k.dtype, k.device, k=k, v=v)
+    if not (_is(page_table, torch.int32, (n, width), dev) and _is(starts, torch.int32, (n,), dev) and
+            _is(cu_seqlens, torch.int32, (n + 1,), dev)):
+        _check_dense(what, k.device, page_table=(page_table, torch.int32, (n, width)),
+                     starts=(starts, torch.int32, (n,)), cu_seqlens=(cu_seqlens, torch.int32, (n + 1,)))
+    _, _, P, Hp, ps, Dp, stride = (_is_pool(k_pages, v_pages, k.dtype, dev) or
+                                   _check_pool(what, k.dtype, k.device, k_pages, v_pages))
     if (Hp, Dp) != (Hkv, D):
         raise ValueError(f"{what}: k has {Hkv} heads of {D}, the pools {Hp} of {Dp}")
     with _scope(k.device, stream):
-        s = forge_attn_paged_append(k, v, k_pages, v_pages, page_table, starts, cu_seqlens, n, rows, Hkv, D, P, ps,
-                                    width, ks, vs, stride, dtype_code(k.dtype))
+        s = library().forge_attn_paged_append(k.data_ptr(), v.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(),
+                                              page_table.data_ptr(), starts.data_ptr(), _at(cu_seqlens), n, rows, Hkv,
+                                              D, P, ps, width, ks, vs, stride, dtype_code(k.dtype), _here(k.device))
     if s != FORGE_OK:
         raise ForgeError(s, "forge_attn_paged_append")
 
@@ -761,6 +845,8 @@ def _host_ints(what, name, x):
     if isinstance(x, torch.Tensor):
         if x.is_cuda:
             raise ValueError(f"{what}: {name} must be on the host")
+        if x.dim() == 1 and x.dtype is torch.int32 and x.is_contiguous():
+            return x
         if x.dim() != 1 or x.dtype not in (torch.int32, torch.int64):
             raise ValueError(f"{what}: {name} must be a list of page numbers")
         if x.dtype == torch.int64 and x.numel() and (int(x.min()) < 0 or int(x.max()) >= 1 << 31):
@@ -777,10 +863,12 @@ def paged_copy(k_pages, v_pages, src, dst, stream=None):
     src, dst = _host_ints(what, "src", src), _host_ints(what, "dst", dst)
     if src.numel() != dst.numel():
         raise ValueError(f"{what}: {src.numel()} sources for {dst.numel()} destinations")
-    nl, ls, P, Hkv, ps, D, stride = _check_pool(what, k_pages.dtype, k_pages.device, k_pages, v_pages, layers=True)
+    nl, ls, P, Hkv, ps, D, stride = (_is_pool(k_pages, v_pages, k_pages.dtype, k_pages.get_device(), layers=True) or
+                                     _check_pool(what, k_pages.dtype, k_pages.device, k_pages, v_pages, layers=True))
     with _scope(k_pages.device, stream):
-        s = forge_attn_paged_copy(k_pages, v_pages, src, dst, src.numel(), nl, ls, P, Hkv, ps, D, stride,
-                                  dtype_code(k_pages.dtype))
+        s = library().forge_attn_paged_copy(k_pages.data_ptr(), v_pages.data_ptr(), src.data_ptr(), dst.data_ptr(),
+                                            src.numel(), nl, ls, P, Hkv, ps, D, stride, dtype_code(k_pages.dtype),
+                                            _here(k_pages.device))
     if s != FORGE_OK:
         raise ForgeError(s, "forge_attn_paged_copy")
 
