@@ -665,13 +665,26 @@ int pd_workers_of(int D, forge_dtype dtype) {
     }
 }
 
+// Workspace: [ part [2 workers][G][D] f32 ][ stat [2 workers][G] float2 ][ cut [B][Hkv] int2 ]
+struct PdLayout {
+    size_t stat, cut, bytes;
+};
+PdLayout pd_layout(int B, int Hq, int Hkv, int D, forge_dtype dtype) {
+    PdLayout l;
+    const size_t slots = (size_t)2 * pd_workers_of(D, dtype) * (Hq / Hkv);
+    l.stat = round256(slots * D * sizeof(float));
+    l.cut = l.stat + round256(slots * sizeof(float2));
+    l.bytes = l.cut + round256((size_t)B * Hkv * sizeof(int2));
+    return l;
+}
+
 template <typename T_, int D, class W>
 forge_status pd_launch(const PdParams &p, cudaStream_t st) {
     using C = PdCfg<T_, D>;
     if (set_smem(decode_paged_split<T_, D, W>, C::SMEM) != FORGE_OK) return FORGE_ERR_CUDA;
     forge_status s = launch_pdl(decode_paged_split<T_, D, W>, dim3((unsigned)p.workers), dim3(kPdThreads), C::SMEM, st, p);
     if (s != FORGE_OK) return s;
-    return launch_pdl(decode_paged_join<T_, D>, dim3((unsigned)(p.B * p.Hq)), dim3(128), 0, st, p);
+    return launch_pdl(decode_paged_join<T_, D>, dim3((unsigned)(p.B * p.Hq)), dim3(D), 0, st, p);
 }
 
 template <int D>
@@ -1253,7 +1266,7 @@ forge_status forge_attn_varlen_bwd(const void *q, const void *k, const void *v, 
 
 size_t forge_attn_decode_paged_workspace_size(int B, int Hq, int Hkv, int D, forge_dtype dtype) {
     if (check_sizes(B, Hq, Hkv, 1, D, dtype) != FORGE_OK || Hq / Hkv > kPdMaxG) return 0;
-    return round256((size_t)2 * pd_workers_of(D, dtype) * (Hq / Hkv) * (size_t)(D + 2) * sizeof(float));
+    return pd_layout(B, Hq, Hkv, D, dtype).bytes;
 }
 
 forge_status forge_attn_decode_paged(const void *q, const void *k_pages, const void *v_pages, void *o, float *lse,
@@ -1270,7 +1283,8 @@ forge_status forge_attn_decode_paged(const void *q, const void *k_pages, const v
     if (!aligned16(q) || !aligned16(o) || !aligned4(page_table) || !aligned4(seq_lens) || (lse && !aligned4(lse)) ||
         (sink && !aligned4(sink)))
         return FORGE_ERR_INVALID_ARG;
-    if (!aligned16(workspace) || workspace_bytes < forge_attn_decode_paged_workspace_size(B, Hq, Hkv, D, dtype))
+    if (workspace == nullptr || (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0 ||
+        workspace_bytes < forge_attn_decode_paged_workspace_size(B, Hq, Hkv, D, dtype))
         return FORGE_ERR_WORKSPACE;
     PdParams p;
     p.q = q;
@@ -1281,7 +1295,10 @@ forge_status forge_attn_decode_paged(const void *q, const void *k_pages, const v
     p.table = page_table;
     p.seq_lens = seq_lens;
     p.sink = sink;
+    const PdLayout l = pd_layout(B, Hq, Hkv, D, dtype);
     p.part = static_cast<float *>(workspace);
+    p.stat = reinterpret_cast<float2 *>(static_cast<char *>(workspace) + l.stat);
+    p.cut = reinterpret_cast<int2 *>(static_cast<char *>(workspace) + l.cut);
     p.page_stride = (long long)page_stride;
     p.B = B; p.Hq = Hq; p.Hkv = Hkv; p.width = table_width; p.page = page_size; p.num_pages = num_pages;
     p.window = effective_window(window, table_width * page_size);

@@ -10,8 +10,9 @@
 // order, and CTA c of nw takes units [U c / nw, U (c + 1) / nw): equal shares whatever
 // the lengths, read from seq_lens on the device. A CTA whose share covers a whole pair
 // writes o and lse itself; a pair cut between CTAs leaves (max, sum, o) per CTA in
-// the workspace, at most two per CTA (its first and its last pair), and
-// decode_paged_join merges them. Nothing depends on a maximum length.
+// the workspace, at most two per CTA (its first and its last pair), the CTA that holds
+// the pair's first unit writes down where, and decode_paged_join merges them. Nothing
+// depends on a maximum length.
 //
 // Inside a CTA the four warps take the four steps of each unit, each with its own ring
 // of 16-byte asynchronous copies and its own online softmax, and merge when the CTA
@@ -66,7 +67,9 @@ struct PdParams {
     const int *table;          // [B][width]
     const int *seq_lens;       // [B]
     const float *sink;
-    float *part;               // [2 nw][G][D + 2]: o, max, sum
+    float *part;               // [2 nw][G][D]: unnormalised o of a cut pair's pieces
+    float2 *stat;              // [2 nw][G]: (max, sum) of those
+    int2 *cut;                 // [B][Hkv]: (first piece's slot, pieces; 0 = the pair was not cut)
     long long page_stride;     // elements between pages
     int B, Hq, Hkv, width, page, num_pages, window, workers;
     float qscale;              // scale * log2(e), or scale / softcap with a cap
@@ -91,19 +94,10 @@ __device__ __forceinline__ PdSeq pd_seq(const PdParams &p, int b) {
     return s;
 }
 
-// Units of all sequences before `until`, over the block (every thread gets it).
-template <int UNIT>
-__device__ __forceinline__ long long pd_units(const PdParams &p, int until, long long *red) {
-    long long n = 0;
-    for (int b = threadIdx.x; b < until; b += blockDim.x) n += pd_seq<UNIT>(p, b).nu;
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) n += __shfl_xor_sync(0xffffffffu, n, o);
-    __syncthreads();
-    if (threadIdx.x % 32 == 0) red[threadIdx.x / 32] = n;
-    __syncthreads();
-    n = 0;
-    for (int w = 0; w < (int)blockDim.x / 32; w++) n += red[w];
-    return n;
+// First unit of share c of n.
+__device__ __forceinline__ long long pd_share(long long U, int c, int n) {
+    if (U < (1 << 20) && n <= 2048) return (unsigned)U * (unsigned)c / (unsigned)n;  // below 2^31
+    return U * c / n;
 }
 
 // Walks units: sequence b, KV head hk, unit j of the pair's nu.
@@ -126,6 +120,9 @@ struct PdIter {
 __device__ __forceinline__ void pd_copy16(uint32_t dst, const void *src, bool live) {
     const int n = live ? 16 : 0;  // 0: nothing is read, the 16 bytes become zeros
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
+}
+__device__ __forceinline__ void pd_copy16(uint32_t dst, const void *src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
 __device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t (&r)[4]) {
     asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
@@ -182,19 +179,23 @@ struct PdWarpBf {
     __device__ __forceinline__ void step(const PdParams &p, uint32_t sK, uint32_t sV, int key0, int lo, int hi, int G,
                                          float *, const float *) {
         const int lane = threadIdx.x % 32;
-        float s[2][4];
+        float s[2][4], s2[2][4];  // two chains of products each: even and odd slices of the head dim
 #pragma unroll
         for (int i = 0; i < 2; i++)
 #pragma unroll
-            for (int e = 0; e < 4; e++) s[i][e] = 0.0f;
+            for (int e = 0; e < 4; e++) s[i][e] = s2[i][e] = 0.0f;
         const int kr = (lane / 16) * 8 + lane % 8, kc = (lane / 8) % 2;
 #pragma unroll
         for (int kk = 0; kk < D / 16; kk++) {
             uint32_t b[4];
             ldsm4(sK + (uint32_t)(kr * C::ROWB + (((2 * kk + kc) ^ (kr & 7)) << 4)), b);
-            mma16816(s[0], q[kk], b[0], b[1]);
-            mma16816(s[1], q[kk], b[2], b[3]);
+            mma16816(kk % 2 ? s2[0] : s[0], q[kk], b[0], b[1]);
+            mma16816(kk % 2 ? s2[1] : s[1], q[kk], b[2], b[3]);
         }
+#pragma unroll
+        for (int i = 0; i < 2; i++)
+#pragma unroll
+            for (int e = 0; e < 4; e++) s[i][e] += s2[i][e];
         const bool part = key0 < lo || key0 + C::KS > hi;
         float f[2];
         bool moved = false;
@@ -439,14 +440,22 @@ __global__ void __launch_bounds__(kPdThreads, PdCfg<T_, D>::PER_SM) decode_paged
     griddep_launch_dependents();
     griddep_wait();
 
-    // this CTA's units, and the sequence that holds the first
-    const long long U = pd_units<C::UNIT>(p, p.B, red) * p.Hkv;
-    const long long nw = min((long long)gridDim.x, U);
-    if ((long long)blockIdx.x >= nw) return;
-    const long long lo = U * blockIdx.x / nw, hi = U * (blockIdx.x + 1) / nw;
+    // this CTA's units, and the sequence that holds the first: prefix sums over the
+    // sequences, 128 at a time (after a pass for the total, if there are more)
+    long long U = 0, lo = 0, hi = 0;
+    int nw = 1;
     PdIter ld;
+    long long pair0 = 0;  // first unit of the iterator's pair
     {
-        __shared__ long long found[2];
+        if (p.B > kPdThreads) {
+            long long n = 0;
+            for (int b = threadIdx.x; b < p.B; b += kPdThreads) n += pd_seq<C::UNIT>(p, b).nu;
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) n += __shfl_xor_sync(0xffffffffu, n, o);
+            if (lane == 0) red[warp] = n;
+            __syncthreads();
+            for (int w = 0; w < kPdWarps; w++) U += red[w] * p.Hkv;
+        }
         long long before = 0;
         for (int b0 = 0; b0 < p.B; b0 += kPdThreads) {
             const int b = b0 + (int)threadIdx.x;
@@ -460,22 +469,33 @@ __global__ void __launch_bounds__(kPdThreads, PdCfg<T_, D>::PER_SM) decode_paged
             __syncthreads();
             if (lane == 31) red[warp] = s;
             __syncthreads();
-            for (int w = 0; w < warp; w++) s += red[w];
             long long chunk = 0;
-            for (int w = 0; w < kPdWarps; w++) chunk += red[w];
+            for (int w = 0; w < kPdWarps; w++) {
+                if (w < warp) s += red[w];
+                chunk += red[w];
+            }
+            if (p.B <= kPdThreads) U = chunk * p.Hkv;
+            if (b0 == 0) {
+                if (U == 0) return;  // every sequence is empty: the join writes them
+                nw = (int)min((long long)gridDim.x, U);
+                if ((int)blockIdx.x >= nw) return;
+                lo = pd_share(U, (int)blockIdx.x, nw);
+                hi = pd_share(U, (int)blockIdx.x + 1, nw);
+            }
             const long long u = (before + s - nu) * p.Hkv;  // first unit of sequence b
             if (nu > 0 && u <= lo && lo < u + (long long)nu * p.Hkv) {
-                found[0] = b;
-                found[1] = u;
+                red[4] = b;
+                red[5] = u;
             }
             before += chunk;
         }
         __syncthreads();
-        ld.b = (int)found[0];
+        ld.b = (int)red[4];
         ld.s = pd_seq<C::UNIT>(p, ld.b);
-        const long long r = lo - found[1];
+        const long long r = lo - red[5];
         ld.hk = (int)(r / ld.s.nu);
         ld.j = (int)(r % ld.s.nu);
+        pair0 = lo - ld.j;
     }
     PdIter at = ld;
 
@@ -497,14 +517,24 @@ __global__ void __launch_bounds__(kPdThreads, PdCfg<T_, D>::PER_SM) decode_paged
         const uint8_t *K = reinterpret_cast<const uint8_t *>(static_cast<const T_ *>(p.k) + base);
         const uint8_t *V = reinterpret_cast<const uint8_t *>(static_cast<const T_ *>(p.v) + base);
         const uint32_t dst = ring + (uint32_t)(stage * 2 * C::STEP);
+        if (pg >= 0 && key0 >= i.s.first && key0 + C::KS <= i.s.len) {  // every row visible
 #pragma unroll
-        for (int e = 0; e < C::KS * C::CPR / 32; e++) {
-            const int c = e * 32 + lane, r = c / C::CPR, key = key0 + r;
-            const bool live = pg >= 0 && key >= i.s.first && key < i.s.len;
-            const uint32_t to = (uint32_t)(r * C::ROWB + (((c % C::CPR) ^ W::swizzle(r)) << 4));
-            const size_t from = live ? (size_t)c * 16 : 0;
-            pd_copy16(dst + to, K + from, live);
-            pd_copy16(dst + C::STEP + to, V + from, live);
+            for (int e = 0; e < C::KS * C::CPR / 32; e++) {
+                const int c = e * 32 + lane, r = c / C::CPR;
+                const uint32_t to = (uint32_t)(r * C::ROWB + (((c % C::CPR) ^ W::swizzle(r)) << 4));
+                pd_copy16(dst + to, K + c * 16);
+                pd_copy16(dst + C::STEP + to, V + c * 16);
+            }
+        } else {
+#pragma unroll 1
+            for (int e = 0; e < C::KS * C::CPR / 32; e++) {
+                const int c = e * 32 + lane, r = c / C::CPR, key = key0 + r;
+                const bool live = pg >= 0 && key >= i.s.first && key < i.s.len;
+                const uint32_t to = (uint32_t)(r * C::ROWB + (((c % C::CPR) ^ W::swizzle(r)) << 4));
+                const size_t from = live ? (size_t)c * 16 : 0;
+                pd_copy16(dst + to, K + from, live);
+                pd_copy16(dst + C::STEP + to, V + from, live);
+            }
         }
     };
     long long to_load = hi - lo;
@@ -577,77 +607,65 @@ __global__ void __launch_bounds__(kPdThreads, PdCfg<T_, D>::PER_SM) decode_paged
                     if (p.lse != nullptr && i % D == 0) p.lse[(size_t)at.b * p.Hq + at.hk * G + r] = lse;
                 }
             } else {
-                float *part = p.part + (size_t)(2 * blockIdx.x + (first_pair ? 0 : 1)) * G * (D + 2);
-                for (int i = threadIdx.x; i < G * D; i += kPdThreads) {
-                    const int r = i / D;
-                    part[r * (D + 2) + i % D] = sO[i] + sO[kPdMaxG * D + i];
-                    if (i % D == 0) {
-                        part[r * (D + 2) + D] = sM[r];
-                        part[r * (D + 2) + D + 1] = sL[r];
-                    }
+                const size_t slot = 2 * (size_t)blockIdx.x + (first_pair ? 0 : 1);
+                for (int i = threadIdx.x; i < G * D; i += kPdThreads) p.part[slot * G * D + i] = sO[i] + sO[kPdMaxG * D + i];
+                if ((int)threadIdx.x < G) p.stat[slot * G + threadIdx.x] = make_float2(sM[threadIdx.x], sL[threadIdx.x]);
+            }
+            if (whole && threadIdx.x == 0) {
+                // where the join finds the pair's pieces: this CTA's, then the first one
+                // of each of the CTAs up to the one that holds the pair's last unit
+                int2 cut = make_int2(2 * (int)blockIdx.x + (first_pair ? 0 : 1), 0);
+                if (!done) {
+                    // share c ends past unit x: c < (x + 1) nw / U
+                    const long long x = pair0 + at.s.nu - 1;
+                    cut.y = (int)(((x + 1) * nw - 1) / U) - (int)blockIdx.x + 1;
                 }
+                p.cut[(size_t)at.b * p.Hkv + at.hk] = cut;
             }
             fresh = true;
             first_pair = false;
             whole = true;
-            // sM, sL and sO are next written after the barriers of the next merge's
-            // put_stats only for sO; the stats need one here
-            __syncthreads();
+            pair0 = u + 1;
+            __syncthreads();  // sM, sL are read before the next pair's are written
         }
         if (u + 1 < hi) at.next<C::UNIT>(p);
     }
     cp_async_wait<0>();
 }
 
-// One block per (sequence, query head): merges the partial results of a pair that
-// was cut between CTAs; writes the empty sequences.
+// One block per (sequence, query head), a thread per head dim: merges the pieces of
+// a pair that was cut between CTAs; writes the empty sequences.
 template <typename T_, int D>
-__global__ void __launch_bounds__(128) decode_paged_join(const PdParams p) {
+__global__ void __launch_bounds__(D) decode_paged_join(const PdParams p) {
     using C = PdCfg<T_, D>;
-    __shared__ long long red[4];
     griddep_launch_dependents();
     griddep_wait();
     const int b = blockIdx.x / p.Hq, hq = blockIdx.x % p.Hq, G = p.Hq / p.Hkv, hk = hq / G, r = hq % G;
-    T_ *O = static_cast<T_ *>(p.o) + ((size_t)b * p.Hq + hq) * D;
+    const int d = threadIdx.x, lane = threadIdx.x % 32;
     const PdSeq s = pd_seq<C::UNIT>(p, b);
-    if (s.nu == 0) {
-        float f, lse;
-        pd_total(-INFINITY, 0.0f, p, hq, f, lse);
-        for (int d = threadIdx.x; d < D; d += 128) from_f32(O + d, 0.0f);
-        if (p.lse != nullptr && threadIdx.x == 0) p.lse[(size_t)b * p.Hq + hq] = lse;
-        return;
-    }
-    const long long U = pd_units<C::UNIT>(p, p.B, red) * p.Hkv;
-    const long long u0 = pd_units<C::UNIT>(p, b, red) * p.Hkv + (long long)hk * s.nu;
-    const long long nw = min((long long)p.workers, U);
-    // CTA c holds units [U c / nw, U (c + 1) / nw)
-    const long long c0 = ((u0 + 1) * nw - 1) / U, c1 = ((u0 + s.nu) * nw - 1) / U;
-    if (c0 == c1) return;
-    // the pair is the last one of CTA c0 (its first one too if it starts its share)
-    // and the first one of the others
-    const long long slot0 = 2 * c0 + (U * c0 / nw == u0 ? 0 : 1);
-    auto part_of = [&](long long c) -> const float * {
-        return p.part + ((size_t)(c == c0 ? slot0 : 2 * c) * G + r) * (D + 2);
-    };
-    float M = -INFINITY;
-    for (long long c = c0; c <= c1; c++) M = fmaxf(M, part_of(c)[D]);
-    float l = 0.0f, acc[D / 64 > 1 ? D / 128 : 1];
-#pragma unroll
-    for (int i = 0; i < (int)(sizeof(acc) / 4); i++) acc[i] = 0.0f;
-    for (long long c = c0; c <= c1; c++) {
-        const float *x = part_of(c);
-        const float f = x[D] == -INFINITY ? 0.0f : ex2_approx(x[D] - M);
-        l += x[D + 1] * f;
-#pragma unroll
-        for (int i = 0; i < (int)(sizeof(acc) / 4); i++)
-            if (threadIdx.x + 128 * i < D) acc[i] = fmaf(x[threadIdx.x + 128 * i], f, acc[i]);
+    const int2 cut = p.cut[(size_t)b * p.Hkv + hk];  // of an earlier call if the sequence is empty
+    if (s.nu > 0 && cut.y == 0) return;
+    float M = -INFINITY, l = 0.0f, acc = 0.0f;
+    if (s.nu > 0) {
+        auto slot = [&](int c) -> size_t { return c == 0 ? (size_t)cut.x : 2 * ((size_t)cut.x / 2 + c); };
+        for (int c0 = 0; c0 < cut.y; c0 += 32) {  // 32 pieces at a time
+            const int n = min(32, cut.y - c0);
+            const float2 x = lane < n ? p.stat[slot(c0 + lane) * G + r] : make_float2(-INFINITY, 0.0f);
+            const float M2 = fmaxf(M, warp_max(x.x));
+            const float M0 = M2 == -INFINITY ? 0.0f : M2;
+            const float f = ex2_approx(x.x - M0), keep = ex2_approx(M - M0);
+            l = l * keep + warp_sum(x.y * f);
+            acc *= keep;
+            M = M2;
+#pragma unroll 8
+            for (int c = 0; c < n; c++)
+                acc = fmaf(p.part[(slot(c0 + c) * G + r) * D + d], __shfl_sync(0xffffffffu, f, c), acc);
+        }
     }
     float f, lse;
     pd_total(M, l, p, hq, f, lse);
-#pragma unroll
-    for (int i = 0; i < (int)(sizeof(acc) / 4); i++)
-        if (threadIdx.x + 128 * i < D) from_f32(O + threadIdx.x + 128 * i, acc[i] * f);
-    if (p.lse != nullptr && threadIdx.x == 0) p.lse[(size_t)b * p.Hq + hq] = lse;
+    from_f32(static_cast<T_ *>(p.o) + ((size_t)b * p.Hq + hq) * D + d, s.nu > 0 ? acc * f : 0.0f);
+    if (p.lse != nullptr && d == 0) p.lse[(size_t)b * p.Hq + hq] = lse;
 }
 
 }  // namespace forge

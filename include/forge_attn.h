@@ -304,7 +304,7 @@ forge_status forge_attn_varlen_bwd(const void *q, const void *k, const void *v, 
  *   0 (a padded batch entry): o = 0 and lse = -inf, or the sink. An entry with a bad
  *   length is taken as empty, a bad page as holding no visible key. Hq / Hkv <= 16. Rows of
  *   the pool that no query sees are not read: what they hold (NaN included) does not matter.
- *   workspace: 16-byte aligned, overwritten, of at least the given size, which does
+ *   workspace: 256-byte aligned, overwritten, of at least the given size, which does
  *   not depend on the lengths. Two kernels: the split pass (the batch's visible keys in
  *   equal shares over the SMs) and the join.
  *
