@@ -439,6 +439,18 @@ int var_pad_rows(int rows, int num_seqs) {
     return (int)((n + 127) / 128 * 128);
 }
 
+// Slots for the parts of key tiles that varlen_plan cuts. A part has about S per / (ctas
+// kPlanParts) query tiles or more (S: all query tiles over the key tiles; per: items of a
+// key tile), so the parts of cut tiles, which have more than that each, are at most
+// 2 S / that = 2 ctas kPlanParts / per; and a sequence of n tiles has n (n + 1) / 2 query
+// tiles in all.
+int var_per_tile(int Hkv, int D) { return Hkv * (D == 256 ? 2 : 1); }
+int var_max_slots(int rows, int tiles, int Hkv, int D) {
+    const long long a = 2ll * sm_count() * kPlanParts / var_per_tile(Hkv, D) + 2;
+    const long long most = rows / 128 + 1, b = tiles * (most < 64 ? most : 64);
+    return (int)(a < b ? a : b);
+}
+
 forge_status check_var_sizes(int num_seqs, int rows, int Hq, int Hkv, int D, forge_dtype dtype) {
     forge_status s = check_sizes(1, Hq, Hkv, rows, D, dtype);
     if (s != FORGE_OK) return s;
@@ -464,25 +476,37 @@ forge_status check_var_args(const VarArgs &a) {
 }
 
 // Workspace: [ count ][ items ][ backward: Delta [Hq][rows] f32 ][ bf16: dq accumulator [Hq][pad_rows][D] f32 ]
+//   bf16 backward:      [ cut list ][ parts [slots][Hkv][dk, dv][128][D] f32 ]
 struct VarLayout {
-    size_t items, delta, acc, bytes;
+    size_t items, delta, acc, cut, parts, bytes;
+    int max_items, slots;
 };
-VarLayout var_layout(int num_seqs, int rows, int Hq, int D, forge_dtype dtype, bool backward) {
+VarLayout var_layout(int num_seqs, int rows, int Hq, int Hkv, int D, forge_dtype dtype, bool backward) {
     VarLayout l;
+    const int tiles = var_max_items(rows, num_seqs, var_unit(D, dtype, backward));
+    const bool cuts = backward && dtype == FORGE_DTYPE_BF16;
+    l.slots = cuts ? var_max_slots(rows, tiles, Hkv, D) : 0;
+    // a tile cut into n parts takes n slots and is n items
+    l.max_items = tiles + l.slots;
     l.items = 256;
-    l.delta = l.items + round256(sizeof(VarItem) * (size_t)var_max_items(rows, num_seqs, var_unit(D, dtype, backward)));
+    l.delta = l.items + round256(sizeof(VarItem) * (size_t)l.max_items);
     l.acc = l.delta + (backward ? delta_bytes(1, Hq, rows) : 0);
-    l.bytes = l.acc;
-    if (backward && dtype == FORGE_DTYPE_BF16)
-        l.bytes += round256(sizeof(float) * (size_t)Hq * var_pad_rows(rows, num_seqs) * D);
+    l.cut = l.acc + (cuts ? round256(sizeof(float) * (size_t)Hq * var_pad_rows(rows, num_seqs) * D) : 0);
+    l.parts = l.cut + (cuts ? round256(16 * ((size_t)l.slots / 2 + 1)) : 0);
+    l.bytes = l.parts + sizeof(float) * (size_t)l.slots * Hkv * 256 * D;
     return l;
 }
 
-VarSched var_sched(const VarArgs &a, void *ws, bool backward) {
+VarSched var_sched(const VarArgs &a, const VarLayout &l, void *ws, bool backward) {
     VarSched v;
-    v.items = reinterpret_cast<const VarItem *>(static_cast<char *>(ws) +
-                                                var_layout(a.num_seqs, a.rows, a.Hq, a.D, a.dtype, backward).items);
+    char *base = static_cast<char *>(ws);
+    v.items = reinterpret_cast<const VarItem *>(base + l.items);
     v.count = static_cast<const int *>(ws);
+    v.next = static_cast<int *>(ws) + 32;  // another 128-byte line than the count, which every CTA reads
+    v.max_slots = l.slots;
+    v.max_items = l.max_items;
+    v.cut = l.slots > 0 ? reinterpret_cast<const int *>(base + l.cut) : nullptr;
+    v.parts = reinterpret_cast<float *>(base + l.parts);
     v.unit = var_unit(a.D, a.dtype, backward);
     v.rows = a.rows;
     v.pad_rows = var_pad_rows(a.rows, a.num_seqs);
@@ -502,7 +526,16 @@ forge_status run_plan(const VarArgs &a, const VarSched &v, bool backward, void *
     p.backward = backward;
     p.items = const_cast<VarItem *>(v.items);
     p.count = const_cast<int *>(v.count);
-    p.max_items = var_max_items(a.rows, a.num_seqs, v.unit);
+    p.next = v.next;
+    p.max_items = v.max_items;
+    p.ctas = v.cut != nullptr ? sm_count() : 0;
+    p.per_tile = var_per_tile(a.Hkv, a.D);
+    // at least six steps a part, below which its loads and its epilogue cost more
+    // than the balance gains
+    const int G = a.Hq / a.Hkv;
+    p.min_part = G >= 3 ? 2 : (6 + G - 1) / G;
+    p.max_slots = v.max_slots;
+    p.cut = const_cast<int *>(v.cut);
     for (int i = 0; i < 3; i++) {
         p.tail[i] = clear ? static_cast<uint4 *>(tail[i]) : nullptr;
         p.tail_chunks[i] = tail_heads[i] * a.D * (a.dtype == FORGE_DTYPE_BF16 ? 2 : 4) / 16;
@@ -538,7 +571,7 @@ forge_status var_fwd_tc(const VarArgs &a, const VarSched &v, void *o, void *o_re
         return FORGE_ERR_CUDA;
     }
     const FwdParams p = var_fwd_params(a, v, o, o_res, lse);
-    const long long items = (long long)var_max_items(a.rows, a.num_seqs, v.unit) * a.Hq;
+    const long long items = (long long)v.max_items * a.Hq;
     if constexpr (D == 256) {
         using C = FwdTc<D>;
         if (set_smem(fwd_tc_kernel<D, D, true>, C::SMEM) != FORGE_OK) return FORGE_ERR_CUDA;
@@ -546,16 +579,12 @@ forge_status var_fwd_tc(const VarArgs &a, const VarSched &v, void *o, void *o_re
                           p);
     } else {
         using C = Fwd2Tc<D>;
-        if (set_smem(fwd2_tc_kernel<D, true, true>, C::SMEM) != FORGE_OK ||
-            set_smem(fwd2_tc_kernel<D, false, true>, C::SMEM) != FORGE_OK)
-            return FORGE_ERR_CUDA;
-        // as the dense forward: persistent for short sequences
-        const bool persistent = a.rows / a.num_seqs <= 1024;
-        if (persistent)
-            return launch_pdl(fwd2_tc_kernel<D, true, true>, dim3((unsigned)(items < sm_count() ? items : sm_count())),
-                              dim3(C::THREADS), C::SMEM, a.st, mq, mk, mv, mo, p);
-        return launch_pdl(fwd2_tc_kernel<D, false, true>, dim3((unsigned)items), dim3(C::THREADS), C::SMEM, a.st, mq, mk,
-                          mv, mo, p);
+        if (set_smem(fwd2_tc_kernel<D, true, true>, C::SMEM) != FORGE_OK) return FORGE_ERR_CUDA;
+        // one CTA an SM for every length: its items are handed out as CTAs get done
+        // (one CTA per item was 218 against 211 us on 8K mixed rows, 28 heads, and 835
+        // against 827 us on 16K rows in three sequences, window 4096)
+        return launch_pdl(fwd2_tc_kernel<D, true, true>, dim3((unsigned)(items < sm_count() ? items : sm_count())),
+                          dim3(C::THREADS), C::SMEM, a.st, mq, mk, mv, mo, p);
     }
 }
 
@@ -581,7 +610,7 @@ forge_status var_fwd_f32(const VarArgs &a, const VarSched &v, void *o, float *ls
     p.o = static_cast<float *>(o);
     p.lse = lse;
     if (set_smem(varlen_f32_fwd<D>, vf_fwd_smem<D>()) != FORGE_OK) return FORGE_ERR_CUDA;
-    const unsigned grid = (unsigned)var_max_items(a.rows, a.num_seqs, v.unit) * (unsigned)a.Hq;
+    const unsigned grid = (unsigned)v.max_items * (unsigned)a.Hq;
     return launch_pdl(varlen_f32_fwd<D>, dim3(grid), dim3(kVfThreads), vf_fwd_smem<D>(), a.st, p);
 }
 
@@ -590,8 +619,11 @@ forge_status var_fwd_f32(const VarArgs &a, const VarSched &v, void *o, float *ls
 template <typename T_, int D>
 forge_status var_bwd(const VarArgs &a, const VarSched &v, const void *o, const void *o_res, const float *lse, const void *dO, void *dq,
                      void *dk, void *dv, float *dsink, float *delta, float *acc) {
-    const int items = var_max_items(a.rows, a.num_seqs, v.unit);
-    forge_status s = launch_pdl(varlen_preprocess<T_, D>, dim3((unsigned)items * (unsigned)a.Hq), dim3(256), 0, a.st,
+    const int items = v.max_items;
+    // the stages around the main kernels: as many blocks as the SMs hold, each taking its share
+    const long long pairs = (long long)items * a.Hq;
+    const unsigned wave = (unsigned)(pairs < 8ll * sm_count() ? pairs : 8ll * sm_count());
+    forge_status s = launch_pdl(varlen_preprocess<T_, D>, dim3(wave), dim3(256), 0, a.st,
                                 static_cast<const T_ *>(o), static_cast<const T_ *>(o_res), static_cast<const T_ *>(dO),
                                 delta, acc, a.Hq, v);
     if (s != FORGE_OK) return s;
@@ -645,8 +677,8 @@ forge_status var_bwd(const VarArgs &a, const VarSched &v, const void *o, const v
         s = launch_pdl(bwd_tc_kernel<D, true>, dim3((unsigned)(work < sm_count() ? work : sm_count())), dim3(C::THREADS),
                        C::SMEM, a.st, mq, mk, mv, mdo, macc, p);
         if (s != FORGE_OK) return s;
-        return launch_pdl(varlen_finalize_dq<D>, dim3((unsigned)items * (unsigned)a.Hq), dim3(256), 0, a.st,
-                          static_cast<const float *>(acc), static_cast<__nv_bfloat16 *>(dq), a.Hq, v);
+        return launch_pdl(varlen_finalize<D>, dim3(wave), dim3(256), 0, a.st,
+                          static_cast<const float *>(acc), static_cast<__nv_bfloat16 *>(dq), p.dk, p.dv, a.Hq, a.Hkv, v);
     }
 }
 
@@ -1196,12 +1228,12 @@ forge_status forge_attn_decode(const void *q, const void *k_cache, const void *v
 
 size_t forge_attn_varlen_fwd_workspace_size(int num_seqs, int rows, int Hq, int Hkv, int D, forge_dtype dtype) {
     if (check_var_sizes(num_seqs, rows, Hq, Hkv, D, dtype) != FORGE_OK) return 0;
-    return var_layout(num_seqs, rows, Hq, D, dtype, false).bytes;
+    return var_layout(num_seqs, rows, Hq, Hkv, D, dtype, false).bytes;
 }
 
 size_t forge_attn_varlen_bwd_workspace_size(int num_seqs, int rows, int Hq, int Hkv, int D, forge_dtype dtype) {
     if (check_var_sizes(num_seqs, rows, Hq, Hkv, D, dtype) != FORGE_OK) return 0;
-    return var_layout(num_seqs, rows, Hq, D, dtype, true).bytes;
+    return var_layout(num_seqs, rows, Hq, Hkv, D, dtype, true).bytes;
 }
 
 forge_status forge_attn_varlen_fwd(const void *q, const void *k, const void *v, void *o, void *o_res, float *lse,
@@ -1218,7 +1250,7 @@ forge_status forge_attn_varlen_fwd(const void *q, const void *k, const void *v, 
         workspace_bytes < forge_attn_varlen_fwd_workspace_size(num_seqs, rows, Hq, Hkv, D, dtype))
         return FORGE_ERR_WORKSPACE;
     a.window = effective_window(window, rows);
-    const VarSched sched = var_sched(a, workspace, false);
+    const VarSched sched = var_sched(a, var_layout(num_seqs, rows, Hq, Hkv, D, dtype, false), workspace, false);
     void *const tail[3] = {o, nullptr, nullptr};
     const int heads[3] = {Hq, 0, 0};
     if ((s = run_plan(a, sched, false, tail, heads, lse, clear_tail != 0)) != FORGE_OK) return s;
@@ -1249,8 +1281,8 @@ forge_status forge_attn_varlen_bwd(const void *q, const void *k, const void *v, 
         workspace_bytes < forge_attn_varlen_bwd_workspace_size(num_seqs, rows, Hq, Hkv, D, dtype))
         return FORGE_ERR_WORKSPACE;
     a.window = effective_window(window, rows);
-    const VarSched sched = var_sched(a, workspace, true);
-    const VarLayout l = var_layout(num_seqs, rows, Hq, D, dtype, true);
+    const VarLayout l = var_layout(num_seqs, rows, Hq, Hkv, D, dtype, true);
+    const VarSched sched = var_sched(a, l, workspace, true);
     float *delta = reinterpret_cast<float *>(static_cast<char *>(workspace) + l.delta);
     float *acc = dtype == FORGE_DTYPE_BF16 ? reinterpret_cast<float *>(static_cast<char *>(workspace) + l.acc) : nullptr;
     void *const tail[3] = {dq, dk, dv};

@@ -97,10 +97,12 @@ struct BwdTc {
     // LSE/Delta rows. The tiles need 1024-byte alignment (128-byte swizzle); the
     // dynamic shared memory base is 1024-aligned in practice, and SLACK covers
     // a base that is not wherever the budget leaves room (the kernel checks).
-    static constexpr uint32_t OFF_TMEM_SLOT = 240, OFF_ABORT = 244;
+    static constexpr uint32_t OFF_ITEM = 352;  // [kVarRing] packed sequences: item numbers
+    static constexpr uint32_t OFF_REQ = 384;   // [NREQ] packed sequences: requests to clear rows
+    static constexpr uint32_t OFF_TMEM_SLOT = 416, OFF_ABORT = 420;
     // LSE and Delta rows of a step, in slot (step % 2): with one Q/dO stage the
     // next step's rows arrive while phase B still reads this step's Delta
-    static constexpr uint32_t OFF_LSE = 256;                        // [2][BM] f32, -LSE * log2(e)
+    static constexpr uint32_t OFF_LSE = 512;                        // [2][BM] f32, -LSE * log2(e)
     static constexpr uint32_t OFF_DLT = OFF_LSE + 2 * BM * 4;       // [2][BM] f32, -scale * Delta
     static constexpr uint32_t CTRL = OFF_DLT + 2 * BM * 4;
     static constexpr uint32_t SLACK = (TILES + CTRL + 1024 <= 232448) ? 1024 : 0;
@@ -148,13 +150,20 @@ struct BwdTc {
                                                           // warps unless DV_BY_DRAIN)
     static constexpr int B_QSH_FULL = B_EPI_DONE + 1;    // the Q half for dK has landed (QSHADOW)
     static constexpr int B_QSH_EMPTY = B_QSH_FULL + 1;   // ... and dK has read it
-    // packed sequences: the same stages with the rows past the sequence's end set
-    // to zero (two warps)
+    // packed sequences: a stage whose rows past the sequence's end two warps have set
+    // to zero; completes a phase only for stages with such rows
     static constexpr int B_KV_FIX = B_QSH_EMPTY + 1;     // [NKV]
     static constexpr int B_Q_FIX = B_KV_FIX + NKV;       // [QST]
     static constexpr int B_QSH_FIX = B_Q_FIX + QST;
-    static constexpr int NBAR = B_QSH_FIX + 1;
-    static_assert(NBAR * 8 <= (int)OFF_TMEM_SLOT, "control block");
+    static constexpr int B_ITEM = B_QSH_FIX + 1;         // [kVarRing] the next item's number is there
+    // requests to the two warps, in a ring: at most one per stage (NKV + QST + 1)
+    // is open, so that a ring of eight never wraps onto one
+    static constexpr int NREQ = 8;
+    static constexpr int B_REQ = B_ITEM + kVarRing;      // [NREQ]
+    static constexpr int NBAR = B_REQ + NREQ;
+    static_assert(NKV + QST + 1 < NREQ, "open requests");
+    static_assert(NBAR * 8 <= (int)OFF_ITEM, "control block");
+    static_assert(!QSHADOW || DH == 128, "the Q shadow has two column blocks");
 };
 
 // A work item: (key tile n, batch b, KV head, head-dim half h), heaviest (n = 0)
@@ -163,6 +172,7 @@ struct BwdTc {
 struct BwdItem {
     int h, bkv, b, hkv, k0, m_lo, nm, steps;
     int row0, T, pad0;  // the sequence's first row, its length, and its first padded row
+    int slot;           // of the partial sums (packed sequences); -1: the whole key tile
 };
 
 struct BwdParams {
@@ -224,6 +234,19 @@ __device__ __forceinline__ void bwd_row_out(uint32_t taddr, __nv_bfloat16 *row, 
 #pragma unroll
             for (int e = 0; e < 4; e++) dst[e] = make_uint4(w16[4 * e], w16[4 * e + 1], w16[4 * e + 2], w16[4 * e + 3]);
         }
+    }
+}
+
+// The same as f32, every row: a part's sum
+__device__ __forceinline__ void bwd_row_part(uint32_t taddr, float *row, int c_lo, int c_hi) {
+#pragma unroll 1
+    for (int c0 = c_lo; c0 < c_hi; c0 += 32) {
+        uint32_t o[32];
+        tmem_ld32(taddr + (uint32_t)c0, o);
+        tmem_ld_wait(o);
+        uint4 *dst = reinterpret_cast<uint4 *>(row + c0);
+#pragma unroll
+        for (int e = 0; e < 8; e++) dst[e] = make_uint4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
     }
 }
 
@@ -383,8 +406,9 @@ __device__ __forceinline__ BwdItem bwd_item(int w, const P &p) {
     int n = w / per_n;
     it.row0 = it.pad0 = 0;
     it.T = p.T;
+    VarItem t = {};
     if constexpr (VAR) {
-        const VarItem t = var_item(p.var, n);
+        t = var_item_part(p.var, n);
         n = t.tile;
         it.row0 = t.row0;
         it.T = t.len;
@@ -399,6 +423,13 @@ __device__ __forceinline__ BwdItem bwd_item(int w, const P &p) {
     it.m_lo = it.k0 / C::BM;
     const int q_last = p.window > 0 ? min(it.T - 1, it.k0 + C::BN - 1 + p.window - 1) : it.T - 1;
     it.nm = q_last / C::BM - it.m_lo + 1;
+    it.slot = -1;
+    if constexpr (VAR) {
+        constexpr int R = 128 / C::BM;  // the schedule counts query tiles of 128 rows
+        it.m_lo += t.m0 * R;
+        it.nm = min(t.nm * R, it.nm - t.m0 * R);
+        if (t.parts > 1) it.slot = t.slot;
+    }
     it.steps = (p.Hq / p.Hkv) * it.nm;
     return it;
 }
@@ -408,9 +439,11 @@ __device__ __forceinline__ BwdItem bwd_item(int w, const P &p) {
 // pipeline carries on from one item into the next; TMEM is allocated once.
 // VAR: packed sequences. Items come from the schedule and the tensor maps cover
 // [heads][rows][D] views of the packed tensors. The last tile of a sequence brings
-// rows of the next one along: warps 14 and 15 set them to zero in K, V, Q and dO
-// before the MMA warp may read the stage (it waits on their barriers), which
-// leaves the rest of the kernel the tiles it would have at a tensor's end.
+// rows of the next one along: the load warp then asks warps 14 and 15 to set them
+// to zero in K, V, Q and dO, and the MMA warp waits for that instead of the loads (only
+// there: a wait on two more warps in every step cost 4.1 instead of 3.0 us a step at
+// head dim 256, whose single stage has no load ahead). The rest of the kernel sees
+// the tiles it would have at a tensor's end.
 template <int D, bool VAR = false>
 __global__ void __launch_bounds__(512, 1)
     bwd_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
@@ -439,7 +472,30 @@ __global__ void __launch_bounds__(512, 1)
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     int nitems = p.num_kt * p.B * p.Hkv * C::NSPLIT;
     const int G = p.Hq / p.Hkv;
-    auto item_of = [&](int pass) -> int { return snake_item(pass, (int)blockIdx.x, (int)gridDim.x); };
+    // the item of a pass: the snake order, or (packed sequences) the number that the
+    // load warp took; nitems or more: none left, -1: abort
+    volatile int *sItem = reinterpret_cast<volatile int *>(ctrl_p + C::OFF_ITEM);
+    volatile int *sReq = reinterpret_cast<volatile int *>(ctrl_p + C::OFF_REQ);
+    // (item_of: by one thread; item_of_warp: by a whole warp, with one answer)
+    auto item_of = [&](int pass) -> int {
+        if constexpr (VAR) {
+            if (pass == 0) return (int)blockIdx.x;
+            if (!mbar_wait(bar(C::B_ITEM + pass % kVarRing), (uint32_t)((pass / kVarRing) & 1), abort_flag)) return -1;
+            return sItem[pass % kVarRing];
+        } else {
+            return snake_item(pass, (int)blockIdx.x, (int)gridDim.x);
+        }
+    };
+    auto item_of_warp = [&](int pass) -> int {
+        if constexpr (VAR) {
+            if (pass == 0) return (int)blockIdx.x;
+            if (!mbar_wait_warp(bar(C::B_ITEM + pass % kVarRing), (uint32_t)((pass / kVarRing) & 1), abort_flag))
+                return -1;
+            return sItem[pass % kVarRing];
+        } else {
+            return snake_item(pass, (int)blockIdx.x, (int)gridDim.x);
+        }
+    };
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < C::NKV; s++) {
@@ -464,7 +520,9 @@ __global__ void __launch_bounds__(512, 1)
         if constexpr (VAR) {
             for (int s = 0; s < C::NKV; s++) mbar_init(bar(C::B_KV_FIX + s), 2);
             for (int s = 0; s < C::QST; s++) mbar_init(bar(C::B_Q_FIX + s), 2);
-            mbar_init(bar(C::B_QSH_FIX), 1);
+            mbar_init(bar(C::B_QSH_FIX), 2);
+            for (int s = 0; s < C::NREQ; s++) mbar_init(bar(C::B_REQ + s), 1);
+            for (int s = 0; s < kVarRing; s++) mbar_init(bar(C::B_ITEM + s), 1);
         }
         *abort_flag = 0;
         fence_mbar_init();
@@ -494,12 +552,35 @@ __global__ void __launch_bounds__(512, 1)
             int issued = 0, kv_issued = 0, qsh_issued = 0;  // loads issued (for the abort drain)
             bool ok = true;
             int gs = 0;  // step count over all of this CTA's items
+            if (VAR && lane == 0) mbar_arrive(bar(C::B_ITEM));  // pass 0
+            // asks for rows [valid, ..) of a stage to be cleared once its load, phase
+            // `parity` of barrier `full`, has landed. kind 0: K and V, 1: Q and dO, 2: the
+            // Q shadow; negative: no more requests.
+            int nreq = 0;
+            auto request = [&](int kind, int stage, uint32_t parity, int valid) {
+                if (lane == 0) {
+                    sReq[nreq % C::NREQ] = kind < 0 ? -1 : (kind << 16) | (stage << 12) | ((int)parity << 8) | valid;
+                    mbar_arrive(bar(C::B_REQ + nreq % C::NREQ));
+                }
+                nreq++;
+            };
             for (int pass = 0; ok; pass++) {
-                const int w = item_of(pass);
+                const int w = item_of_warp(pass);
+                if (VAR && w < 0) {
+                    ok = false;
+                    break;
+                }
                 if (w >= nitems) break;
                 const BwdItem I = bwd_item<C, VAR>(w, p);
-                // this CTA's last item: the next kernel may start launching
-                if (lane == 0 && item_of(pass + 1) >= nitems) griddep_launch_dependents();
+                // packed sequences: the next item's number is on its way while this
+                // one's first loads are issued
+                int next = 0;
+                if constexpr (VAR) {
+                    if (lane == 0) next = (int)gridDim.x + atomicAdd(p.var.next, 1);
+                } else {
+                    // this CTA's last item: the next kernel may start launching
+                    if (lane == 0 && item_of(pass + 1) >= nitems) griddep_launch_dependents();
+                }
                 // K, V of the item into buffer pass % NKV once the item that used it
                 // NKV items ago has no product left reading it
                 const int kvs = pass % C::NKV;
@@ -516,6 +597,7 @@ __global__ void __launch_bounds__(512, 1)
                     }
                 }
                 kv_issued++;
+                if (VAR && I.T - I.k0 < C::BN) request(0, kvs, (uint32_t)((pass / C::NKV) & 1), I.T - I.k0);
                 BwdStep sp(I, p.q_desc);
                 for (int i = 0; i < I.steps; i++, gs++, sp.next(I, G, p.q_desc)) {
                     const int st = gs % C::QST;
@@ -546,12 +628,18 @@ __global__ void __launch_bounds__(512, 1)
                         }
                     }
                     issued++;
+                    if (VAR && i == 0 && lane == 0) {
+                        sItem[(pass + 1) % kVarRing] = next;
+                        mbar_arrive(bar(C::B_ITEM + (pass + 1) % kVarRing));
+                        if (next >= nitems) griddep_launch_dependents();
+                    }
 #pragma unroll
                     for (int r = 0; r < C::BM / 32; r++) {
                         sLSE[(gs & 1) * C::BM + lane + 32 * r] = -lv[r];
                         sDLT[(gs & 1) * C::BM + lane + 32 * r] = -dv[r];
                     }
                     mbar_arrive(bar(C::B_Q_FULL + st));
+                    if (VAR && I.T - m * C::BM < C::BM) request(1, st, ph, I.T - m * C::BM);
                     if constexpr (C::QSHADOW) {
                         // this CTA's half of Q(gs) again, for dK(gs), once dK(gs - 1) has
                         // read the previous one
@@ -566,9 +654,11 @@ __global__ void __launch_bounds__(512, 1)
                                             I.row0 + m * C::BM, bhq);
                         }
                         qsh_issued++;
+                        if (VAR && I.T - m * C::BM < C::BM) request(2, 0, (uint32_t)(gs & 1), I.T - m * C::BM);
                     }
                 }
             }
+            if (VAR && ok) request(-1, 0, 0, 0);
             if (!ok && lane == 0) {
                 // let the copies already issued land before the CTA exits
                 for (int back = 1; back <= min(kv_issued, C::NKV); back++) {
@@ -585,9 +675,21 @@ __global__ void __launch_bounds__(512, 1)
         } else if (warp == C::W_MMA && lane == 0) {
             // ------------------------------------------------------ MMA issuer
             // S^T(j) = K Q(j)^T once stage j % QST holds Q(j) (j counts steps over all items)
-            auto wait_q = [&](int j) -> bool {
-                if (!mbar_wait(bar((VAR ? C::B_Q_FIX : C::B_Q_FULL) + j % C::QST), (uint32_t)((j / C::QST) & 1), abort_flag))
-                    return false;
+            // (fixed: one phase bit for each barrier of cleared stages; ragged: the step's
+            // query tile runs past the sequence's end)
+            uint32_t fixed = 0;
+            auto wait_fix = [&](int b) -> bool {
+                const uint32_t bit = 1u << (b - C::B_KV_FIX);
+                const bool done = mbar_wait(bar(b), (fixed & bit) ? 1u : 0u, abort_flag);
+                fixed ^= bit;
+                return done;
+            };
+            auto wait_q = [&](int j, bool ragged) -> bool {
+                if (VAR && ragged) {
+                    if (!wait_fix(C::B_Q_FIX + j % C::QST)) return false;
+                } else {
+                    if (!mbar_wait(bar(C::B_Q_FULL + j % C::QST), (uint32_t)((j / C::QST) & 1), abort_flag)) return false;
+                }
                 tc_fence_after();
                 return true;
             };
@@ -596,17 +698,27 @@ __global__ void __launch_bounds__(512, 1)
             int gs = 0, pass = 0;
             for (; ok; pass++) {
                 const int w = item_of(pass);
+                if (VAR && w < 0) {
+                    ok = false;
+                    break;
+                }
                 if (w >= nitems) break;
                 const BwdItem I = bwd_item<C, VAR>(w, p);
                 const int kvs = pass % C::NKV;
                 const uint32_t sK = sK0 + (uint32_t)kvs * C::KVB, sV = sK + C::TK;
                 const uint32_t h_q = (uint32_t)I.h * (C::DH / 64) * C::CBQ;  // column-block offset of half h
                 const uint32_t h_k = (uint32_t)I.h * (C::DH / 64) * C::CBK;
-                if (!(ok = mbar_wait(bar((VAR ? C::B_KV_FIX : C::B_KV_FULL) + kvs), (uint32_t)((pass / C::NKV) & 1),
-                                     abort_flag)))
-                    break;
+                if (VAR && I.T - I.k0 < C::BN) {
+                    if (!(ok = wait_fix(C::B_KV_FIX + kvs))) break;
+                } else {
+                    if (!(ok = mbar_wait(bar(C::B_KV_FULL + kvs), (uint32_t)((pass / C::NKV) & 1), abort_flag))) break;
+                }
                 tc_fence_after();
-                if (!(ok = wait_q(gs))) break;
+                // step order of the item, one step ahead: which query tiles are ragged
+                BwdStep sp(I, p.q_desc);
+                auto ragged = [&]() -> bool { return VAR && I.T - sp.m * C::BM < C::BM; };
+                bool now = ragged();  // this step's
+                if (!(ok = wait_q(gs, now))) break;
                 bwd_mma_kq<C>(tmem + C::COL_S, sK, sQ0 + (gs % C::QST) * C::TQ);
                 tc_commit(bar(C::B_S_FULL));
                 // in the aliased layout dP^T overwrites the previous dQ^T: wait for its drain
@@ -620,6 +732,11 @@ __global__ void __launch_bounds__(512, 1)
                     const int st = gs % C::QST;
                     const uint32_t sQ = sQ0 + st * C::TQ, sdO = sdO0 + st * C::TQ;
                     const bool more = i + 1 < I.steps;
+                    const bool here = now;
+                    if constexpr (VAR) {
+                        sp.next(I, G, p.q_desc);
+                        now = more && ragged();  // from here on the next step's
+                    }
                     // dV += P^T dO, P^T from TMEM (phase A of step gs)
                     if (!(ok = mbar_wait(bar(C::B_P_FULL), (uint32_t)(gs & 1), abort_flag))) break;
                     tc_fence_after();
@@ -638,7 +755,7 @@ __global__ void __launch_bounds__(512, 1)
                     // only be loaded once dK(gs) has read Q(gs), so S^T(gs + 1) then comes
                     // after dQ(gs).
                     if (EARLY_S && more) {
-                        if (!(ok = wait_q(gs + 1))) break;
+                        if (!(ok = wait_q(gs + 1, now))) break;
                         bwd_mma_kq<C>(tmem + C::COL_S, sK, sQ0 + ((gs + 1) % C::QST) * C::TQ);
                         tc_commit(bar(C::B_S_FULL));
                     }
@@ -650,8 +767,11 @@ __global__ void __launch_bounds__(512, 1)
                     if (!(ok = mbar_wait(bar(C::B_DS_FULL), (uint32_t)(gs & 1), abort_flag))) break;
                     tc_fence_after();
                     if constexpr (C::QSHADOW) {
-                        if (!(ok = mbar_wait(bar(VAR ? C::B_QSH_FIX : C::B_QSH_FULL), (uint32_t)(gs & 1), abort_flag)))
-                            break;
+                        if (VAR && here) {
+                            if (!(ok = wait_fix(C::B_QSH_FIX))) break;
+                        } else {
+                            if (!(ok = mbar_wait(bar(C::B_QSH_FULL), (uint32_t)(gs & 1), abort_flag))) break;
+                        }
                         tc_fence_after();
                         bwd_mma_dk<C>(tmem, sdS, sQsh, i == 0);
                         tc_commit(bar(C::B_QSH_EMPTY));
@@ -669,7 +789,7 @@ __global__ void __launch_bounds__(512, 1)
                     tc_commit(bar(C::B_DQ_FULL));
                     tc_commit(bar(C::B_DS_EMPTY));
                     if (!EARLY_S && more) {
-                        if (!(ok = wait_q(gs + 1))) break;
+                        if (!(ok = wait_q(gs + 1, now))) break;
                         bwd_mma_kq<C>(tmem + C::COL_S, sK, sQ0 + ((gs + 1) % C::QST) * C::TQ);
                         tc_commit(bar(C::B_S_FULL));
                     }
@@ -695,45 +815,25 @@ __global__ void __launch_bounds__(512, 1)
             }
         } else if (VAR && warp > C::W_MMA) {
             // -------------------- packed sequences: zero the rows past the end
-            // (warp 14: K, Q and the Q shadow; warp 15: V and dO). They arrive for
-            // every stage, zeroed or not, so phases count stages as elsewhere.
-            const bool second = warp != C::W_MMA + 1;
-            bool ok = true;
-            int gs = 0;
-            for (int pass = 0; ok; pass++) {
-                const int w = item_of(pass);
-                if (w >= nitems) break;
-                const BwdItem I = bwd_item<C, VAR>(w, p);
-                const int kvs = pass % C::NKV;
-                if (!(ok = mbar_wait_warp(bar(C::B_KV_FULL + kvs), (uint32_t)((pass / C::NKV) & 1), abort_flag))) break;
-                if (I.T - I.k0 < C::BN) {
-                    zero_tail_rows<C::BN, C::NCB, 32>(sK0 + (uint32_t)kvs * C::KVB + (second ? C::TK : 0u), C::CBK,
-                                                      I.T - I.k0, lane);
-                    fence_proxy_async_smem();
-                }
+            // (warp 14: K, Q, the Q shadow's first 64 columns; warp 15: V, dO, its others)
+            const uint32_t second = warp == C::W_MMA + 1 ? 0u : 1u;
+            for (int n = 0;; n++) {
+                if (!mbar_wait_warp(bar(C::B_REQ + n % C::NREQ), (uint32_t)((n / C::NREQ) & 1), abort_flag)) break;
+                const int r = sReq[n % C::NREQ];
+                if (r < 0) break;
+                const int kind = r >> 16, stage = (r >> 12) & 15, valid = r & 255;
+                const int full = kind == 0 ? C::B_KV_FULL + stage : kind == 1 ? C::B_Q_FULL + stage : C::B_QSH_FULL;
+                if (!mbar_wait_warp(bar(full), (uint32_t)((r >> 8) & 1), abort_flag)) break;
+                if (kind == 0)
+                    zero_tail_rows<C::BN, C::NCB, 32>(sK0 + (uint32_t)stage * C::KVB + second * C::TK, C::CBK, valid, lane);
+                else if (kind == 1)
+                    zero_tail_rows<C::BM, C::NCB, 32>((second ? sdO0 : sQ0) + (uint32_t)stage * C::TQ, C::CBQ, valid, lane);
+                else
+                    zero_tail_rows<C::BM, 1, 32>(sQsh + second * C::CBQ, C::CBQ, valid, lane);
+                fence_proxy_async_smem();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(bar(C::B_KV_FIX + kvs));
-                BwdStep sp(I, p.q_desc);
-                for (int i = 0; i < I.steps; i++, gs++, sp.next(I, G, p.q_desc)) {
-                    const int st = gs % C::QST;
-                    const int end = I.T - sp.m * C::BM;
-                    if (!(ok = mbar_wait_warp(bar(C::B_Q_FULL + st), (uint32_t)((gs / C::QST) & 1), abort_flag))) break;
-                    if (end < C::BM) {
-                        zero_tail_rows<C::BM, C::NCB, 32>((second ? sdO0 : sQ0) + st * C::TQ, C::CBQ, end, lane);
-                        fence_proxy_async_smem();
-                    }
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(bar(C::B_Q_FIX + st));
-                    if (C::QSHADOW && !second) {
-                        if (!(ok = mbar_wait_warp(bar(C::B_QSH_FULL), (uint32_t)(gs & 1), abort_flag))) break;
-                        if (end < C::BM) {
-                            zero_tail_rows<C::BM, C::DH / 64, 32>(sQsh, C::CBQ, end, lane);
-                            fence_proxy_async_smem();
-                        }
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(bar(C::B_QSH_FIX));
-                    }
-                }
+                if (lane == 0)
+                    mbar_arrive(bar(kind == 0 ? C::B_KV_FIX + stage : kind == 1 ? C::B_Q_FIX + stage : C::B_QSH_FIX));
             }
         }
     } else if (warp < C::W_DRAIN) {
@@ -746,7 +846,11 @@ __global__ void __launch_bounds__(512, 1)
         bool ok = true;
         int gs = 0;
         for (int pass = 0; ok; pass++) {
-            const int w = item_of(pass);
+            const int w = item_of_warp(pass);
+            if (VAR && w < 0) {
+                ok = false;
+                break;
+            }
             if (w >= nitems) break;
             const BwdItem I = bwd_item<C, VAR>(w, p);
             const int kj = I.k0 + kr;
@@ -807,10 +911,19 @@ __global__ void __launch_bounds__(512, 1)
                 // epilogue of the item: dV rows, this warp's half of the columns
                 if (!(ok = mbar_wait_warp(bar(C::B_KDONE), (uint32_t)(pass & 1), abort_flag))) break;
                 tc_fence_after();
-                const size_t kr_c = (size_t)min(kj, I.T - 1);
-                __nv_bfloat16 *row =
-                    p.dv + (VAR ? (I.row0 + kr_c) * p.Hkv + I.hkv : (size_t)I.bkv * p.T + kr_c) * D + I.h * C::DH;
-                bwd_row_out(tmem + lane_base + C::COL_DV, row, hc * (C::DH / 2), (hc + 1) * (C::DH / 2), kj < I.T);
+                // packed sequences: read the item again instead of holding it over the steps
+                const BwdItem E = VAR ? bwd_item<C, VAR>(w, p) : I;
+                const size_t kr_c = (size_t)min(E.k0 + kr, E.T - 1);
+                if (VAR && E.slot >= 0) {
+                    bwd_row_part(tmem + lane_base + C::COL_DV,
+                                 p.var.parts + ((((size_t)E.slot * p.Hkv + E.hkv) * 2 + 1) * 128 + kr) * D + E.h * C::DH,
+                                 hc * (C::DH / 2), (hc + 1) * (C::DH / 2));
+                } else {
+                    __nv_bfloat16 *row =
+                        p.dv + (VAR ? (E.row0 + kr_c) * p.Hkv + E.hkv : (size_t)E.bkv * p.T + kr_c) * D + E.h * C::DH;
+                    bwd_row_out(tmem + lane_base + C::COL_DV, row, hc * (C::DH / 2), (hc + 1) * (C::DH / 2),
+                                E.k0 + kr < E.T);
+                }
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(bar(C::B_EPI_DONE));
@@ -824,7 +937,11 @@ __global__ void __launch_bounds__(512, 1)
         bool ok = true;
         int gs = 0;
         for (int pass = 0; ok; pass++) {
-            const int w = item_of(pass);
+            const int w = item_of_warp(pass);
+            if (VAR && w < 0) {
+                ok = false;
+                break;
+            }
             if (w >= nitems) break;
             const BwdItem I = bwd_item<C, VAR>(w, p);
             BwdStep sp(I, p.q_desc);
@@ -895,11 +1012,18 @@ __global__ void __launch_bounds__(512, 1)
             // epilogue of the item: dK rows (and dV rows where the drain warps take them)
             if (!(ok = mbar_wait_warp(bar(C::B_KDONE), (uint32_t)(pass & 1), abort_flag))) break;
             tc_fence_after();
-            const int kj = I.k0 + t;
-            const size_t kr_c = (size_t)min(kj, I.T - 1);
-            const size_t roff = (VAR ? (I.row0 + kr_c) * p.Hkv + I.hkv : (size_t)I.bkv * p.T + kr_c) * D + I.h * C::DH;
-            bwd_row_out(tmem + lane_base + C::COL_DK, p.dk + roff, 0, C::DH, kj < I.T);
-            if constexpr (C::DV_BY_DRAIN) bwd_row_out(tmem + lane_base + C::COL_DV, p.dv + roff, 0, C::DH, kj < I.T);
+            const BwdItem E = VAR ? bwd_item<C, VAR>(w, p) : I;
+            const int kj = E.k0 + t;
+            const size_t kr_c = (size_t)min(kj, E.T - 1);
+            const size_t roff = (VAR ? (E.row0 + kr_c) * p.Hkv + E.hkv : (size_t)E.bkv * p.T + kr_c) * D + E.h * C::DH;
+            if (VAR && E.slot >= 0) {
+                float *part = p.var.parts + (((size_t)E.slot * p.Hkv + E.hkv) * 256 + t) * D + E.h * C::DH;
+                bwd_row_part(tmem + lane_base + C::COL_DK, part, 0, C::DH);
+                if constexpr (C::DV_BY_DRAIN) bwd_row_part(tmem + lane_base + C::COL_DV, part + 128 * D, 0, C::DH);
+            } else {
+                bwd_row_out(tmem + lane_base + C::COL_DK, p.dk + roff, 0, C::DH, kj < E.T);
+                if constexpr (C::DV_BY_DRAIN) bwd_row_out(tmem + lane_base + C::COL_DV, p.dv + roff, 0, C::DH, kj < E.T);
+            }
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(bar(C::B_EPI_DONE));

@@ -68,8 +68,10 @@ struct Fwd2Tc {
     static constexpr int B_P_FULL = B_S_FULL + 2;         // [2]
     static constexpr int B_O_FINAL = B_P_FULL + 2;        // [2]
     static constexpr int B_O_EMPTY = B_O_FINAL + 2;       // [2] O_x read out of TMEM
-    static constexpr int NBAR = B_O_EMPTY + 2;
+    static constexpr int B_ITEM = B_O_EMPTY + 2;          // [kVarRing] packed sequences: the next item's number is there
+    static constexpr int NBAR = B_ITEM + kVarRing;
     static constexpr uint32_t OFF_TMEM_SLOT = 512, OFF_ABORT = 516;
+    static constexpr uint32_t OFF_ITEM = 528;             // [kVarRing] item numbers
     static constexpr int EMU_MASK = 7;                 // pairs with (c & 7) == 7 use the FMA-pipe exp2
     static_assert(NBAR * 8 <= 512, "control block");
     static_assert(SMEM <= 232448, "shared memory");
@@ -188,8 +190,27 @@ __global__ void __launch_bounds__(384, 1)
 
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     int nitems = ((p.num_qt + 1) / 2) * p.B * p.Hq;
+    volatile int *sItem = reinterpret_cast<volatile int *>(smem_raw + C::OFF_ITEM);
     auto item_of = [&](int pass) -> int {
-        return PERSIST ? snake_item(pass, (int)blockIdx.x, (int)gridDim.x) : (pass == 0 ? (int)blockIdx.x : nitems);
+        if constexpr (PERSIST && VAR) {
+            // the number that the producer took; nitems or more: none left, -1: abort
+            if (pass == 0) return (int)blockIdx.x;
+            if (!mbar_wait(bar(C::B_ITEM + pass % kVarRing), (uint32_t)((pass / kVarRing) & 1), abort_flag)) return -1;
+            return sItem[pass % kVarRing];
+        } else {
+            return PERSIST ? snake_item(pass, (int)blockIdx.x, (int)gridDim.x) : (pass == 0 ? (int)blockIdx.x : nitems);
+        }
+    };
+    // the same by a whole warp, with one answer
+    auto item_of_warp = [&](int pass) -> int {
+        if constexpr (PERSIST && VAR) {
+            if (pass == 0) return (int)blockIdx.x;
+            if (!mbar_wait_warp(bar(C::B_ITEM + pass % kVarRing), (uint32_t)((pass / kVarRing) & 1), abort_flag))
+                return -1;
+            return sItem[pass % kVarRing];
+        } else {
+            return item_of(pass);
+        }
     };
 
     if (threadIdx.x == 0) {
@@ -207,6 +228,8 @@ __global__ void __launch_bounds__(384, 1)
             mbar_init(bar(C::B_O_FINAL + x), 1);
             mbar_init(bar(C::B_O_EMPTY + x), 4);
         }
+        if constexpr (PERSIST && VAR)
+            for (int s = 0; s < kVarRing; s++) mbar_init(bar(C::B_ITEM + s), 1);
         *abort_flag = 0;
         fence_mbar_init();
     }
@@ -235,12 +258,24 @@ __global__ void __launch_bounds__(384, 1)
                 const uint64_t keep = policy_evict_last();
                 int issued = 0, q_issued = 0;  // ring slots and Q buffers loaded (for the abort drain)
                 bool ok = true;
+                if constexpr (PERSIST && VAR) mbar_arrive(bar(C::B_ITEM));  // pass 0
                 for (int pass = 0; ok && (PERSIST || pass == 0); pass++) {
                     const int w = item_of(pass);
+                    if (VAR && w < 0) {
+                        ok = false;
+                        break;
+                    }
                     if (w >= nitems) break;
                     const Fwd2Item I = fwd2_item<C, VAR>(w, p);
-                    // this CTA's last item: the next kernel may start launching
-                    if (item_of(pass + 1) >= nitems) griddep_launch_dependents();
+                    // packed sequences: the next item's number is on its way while this
+                    // one's queries are loaded
+                    int next = 0;
+                    if constexpr (PERSIST && VAR) {
+                        next = (int)gridDim.x + atomicAdd(p.var.next, 1);
+                    } else {
+                        // this CTA's last item: the next kernel may start launching
+                        if (item_of(pass + 1) >= nitems) griddep_launch_dependents();
+                    }
                     // the item's queries once both O stores of the item that used this
                     // buffer NQB items ago have read it
                     const int qb = pass % C::NQB;
@@ -257,6 +292,11 @@ __global__ void __launch_bounds__(384, 1)
                                         I.bh);
                     }
                     q_issued++;
+                    if constexpr (PERSIST && VAR) {
+                        sItem[(pass + 1) % kVarRing] = next;
+                        mbar_arrive(bar(C::B_ITEM + (pass + 1) % kVarRing));
+                        if (next >= nitems) griddep_launch_dependents();
+                    }
                     // ring slots in order K(lo), V(lo), K(lo+1), V(lo+1), ...
                     for (int j = I.lo; ok && j <= I.hi; j++) {
                         for (int kv = 0; kv < 2 && ok; kv++) {
@@ -300,6 +340,10 @@ __global__ void __launch_bounds__(384, 1)
                 int pass = 0;
                 for (; ok && (PERSIST || pass == 0); pass++) {
                     const int w = item_of(pass);
+                    if (VAR && w < 0) {
+                        ok = false;
+                        break;
+                    }
                     if (w >= nitems) break;
                     const Fwd2Item I = fwd2_item<C, VAR>(w, p);
                     const int qb = pass % C::NQB;
@@ -392,7 +436,11 @@ __global__ void __launch_bounds__(384, 1)
         int slot0 = 0;  // ring slot of the current item's K(lo)
         bool ok = true;
         for (int pass = 0; ok && (PERSIST || pass == 0); pass++) {
-            const int w = item_of(pass);
+            const int w = item_of_warp(pass);
+            if (VAR && w < 0) {
+                ok = false;
+                break;
+            }
             if (w >= nitems) break;
             const Fwd2Item I = fwd2_item<C, VAR>(w, p);
             const int qb = pass % C::NQB;

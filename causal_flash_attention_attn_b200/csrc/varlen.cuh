@@ -26,6 +26,7 @@
 
 namespace forge {
 
+constexpr int kPlanParts = 2;
 constexpr int kPlanThreads = 1024;  // also the weight classes, and the sequences held in shared memory at once
 
 struct VarPlanParams {
@@ -35,8 +36,13 @@ struct VarPlanParams {
     int window;    // 0 = none
     int backward;  // weights: 0 = keys a query tile sees, 1 = queries that see a key tile
     VarItem *items;
-    int *count;
+    int *count, *next;
     int max_items;
+    // backward on the tensor cores: key tiles with many query tiles are cut into parts
+    // (0 = never): of about 1 / kPlanParts of a CTA's share, which is all (key tile, KV
+    // head, head-dim half) items over `ctas`, and at least min_part query tiles
+    int ctas, per_tile, min_part, max_slots;
+    int *cut;
     // tensors whose rows behind the last sequence are set to zero (nullptr = none):
     // [rows][row_chunks * 16 bytes]
     uint4 *tail[3];
@@ -92,20 +98,32 @@ __global__ void __launch_bounds__(kPlanThreads) varlen_plan(const VarPlanParams 
         return;
     }
     __shared__ int cls[kPlanThreads], first[kPlanThreads], length[kPlanThreads], padded[kPlanThreads], sums[32];
+    __shared__ int slots, cuts, part_tiles;
+    __shared__ unsigned long long steps;
     const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
     const int gran = max(128, (p.rows + kPlanThreads - 1) / kPlanThreads);
     const int most = p.window > 0 ? (int)min((long long)p.window + p.unit, (long long)p.rows) : p.rows;
-    auto klass = [&](int len, int t) -> int {
-        const int span = p.backward ? len - t * p.unit : min(len, (t + 1) * p.unit);
-        return min(min(span, most) / gran, kPlanThreads - 1);
+    // query tiles that see key tile t
+    auto q_tiles = [&](int len, int t) -> int {
+        const int k1 = (t + 1) * p.unit - 1;
+        const int last = p.window > 0 ? (int)min((long long)len - 1, (long long)k1 + p.window - 1) : len - 1;
+        return last / p.unit - t + 1;
     };
+    auto klass = [&](int span) -> int { return min(min(span, most) / gran, kPlanThreads - 1); };
     bool bad = tid == 0 && p.cu[0] != 0;
     cls[tid] = 0;
+    if (tid == 0) {
+        slots = cuts = 0;
+        part_tiles = 0x7fffffff;
+        steps = 0;
+    }
     int total = 0;
-    for (int pass = 0; pass < 2; pass++) {
+    // pass 0 (with cutting): all query tiles; pass 1: class sizes; pass 2: the list
+    for (int pass = p.ctas > 0 ? 0 : 1; pass < 3; pass++) {
+        const bool loads = pass == (p.ctas > 0 ? 0 : 1) || p.num_seqs > kPlanThreads;
         int pad = 0;
         for (int c0 = 0; c0 < p.num_seqs; c0 += kPlanThreads) {
-            if (pass == 0 || p.num_seqs > kPlanThreads) {
+            if (loads) {
                 const int b = c0 + tid;
                 int s = 0, len = 0;
                 if (b < p.num_seqs) {
@@ -125,22 +143,61 @@ __global__ void __launch_bounds__(kPlanThreads) varlen_plan(const VarPlanParams 
             __syncthreads();
             for (int i = warp; i < min(kPlanThreads, p.num_seqs - c0); i += 32) {
                 const int len = length[i];
+                unsigned long long n = 0;
                 for (int t = lane; t * p.unit < len; t += 32) {
-                    const int at = atomicAdd(&cls[klass(len, t)], 1);
-                    if (pass == 1 && at < p.max_items) p.items[at] = VarItem{first[i], len, t, padded[i]};
+                    if (pass == 0) {
+                        n += q_tiles(len, t);
+                        continue;
+                    }
+                    if (p.backward) {
+                        const int nm = q_tiles(len, t);
+                        int parts = nm > part_tiles ? (nm + part_tiles - 1) / part_tiles : 1, slot = 0;
+                        if (pass == 2 && parts > 1) {
+                            // the host's bound on the slots covers every cut
+                            slot = atomicAdd(&slots, parts);
+                            int *c = p.cut + 4 + 4 * atomicAdd(&cuts, 1);
+                            c[0] = first[i] + t * p.unit;
+                            c[1] = min(p.unit, len - t * p.unit);
+                            c[2] = slot;
+                            c[3] = parts;
+                        }
+                        for (int x = 0; x < parts; x++) {
+                            // the first nm % parts parts have one query tile more
+                            const int m0 = nm / parts * x + min(nm % parts, x), m1 = m0 + nm / parts + (x < nm % parts);
+                            const int at = atomicAdd(&cls[klass((m1 - m0) * p.unit)], 1);
+                            if (pass == 2 && at < p.max_items)
+                                p.items[at] = VarItem{first[i], len, t, padded[i], m0, m1 - m0, slot + x, parts};
+                        }
+                    } else {
+                        const int at = atomicAdd(&cls[klass(min(len, (t + 1) * p.unit))], 1);
+                        if (pass == 2 && at < p.max_items) p.items[at] = VarItem{first[i], len, t, padded[i], 0, 0, 0, 1};
+                    }
+                }
+                if (pass == 0) {
+#pragma unroll
+                    for (int o = 16; o > 0; o >>= 1) n += __shfl_xor_sync(0xffffffffu, n, o);
+                    if (lane == 0) atomicAdd(&steps, n);
                 }
             }
         }
         __syncthreads();
-        if (pass == 0) {
-            // lengths that do not add up could overlap: nothing is scheduled then
-            if (__syncthreads_or(bad)) {
-                if (tid == 0) {
-                    *p.count = 0;
-                    record_status(kStatusInvalidArg);
-                }
-                return;
+        // lengths that do not add up could overlap: nothing is scheduled then
+        if (pass < 2 && __syncthreads_or(bad)) {
+            if (tid == 0) {
+                *p.count = *p.next = 0;
+                if (p.ctas > 0) p.cut[0] = 0;
+                record_status(kStatusInvalidArg);
             }
+            return;
+        }
+        if (pass == 0) {
+            if (tid == 0) {
+                const unsigned long long n = (steps * p.per_tile + p.ctas * kPlanParts - 1) / (p.ctas * kPlanParts);
+                part_tiles = max((int)min(n, (unsigned long long)p.rows), p.min_part);
+            }
+            __syncthreads();
+        }
+        if (pass == 1) {
             // class sizes -> first place of each class, the heaviest class first
             const int n = cls[kPlanThreads - 1 - tid];
             const int at = plan_scan(n, total, sums);
@@ -149,13 +206,17 @@ __global__ void __launch_bounds__(kPlanThreads) varlen_plan(const VarPlanParams 
             __syncthreads();
         }
     }
-    if (tid == 0) *p.count = min(total, p.max_items);
+    if (tid == 0) {
+        *p.count = min(total, p.max_items);
+        *p.next = 0;
+        if (p.ctas > 0) p.cut[0] = cuts;
+    }
 }
 
 // Delta_i = rowsum(dO_i * o_i) of a tile of one head (o + o_res, where the forward
 // wrote o's rounding residual), and (acc != nullptr)
-// the tile's rows of the padded dq accumulator set to zero. One block per (tile,
-// head), heads innermost; LPR lanes a row as in bwd_preprocess.
+// the tile's rows of the padded dq accumulator set to zero. The blocks take the (item,
+// head) pairs in turn, heads innermost; LPR lanes a row as in bwd_preprocess.
 template <typename T, int D>
 __global__ void __launch_bounds__(256) varlen_preprocess(const T *__restrict__ o, const T *__restrict__ o_res,
                                                          const T *__restrict__ dO, float *__restrict__ delta, float *__restrict__ acc, int Hq,
@@ -164,62 +225,94 @@ __global__ void __launch_bounds__(256) varlen_preprocess(const T *__restrict__ o
     constexpr int RPB = 256 / LPR;                // rows per pass of the block
     griddep_launch_dependents();
     griddep_wait();
-    const int item = blockIdx.x / Hq, h = blockIdx.x % Hq;
-    if (item >= var_count(var)) return;
-    const VarItem it = var_item(var, item);
-    const int sub = threadIdx.x % LPR, n = min(var.unit, it.len - it.tile * var.unit);
-    const size_t row0 = (size_t)it.row0 + (size_t)it.tile * var.unit;
-    float *arow0 = acc == nullptr ? nullptr : acc + ((size_t)h * var.pad_rows + it.pad0 + (size_t)it.tile * var.unit) * D;
-    for (int r0 = 0; r0 < n; r0 += RPB) {
-        const int r = r0 + threadIdx.x / LPR;
-        const bool live = r < n;
-        const size_t at = ((row0 + (live ? r : 0)) * Hq + h) * D;  // every lane takes part in the shuffles
-        if (acc != nullptr && live)
-            for (int c = sub * 4; c < D; c += 4 * LPR)
-                *reinterpret_cast<float4 *>(arow0 + (size_t)r * D + c) = make_float4(0.f, 0.f, 0.f, 0.f);
-        float sum = 0.0f;
+    const int work = var_count(var) * Hq, sub = threadIdx.x % LPR;
+    for (int idx = blockIdx.x; idx < work; idx += gridDim.x) {
+        const int item = idx / Hq, h = idx % Hq;
+        const VarItem it = var_item_part(var, item);
+        if (it.m0 > 0) continue;  // the tile comes once more as another part
+        const int n = min(var.unit, it.len - it.tile * var.unit);
+        const size_t row0 = (size_t)it.row0 + (size_t)it.tile * var.unit;
+        float *arow0 = acc == nullptr ? nullptr : acc + ((size_t)h * var.pad_rows + it.pad0 + (size_t)it.tile * var.unit) * D;
+        for (int r0 = 0; r0 < n; r0 += RPB) {
+            const int r = r0 + threadIdx.x / LPR;
+            const bool live = r < n;
+            const size_t at = ((row0 + (live ? r : 0)) * Hq + h) * D;  // every lane takes part in the shuffles
+            if (acc != nullptr && live)
+                for (int c = sub * 4; c < D; c += 4 * LPR)
+                    *reinterpret_cast<float4 *>(arow0 + (size_t)r * D + c) = make_float4(0.f, 0.f, 0.f, 0.f);
+            float sum = 0.0f;
 #pragma unroll
-        for (int c = sub * 8; c < D; c += 8 * LPR) {
-            float a[8], b[8];
-            load8(o + at + c, a);
-            load8(dO + at + c, b);
-            if (o_res != nullptr) {
-                float r[8];
-                load8(o_res + at + c, r);
+            for (int c = sub * 8; c < D; c += 8 * LPR) {
+                float a[8], b[8];
+                load8(o + at + c, a);
+                load8(dO + at + c, b);
+                if (o_res != nullptr) {
+                    float r[8];
+                    load8(o_res + at + c, r);
 #pragma unroll
-                for (int i = 0; i < 8; i++) a[i] += r[i];
+                    for (int i = 0; i < 8; i++) a[i] += r[i];
+                }
+#pragma unroll
+                for (int i = 0; i < 8; i++) sum = fmaf(a[i], b[i], sum);
             }
 #pragma unroll
-            for (int i = 0; i < 8; i++) sum = fmaf(a[i], b[i], sum);
+            for (int off = LPR / 2; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
+            if (sub == 0 && live) delta[(size_t)h * var.rows + row0 + r] = sum;
         }
-#pragma unroll
-        for (int off = LPR / 2; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
-        if (sub == 0 && live) delta[(size_t)h * var.rows + row0 + r] = sum;
     }
 }
 
-// dq rows of a 128-row tile of one head from the padded accumulator.
+// The last stage of the bf16 backward: dk and dv of the key tiles that were cut, the
+// parts' sums added in their order, and dq rows from the padded accumulator, 128-row
+// tiles of one head. The blocks take the units of both in turn.
 template <int D>
-__global__ void __launch_bounds__(256) varlen_finalize_dq(const float *__restrict__ acc, __nv_bfloat16 *__restrict__ dq,
-                                                          int Hq, const VarSched var) {
+__global__ void __launch_bounds__(256) varlen_finalize(const float *__restrict__ acc, __nv_bfloat16 *__restrict__ dq,
+                                                       __nv_bfloat16 *__restrict__ dk, __nv_bfloat16 *__restrict__ dv,
+                                                       int Hq, int Hkv, const VarSched var) {
     constexpr int CH = D / 8;  // 8-element chunks per row
     griddep_launch_dependents();
     griddep_wait();
-    const int item = blockIdx.x / Hq, h = blockIdx.x % Hq;
-    if (item >= var_count(var)) return;
-    const VarItem it = var_item(var, item);
-    const int n = min(var.unit, it.len - it.tile * var.unit);
-    const size_t row0 = (size_t)it.row0 + (size_t)it.tile * var.unit;
-    const float *arow0 = acc + ((size_t)h * var.pad_rows + it.pad0 + (size_t)it.tile * var.unit) * D;
-    for (int i = threadIdx.x; i < n * CH; i += 256) {
-        const int r = i / CH, c = i % CH;
-        float f[8];
-        load8(arow0 + (size_t)r * D + c * 8, f);
-        uint4 u;
-        uint32_t *w = reinterpret_cast<uint32_t *>(&u);
+    {
+        // units of 256 chunks: 256 / CH rows of one of (dk, dv), KV head, cut tile
+        constexpr int RPU = 256 / CH, UPT = 128 / RPU;
+        const int units = var.cut[0] * Hkv * 2 * UPT;
+        for (int u = blockIdx.x; u < units; u += gridDim.x) {
+            const int r = u % UPT * RPU + (int)threadIdx.x / CH, c = (int)threadIdx.x % CH * 8;
+            const int which = u / UPT % 2, h = u / (UPT * 2) % Hkv;
+            const int4 t = *reinterpret_cast<const int4 *>(var.cut + 4 + 4 * (u / (UPT * 2 * Hkv)));
+            if (r >= t.y) continue;
+            float sum[8] = {};
+            for (int x = 0; x < t.w; x++) {
+                float f[8];
+                load8(var.parts + ((((size_t)(t.z + x) * Hkv + h) * 2 + which) * 128 + r) * D + c, f);
 #pragma unroll
-        for (int e = 0; e < 4; e++) w[e] = pack_bf16x2(f[2 * e], f[2 * e + 1]);
-        *reinterpret_cast<uint4 *>(dq + ((row0 + r) * Hq + h) * D + c * 8) = u;
+                for (int e = 0; e < 8; e++) sum[e] += f[e];
+            }
+            uint4 o;
+            uint32_t *w = reinterpret_cast<uint32_t *>(&o);
+#pragma unroll
+            for (int e = 0; e < 4; e++) w[e] = pack_bf16x2(sum[2 * e], sum[2 * e + 1]);
+            *reinterpret_cast<uint4 *>((which ? dv : dk) + ((size_t)(t.x + r) * Hkv + h) * D + c) = o;
+        }
+    }
+    const int work = var_count(var) * Hq;
+    for (int idx = blockIdx.x; idx < work; idx += gridDim.x) {
+        const int item = idx / Hq, h = idx % Hq;
+        const VarItem it = var_item_part(var, item);
+        if (it.m0 > 0) continue;  // the tile comes once more as another part
+        const int n = min(var.unit, it.len - it.tile * var.unit);
+        const size_t row0 = (size_t)it.row0 + (size_t)it.tile * var.unit;
+        const float *arow0 = acc + ((size_t)h * var.pad_rows + it.pad0 + (size_t)it.tile * var.unit) * D;
+        for (int i = threadIdx.x; i < n * CH; i += 256) {
+            const int r = i / CH, c = i % CH;
+            float f[8];
+            load8(arow0 + (size_t)r * D + c * 8, f);
+            uint4 u;
+            uint32_t *w = reinterpret_cast<uint32_t *>(&u);
+#pragma unroll
+            for (int e = 0; e < 4; e++) w[e] = pack_bf16x2(f[2 * e], f[2 * e + 1]);
+            *reinterpret_cast<uint4 *>(dq + ((row0 + r) * Hq + h) * D + c * 8) = u;
+        }
     }
 }
 

@@ -12,6 +12,10 @@ struct alignas(16) VarItem {
     int len;   // rows of the sequence
     int tile;  // tile index within the sequence
     int pad0;  // first row of the sequence in tensors whose sequences are padded to 128 rows
+    // backward: this item walks the query tiles m0 .. m0 + nm - 1 (of 128 rows, counted from
+    // the key tile's own), and is one of `parts` that share the key tile: part
+    // number `slot` of the partial sums if parts > 1
+    int m0, nm, slot, parts;
 };
 
 // The schedule of one call, in device memory. Both are written by an earlier
@@ -20,6 +24,10 @@ struct alignas(16) VarItem {
 struct VarSched {
     const VarItem *items;
     const int *count;  // tiles in `items`
+    int *next;         // items handed out so far (var_next), set to 0 by the schedule's kernel
+    float *parts;      // backward: partial [slot][Hkv][dk, dv][128][D] of key tiles cut into parts
+    int max_items, max_slots;
+    const int *cut;        // [0]: key tiles cut; then 4 ints each: row0 + first key, keys, first slot, parts
     int unit;          // rows of a tile
     int rows;          // rows of the packed tensors
     int pad_rows;      // rows of the padded tensors (an upper bound)
@@ -31,8 +39,28 @@ __device__ __forceinline__ VarItem var_item(const VarSched &v, int i) {
                  : "=r"(t.row0), "=r"(t.len), "=r"(t.tile), "=r"(t.pad0)
                  : "l"(v.items + i)
                  : "memory");
+    return t;  // m0 .. parts are read by var_item_part
+}
+__device__ __forceinline__ VarItem var_item_part(const VarSched &v, int i) {
+    VarItem t = var_item(v, i);
+    asm volatile("ld.global.v4.b32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(t.m0), "=r"(t.nm), "=r"(t.slot), "=r"(t.parts)
+                 : "l"(&v.items[i].m0)
+                 : "memory");
     return t;
 }
+
+// Work items handed out one at a time in the schedule's order, heaviest first: a CTA
+// that gets done early takes more (a fixed order would leave it idle: the lengths are
+// not known at launch). The first item is the CTA's own number; while it loads an item,
+// one thread takes the next one's number and publishes it in a ring of kVarRing shared
+// words, each with a barrier on which every role waits (pass p >= 1: word and barrier
+// p % kVarRing, phase (p / kVarRing) & 1, the barriers of pass 0 completed at the start).
+// No role releases a word. The thread publishes pass p + 1 when it has issued the first
+// loads of pass p, for which the buffers of pass p - 2 (or p - 1) must have been freed:
+// by then every product of pass p - 2 is done, hence every role has finished pass p - 3, and
+// the word to be written, last used for pass p + 1 - kVarRing = p - 7, has been read.
+constexpr int kVarRing = 8;
 __device__ __forceinline__ int var_count(const VarSched &v) {
     int n;
     asm volatile("ld.global.b32 %0, [%1];" : "=r"(n) : "l"(v.count) : "memory");

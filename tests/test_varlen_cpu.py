@@ -59,12 +59,12 @@ def test_varlen_bwd_rejects_its_own():
 def test_varlen_workspace_sizes():
     f, b = fa.forge_attn_varlen_fwd_workspace_size, fa.forge_attn_varlen_bwd_workspace_size
     assert f(3, 500, 4, 3, 128, BF) == 0 and b(0, 500, 4, 2, 128, BF) == 0
-    # a tile per 256 rows and one more per sequence, 16 bytes each
-    assert f(3, 500, 4, 2, 128, BF) >= 256 + 16 * (500 // 256 + 3)
+    # a tile per 256 rows and one more per sequence, 32 bytes each
+    assert f(3, 500, 4, 2, 128, BF) >= 256 + 32 * (500 // 256 + 3)
     # never more tiles than rows: 64 sequences of one row each
-    assert f(1 << 20, 64, 4, 2, 128, BF) <= 256 + 16 * 64 + 256
+    assert f(1 << 20, 64, 4, 2, 128, BF) <= 256 + 32 * 64 + 256
     # f32 has no accumulator; bf16 pads each sequence to 128 rows
-    assert b(3, 500, 4, 2, 128, F32) < 256 + 16 * 11 + 256 + 4 * 4 * 500 + 512
+    assert b(3, 500, 4, 2, 128, F32) < 256 + 32 * 11 + 256 + 4 * 4 * 500 + 512
     assert b(3, 500, 4, 2, 128, BF) >= 4 * 4 * 128 * (500 + 3 * 127)
 
 

@@ -242,11 +242,11 @@ def test_equal_lengths_give_the_dense_call(D, T):
         return x.view(B, T, -1, D).transpose(1, 2).contiguous()
     do, dl = fa.attention_fwd(dense(q), dense(k), dense(v))
     ddq, ddk, ddv = fa.attention_bwd(dense(q), dense(k), dense(v), do, dl, dense(dO))
-    # the same kernels on the same tiles in the same order
+    # the same forward on the same tiles in the same order; the packed backward may cut a key
+    # tile's queries into parts, whose sums then add up in another order
     assert torch.equal(dense(o), do) and torch.equal(lse.view(Hq, B, T).transpose(0, 1), dl)
-    if not (D == 128 and T > 512):
-        assert torch.equal(dense(dk), ddk) and torch.equal(dense(dv), ddv)
     check_close("dk", dense(dk), ddk.double().cpu().numpy(), "bf16")
+    check_close("dv", dense(dv), ddv.double().cpu().numpy(), "bf16")
     check_close("dq", dense(dq), ddq.double().cpu().numpy(), "bf16")
 
 
