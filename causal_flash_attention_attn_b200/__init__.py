@@ -650,8 +650,8 @@ def attention_varlen_fwd(q, k, v, cu_seqlens, scale=None, window=0, softcap=0.0,
     what = "attention_varlen_fwd"
     rows, Hq, Hkv, D, (qs, ks, vs) = (_is_packed(q, k, v, cu_seqlens, sink) or
                                       _check_packed(what, q, k, v, cu_seqlens, sink))
-    scale = 1.0 / math.sqrt(D) if scale is None else scale
-    dt, n = dtype_code(q.dtype), cu_seqlens.numel() - 1
+    scale = 1.0 / math.sqrt(D) if scale is None else float(scale)
+    window, softcap, dt, n = int(window), float(softcap), dtype_code(q.dtype), cu_seqlens.numel() - 1
     with _scope(q.device, stream):
         o = torch.empty((rows, Hq, D), dtype=q.dtype, device=q.device)
         o_res = torch.empty_like(o) if return_residual and dt == FORGE_DTYPE_BF16 else None
@@ -681,21 +681,31 @@ def attention_varlen_bwd(q, k, v, o, lse, dO, cu_seqlens, scale=None, window=0, 
             _is(lse, torch.float32, (Hq, rows), dev)):
         _check_dense(what, q.device, o=(o, q.dtype, shape), lse=(lse, torch.float32, (Hq, rows)),
                      o_res=(o_res, q.dtype, shape), dO=(dO, q.dtype, shape))
-    scale = 1.0 / math.sqrt(D) if scale is None else scale
-    dt, n = dtype_code(q.dtype), cu_seqlens.numel() - 1
+    scale = 1.0 / math.sqrt(D) if scale is None else float(scale)
     with _scope(q.device, stream):
-        dq, dk, dv = (torch.empty(x.shape, dtype=x.dtype, device=x.device) for x in (q, k, v))
-        dsink = torch.empty((Hq,), dtype=torch.float32, device=q.device) if sink is not None else None
-        L = library()
-        nbytes = L.forge_attn_varlen_bwd_workspace_size(n, rows, Hq, Hkv, D, dt)
-        ws = torch.empty(nbytes, dtype=torch.uint8, device=q.device)
-        s = L.forge_attn_varlen_bwd(q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), _at(o_res), lse.data_ptr(),
-                                    dO.data_ptr(), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), cu_seqlens.data_ptr(),
-                                    n, rows, Hq, Hkv, D, qs, ks, vs, scale, window, softcap, _at(sink), _at(dsink), 1,
-                                    dt, ws.data_ptr(), nbytes, _here(q.device))
+        g = _varlen_bwd(q, k, v, o, o_res, lse, dO, cu_seqlens, sink, scale, int(window), float(softcap), rows, Hq, Hkv,
+                        D, qs, ks, vs)
+    return g if sink is not None else g[:3]
+
+
+def _varlen_bwd(q, k, v, o, o_res, lse, dO, cu_seqlens, sink, scale, window, softcap, rows, Hq, Hkv, D, qs, ks, vs):
+    """The call of attention_varlen_bwd on checked arguments, on the current device and stream."""
+    from torch import empty, float32, uint8
+    L, dtype, device, n = library(), q.dtype, q.device, cu_seqlens.shape[0] - 1
+    dt = dtype_code(dtype)
+    dq = empty((rows, Hq, D), dtype=dtype, device=device)
+    dk = empty((rows, Hkv, D), dtype=dtype, device=device)
+    dv = empty((rows, Hkv, D), dtype=dtype, device=device)
+    dsink = empty((Hq,), dtype=float32, device=device) if sink is not None else None
+    nbytes = L.forge_attn_varlen_bwd_workspace_size(n, rows, Hq, Hkv, D, dt)
+    ws = empty(nbytes, dtype=uint8, device=device)
+    s = L.forge_attn_varlen_bwd(q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), _at(o_res), lse.data_ptr(),
+                                dO.data_ptr(), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), cu_seqlens.data_ptr(), n,
+                                rows, Hq, Hkv, D, qs, ks, vs, scale, window, softcap, _at(sink), _at(dsink), 1, dt,
+                                ws.data_ptr(), nbytes, _here(device))
     if s != FORGE_OK:
         raise ForgeError(s, "forge_attn_varlen_bwd")
-    return (dq, dk, dv, dsink) if sink is not None else (dq, dk, dv)
+    return dq, dk, dv, dsink
 
 
 _attention_varlen_fn = None
@@ -714,14 +724,18 @@ def _attention_varlen_function():
                 o, lse, o_res = attention_varlen_fwd(q, k, v, cu_seqlens, scale, window, softcap, sink=sink,
                                                      return_residual=True)
                 ctx.save_for_backward(q, k, v, o, o_res, lse, cu_seqlens, sink)
-                ctx.args = (scale, window, softcap)
+                rows, Hq, D = q.shape
+                ctx.args = (scale, window, softcap, rows, Hq, k.shape[1], D,
+                            *((x.stride(0) if rows > 1 else x.shape[1] * D) for x in (q, k, v)))
                 return o
 
             @staticmethod
             def backward(ctx, dO):
+                # the forward has checked everything but dO, which autograd gives o's type
+                # and shape, with the device and the stream of the forward current
                 q, k, v, o, o_res, lse, cu_seqlens, sink = ctx.saved_tensors
-                g = attention_varlen_bwd(q, k, v, o, lse, dO.contiguous(), cu_seqlens, *ctx.args, sink=sink, o_res=o_res)
-                return g[0], g[1], g[2], None, (g[3] if sink is not None else None), None, None, None
+                dq, dk, dv, dsink = _varlen_bwd(q, k, v, o, o_res, lse, dO.contiguous(), cu_seqlens, sink, *ctx.args)
+                return dq, dk, dv, None, dsink, None, None, None
 
         _attention_varlen_fn = ForgeAttentionVarlen
     return _attention_varlen_fn
@@ -785,8 +799,8 @@ def attention_decode_paged(q, k_pages, v_pages, page_table, seq_lens, scale=None
             _is(seq_lens, torch.int32, (B,), dev) and _is(sink, torch.float32, (Hq,), dev)):
         _check_dense(what, q.device, q=(q, q.dtype, q.shape), page_table=(page_table, torch.int32, (B, width)),
                      seq_lens=(seq_lens, torch.int32, (B,)), sink=(sink, torch.float32, (Hq,)))
-    scale = 1.0 / math.sqrt(D) if scale is None else scale
-    dt = dtype_code(q.dtype)
+    scale = 1.0 / math.sqrt(D) if scale is None else float(scale)
+    window, softcap, dt = int(window), float(softcap), dtype_code(q.dtype)
     with _scope(q.device, stream):
         o = torch.empty_like(q)
         lse = torch.empty((B, Hq), dtype=torch.float32, device=q.device)

@@ -1351,7 +1351,8 @@ forge_status forge_attn_paged_append(const void *k, const void *v, void *k_pages
                                      size_t page_stride, forge_dtype dtype, void *stream) {
     forge_status s = check_pool(k_pages, v_pages, Hkv, D, num_pages, page_size, page_stride, dtype);
     if (s != FORGE_OK) return s;
-    if (num_seqs < 1 || rows < 1 || rows > (1 << 30) || table_width < 1) return FORGE_ERR_INVALID_ARG;
+    if (num_seqs < 1 || rows < 1 || rows > (1 << 30) || table_width < 1 || (long long)table_width * page_size > (1 << 30))
+        return FORGE_ERR_INVALID_ARG;
     if (cu_seqlens == nullptr && rows != num_seqs) return FORGE_ERR_INVALID_ARG;
     if (!aligned16(k) || !aligned16(v) || !aligned4(page_table) || !aligned4(starts) ||
         (cu_seqlens && !aligned4(cu_seqlens)))

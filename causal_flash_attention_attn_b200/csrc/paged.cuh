@@ -11,7 +11,8 @@
 namespace forge {
 
 constexpr int kAppendThreads = 256;
-constexpr int kAppendTokens = 16;  // tokens of one block, at most
+constexpr int kAppendTokens = 4;  // tokens of one block, at most
+constexpr int kAppendUnroll = 4;
 
 struct AppendParams {
     const uint8_t *src[2];   // K, V: [rows][Hkv][row bytes], rows src_stride bytes apart
@@ -25,53 +26,85 @@ struct AppendParams {
     int tokens;              // tokens of one block
 };
 
-// A block first finds the place of each of its tokens (one thread a token: the
-// sequence by bisection of cu, then its page), then copies their Hkv rows of K and V.
-__global__ void __launch_bounds__(kAppendThreads) paged_append(const AppendParams p) {
+// A token has 2 Hkv rows (K's heads, then V's) of `chunks` 16-byte chunks. A thread keeps
+// its chunk of its row over the block's tokens (tokens smaller than the block are taken
+// several at a time), so that a copy needs no division. It loads its first kAppendUnroll
+// tokens' chunks at once; while they are on their way the block finds where its tokens
+// go, one thread a token: the sequence by bisection of cu, then its page, a chain of
+// dependent loads as long as the copy itself. 16384 tokens of 8 heads of 128 in bf16 (134 MB
+// moved): 23.8 us, 86 % of the measured copy rate; places first, then copies took 35 us,
+// eight tokens a block 24.6-26.4.
+__global__ void __launch_bounds__(kAppendThreads, 6) paged_append(const __grid_constant__ AppendParams p) {
     __shared__ long long place[kAppendTokens];  // byte offset of the token's row of head 0; -1 = none
     griddep_launch_dependents();
     griddep_wait();
     const int t0 = blockIdx.x * p.tokens, n = min(p.tokens, p.rows - t0);
     const long long head = (long long)p.page * p.chunks * 16;  // bytes between a page's heads
+    const int per = 2 * p.Hkv * p.chunks, side = max(1, kAppendThreads / per);
+    const int t1 = (int)threadIdx.x / per;  // which of the tokens side by side
+    int i = t1 < side ? (int)threadIdx.x % per : per, t = t1;
+    const uint8_t *src = nullptr;
+    uint8_t *dst = nullptr;
+    long long step = 0;
+    auto row = [&]() {  // this thread's chunk i of a token
+        if (i >= per) return;
+        const bool v = i >= per / 2;
+        const int h = (v ? i - per / 2 : i) / p.chunks, c = i % p.chunks;
+        step = v ? p.src_stride[1] : p.src_stride[0];
+        src = (v ? p.src[1] : p.src[0]) + t0 * step + ((long long)h * p.chunks + c) * 16;
+        dst = (v ? p.dst[1] : p.dst[0]) + h * head + (long long)c * 16;
+    };
+    uint4 x[kAppendUnroll];
+    auto load = [&]() {
+#pragma unroll
+        for (int e = 0; e < kAppendUnroll; e++)
+            if (i < per && t + e * side < n) x[e] = *reinterpret_cast<const uint4 *>(src + (t + e * side) * step);
+    };
+    row();
+    load();
     if ((int)threadIdx.x < n) {
-        const int t = t0 + threadIdx.x;
-        int b = t, i = 0;
-        bool live = t < p.num_seqs, bad = false;
+        const int tok = t0 + threadIdx.x;
+        int b = tok, first = tok;
+        bool live = tok < p.num_seqs;
         if (p.cu != nullptr) {
-            // the last sequence that starts at or before t: cu[b] <= t < cu[b + 1]
+            // the last sequence that starts at or before the token: cu[b] <= tok < cu[b + 1]
             int lo = 0, hi = p.num_seqs;
             while (lo < hi) {
                 const int mid = (lo + hi) / 2;
-                if (p.cu[mid + 1] <= t) lo = mid + 1;
+                if (p.cu[mid + 1] <= tok) lo = mid + 1;
                 else hi = mid;
             }
             b = lo;
             live = b < p.num_seqs;  // rows behind the last sequence go nowhere
-            if (live) {
-                i = t - p.cu[b];
-                bad = i < 0;
-            }
+            if (live) first = p.cu[b];
         }
         long long at = -1;
         if (live) {
-            const long long start = p.starts[b], pos = start + i;
-            bad |= start < 0 || pos >= (long long)p.width * p.page;
+            const long long start = p.starts[b], pos = start + tok - first;
+            bool bad = tok < first || start < 0 || pos >= (long long)p.width * p.page;
             if (!bad) {
-                const int pg = p.table[(long long)b * p.width + pos / p.page];
+                const int pg = p.table[(long long)b * p.width + (int)pos / p.page];
                 bad = (unsigned)pg >= (unsigned)p.num_pages;
-                if (!bad) at = pg * p.page_stride + (pos % p.page) * p.chunks * 16;
+                if (!bad) at = pg * p.page_stride + ((int)pos % p.page) * p.chunks * 16;
             }
             if (bad) record_status(kStatusInvalidArg);
         }
         place[threadIdx.x] = at;
     }
     __syncthreads();
-    const int per = p.Hkv * p.chunks;  // chunks of one token's K (or V)
-    for (int i = threadIdx.x; i < n * per * 2; i += kAppendThreads) {
-        const int t = i / (2 * per), r = i % (2 * per), kv = r / per, c = r % per;
-        if (place[t] < 0) continue;
-        const uint4 x = *reinterpret_cast<const uint4 *>(p.src[kv] + (long long)(t0 + t) * p.src_stride[kv] + (long long)c * 16);
-        *reinterpret_cast<uint4 *>(p.dst[kv] + place[t] + (c / p.chunks) * head + (long long)(c % p.chunks) * 16) = x;
+    while (i < per) {
+#pragma unroll
+        for (int e = 0; e < kAppendUnroll; e++) {
+            const int u = t + e * side;
+            if (u < n && place[u] >= 0) *reinterpret_cast<uint4 *>(dst + place[u]) = x[e];
+        }
+        t += side * kAppendUnroll;
+        if (t >= n) {
+            t = t1;
+            i += kAppendThreads;
+            row();
+        }
+        load();
     }
 }
 
