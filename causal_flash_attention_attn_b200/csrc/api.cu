@@ -579,12 +579,15 @@ forge_status var_fwd_tc(const VarArgs &a, const VarSched &v, void *o, void *o_re
                           p);
     } else {
         using C = Fwd2Tc<D>;
-        if (set_smem(fwd2_tc_kernel<D, true, true>, C::SMEM) != FORGE_OK) return FORGE_ERR_CUDA;
+        // a forward whose backward will want dsink: P in two terms
+        auto *kernel = a.sink != nullptr && o_res != nullptr ? fwd2_tc_kernel<D, true, true, true>
+                                                             : fwd2_tc_kernel<D, true, true, false>;
+        if (set_smem(kernel, C::SMEM) != FORGE_OK) return FORGE_ERR_CUDA;
         // one CTA an SM for every length: its items are handed out as CTAs get done
         // (one CTA per item was 218 against 211 us on 8K mixed rows, 28 heads, and 835
         // against 827 us on 16K rows in three sequences, window 4096)
-        return launch_pdl(fwd2_tc_kernel<D, true, true>, dim3((unsigned)(items < sm_count() ? items : sm_count())),
-                          dim3(C::THREADS), C::SMEM, a.st, mq, mk, mv, mo, p);
+        return launch_pdl(kernel, dim3((unsigned)(items < sm_count() ? items : sm_count())), dim3(C::THREADS), C::SMEM,
+                          a.st, mq, mk, mv, mo, p);
     }
 }
 

@@ -163,6 +163,24 @@ __device__ __forceinline__ void exp_chunk32(const uint32_t (&s)[32], uint64_t sl
     }
 }
 
+// The same with P split into two bf16 terms, P = hi + lo (lo = bf16(P - hi)); every
+// exponential by MUFU (2^-22; the FMA-pipe one is within 3e-6 only).
+template <bool CAP>
+__device__ __forceinline__ void exp_chunk32_split(const uint32_t (&s)[32], uint64_t sl2x2, uint64_t negm2,
+                                                  uint64_t (&rs)[2], uint32_t (&hi)[16], uint32_t (&lo)[16]) {
+#pragma unroll
+    for (int c = 0; c < 16; c++) {
+        const uint64_t x2 = f2_make(__uint_as_float(s[2 * c]), __uint_as_float(s[2 * c + 1]));
+        float y0, y1;
+        f2_split(CAP ? f2_add(x2, negm2) : f2_fma(x2, sl2x2, negm2), y0, y1);
+        const float p0 = ex2_approx(y0), p1 = ex2_approx(y1);
+        rs[c & 1] = f2_add(rs[c & 1], f2_make(p0, p1));
+        hi[c] = pack_bf16x2(p0, p1);
+        const float2 h = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&hi[c]));
+        lo[c] = pack_bf16x2(p0 - h.x, p1 - h.y);
+    }
+}
+
 // Persistent: gridDim.x CTAs walk the work items (pairs of query tiles of one
 // head, heaviest first) in the snake order of snake_item; barrier phases count
 // KV tiles (or items) over the CTA's whole run and TMEM is allocated once.
@@ -173,7 +191,11 @@ __device__ __forceinline__ void exp_chunk32(const uint32_t (&s)[32], uint64_t sl
 // that a sequence's last tiles bring along are kept out: K's by the causal mask,
 // V's by zeroing them in shared memory (the softmax warpgroup of the last tile,
 // before it hands its P to the MMA warp), O's by storing that tile row by row.
-template <int D, bool PERSIST, bool VAR = false>
+// SPLIT: O += P V with P as two bf16 terms (P lo beside P hi in S's columns), so that
+// O, and with its residual the backward's Delta, are accurate to ~2^-17 instead of
+// carrying P's rounding. dsink, an f32 gradient that is a sum of Delta over all rows, needs
+// that: 1.6e-3 of its norm off without, 7e-6 with it (1000 + 700 + 333 rows).
+template <int D, bool PERSIST, bool VAR = false, bool SPLIT = false>
 __global__ void __launch_bounds__(384, 1)
     fwd2_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                    const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmO,
@@ -366,6 +388,12 @@ __global__ void __launch_bounds__(384, 1)
                         for (int kk = 0; kk < C::BN / 16; kk++)
                             mma_ts(tmem + C::col_o(x), tmem + C::col_s(x) + kk * 8, sdesc_step(dv, kk * 2048), ID_PV,
                                    (acc || kk > 0) ? 1u : 0u);
+                        if constexpr (SPLIT) {
+#pragma unroll
+                            for (int kk = 0; kk < C::BN / 16; kk++)
+                                mma_ts(tmem + C::col_o(x), tmem + C::col_s(x) + 64 + kk * 8, sdesc_step(dv, kk * 2048),
+                                       ID_PV, 1u);
+                        }
                     };
                     if (!(ok = mbar_wait(bar(C::B_Q_FULL + qb), (uint32_t)((pass / C::NQB) & 1), abort_flag))) break;
                     if (!(ok = wait_full(slot0))) break;
@@ -527,7 +555,16 @@ __global__ void __launch_bounds__(384, 1)
                 // 32 scores -> 16 packed P columns; P column c holds scores 2c, 2c+1.
                 // Masked scores are -inf and need the MUFU exp2 (the FMA-pipe one
                 // is only valid for finite arguments); chunks no row sees are 0.
-                if (dead | part) {
+                if constexpr (SPLIT) {
+#pragma unroll
+                    for (int q4 = 0; q4 < 4; q4++) {
+                        uint32_t pk[16], lo16[16];
+                        if (cap) exp_chunk32_split<true>(s[q4], sl2x2, negm2, rs, pk, lo16);
+                        else exp_chunk32_split<false>(s[q4], sl2x2, negm2, rs, pk, lo16);
+                        tmem_st16(tS + 16 * q4, pk);
+                        tmem_st16(tS + 64 + 16 * q4, lo16);
+                    }
+                } else if (dead | part) {
 #pragma unroll
                     for (int q4 = 0; q4 < 4; q4++) {
                         uint32_t pk[16];

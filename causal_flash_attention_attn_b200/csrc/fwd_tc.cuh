@@ -470,11 +470,13 @@ __global__ void __launch_bounds__(320, 1)
             const float msub = (m == -INFINITY) ? 0.0f : m;
             uint32_t pk[32];
             float rs;
+            // no FMA-pipe exponentials (3e-6) where dsink will be formed from O
+            const bool mufu = need_mask || (VAR && p.sink != nullptr && p.o_res != nullptr);
             if (cap) {
-                rs = need_mask ? fwd_exp_half<true, false, C::PSPLIT>(s, pk, p.scale_log2, msub)
+                rs = mufu ? fwd_exp_half<true, false, C::PSPLIT>(s, pk, p.scale_log2, msub)
                                : fwd_exp_half<true, true, C::PSPLIT>(s, pk, p.scale_log2, msub);
             } else {
-                rs = need_mask ? fwd_exp_half<false, false, C::PSPLIT>(s, pk, p.scale_log2, msub)
+                rs = mufu ? fwd_exp_half<false, false, C::PSPLIT>(s, pk, p.scale_log2, msub)
                                : fwd_exp_half<false, true, C::PSPLIT>(s, pk, p.scale_log2, msub);
             }
             // P (bf16 pairs) of this half's 64 keys: columns [32 hf, 32 hf + 32) of S

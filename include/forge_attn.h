@@ -261,7 +261,9 @@ forge_status forge_attn_decode(const void *q, const void *k_cache, const void *v
  *  - o_res [rows][Hq][D] (dtype; may be NULL): the forward writes o's rounding residual,
  *    o - bf16(o) as bf16, there, and the backward, given it, takes Delta from o + o_res. Without it
  *    (NULL in the backward) Delta carries o's rounding, which shows in dq, dk and dsink where
- *    rows attend to few keys. f32: neither written nor read.
+ *    rows attend to few keys. With a sink, a forward that writes o_res also keeps P in two
+ *    bf16 terms (o accurate to ~2^-17 before its rounding), which dsink, a sum of Delta over all
+ *    rows, needs: give o_res wherever dsink matters. f32: neither written nor read.
  *  - sink, dsink: as in forge_attn_fwd_ext / forge_attn_bwd_ext. scale, window, softcap
  *    as in forge_attn_fwd (a window >= rows acts as off).
  *  - rows and num_seqs >= 1, num_seqs <= 2^20, (rows / 64 + num_seqs) * Hq < 2^30; the limits
