@@ -30,6 +30,7 @@ namespace {
 
 // ------------------------------------------------------------------ validation
 bool aligned16(const void *p) { return p != nullptr && (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+bool aligned32(const void *p) { return p != nullptr && (reinterpret_cast<uintptr_t>(p) & 31u) == 0; }
 bool aligned4(const void *p) { return p != nullptr && (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 
 forge_status check_sizes(int B, int Hq, int Hkv, int T, int D, forge_dtype dtype) {
@@ -1248,7 +1249,7 @@ forge_status forge_attn_varlen_fwd(const void *q, const void *k, const void *v, 
                  sink, dtype, static_cast<cudaStream_t>(stream)};
     forge_status s = check_var_args(a);
     if (s != FORGE_OK) return s;
-    if (!aligned16(o) || !aligned16(lse) || (o_res != nullptr && !aligned16(o_res))) return FORGE_ERR_INVALID_ARG;
+    if (!aligned16(o) || !aligned16(lse) || (o_res != nullptr && !aligned32(o_res))) return FORGE_ERR_INVALID_ARG;
     if (workspace == nullptr || (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0 ||
         workspace_bytes < forge_attn_varlen_fwd_workspace_size(num_seqs, rows, Hq, Hkv, D, dtype))
         return FORGE_ERR_WORKSPACE;
@@ -1277,7 +1278,7 @@ forge_status forge_attn_varlen_bwd(const void *q, const void *k, const void *v, 
     if (s != FORGE_OK) return s;
     if (!aligned16(o) || !aligned16(lse) || !aligned16(dO) || !aligned16(dq) || !aligned16(dk) || !aligned16(dv))
         return FORGE_ERR_INVALID_ARG;
-    if (o_res != nullptr && !aligned16(o_res)) return FORGE_ERR_INVALID_ARG;
+    if (o_res != nullptr && !aligned32(o_res)) return FORGE_ERR_INVALID_ARG;
     if (dsink != nullptr && (!aligned4(dsink) || !aligned4(sink))) return FORGE_ERR_INVALID_ARG;
     if (dtype == FORGE_DTYPE_F32) o_res = nullptr;  // an f32 o has no residual
     if (workspace == nullptr || (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0 ||

@@ -244,9 +244,8 @@ __device__ __forceinline__ void bwd_row_part(uint32_t taddr, float *row, int c_l
         uint32_t o[32];
         tmem_ld32(taddr + (uint32_t)c0, o);
         tmem_ld_wait(o);
-        uint4 *dst = reinterpret_cast<uint4 *>(row + c0);
 #pragma unroll
-        for (int e = 0; e < 8; e++) dst[e] = make_uint4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+        for (int e = 0; e < 4; e++) st_global_v8(row + c0 + 8 * e, o + 8 * e);
     }
 }
 

@@ -637,10 +637,9 @@ __global__ void __launch_bounds__(384, 1)
                         uint32_t lo16[16];
                         o_pairs32(o, inv_l, w16, lo16);
                         if (qi < I.T) {
-                            uint4 *dst = reinterpret_cast<uint4 *>(p.o_res + ((size_t)(I.row0 + qi) * p.Hq + I.bh) * D + c0);
-#pragma unroll
-                            for (int i = 0; i < 4; i++)
-                                dst[i] = make_uint4(lo16[4 * i], lo16[4 * i + 1], lo16[4 * i + 2], lo16[4 * i + 3]);
+                            __nv_bfloat16 *dst = p.o_res + ((size_t)(I.row0 + qi) * p.Hq + I.bh) * D + c0;
+                            st_global_v8(dst, lo16);
+                            st_global_v8(dst + 16, lo16 + 8);
                         }
                     } else {
 #pragma unroll

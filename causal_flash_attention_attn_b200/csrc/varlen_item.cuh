@@ -67,6 +67,15 @@ __device__ __forceinline__ int var_count(const VarSched &v) {
     return n;
 }
 
+// 32 bytes, one whole sector, to global memory (32-byte aligned). Where each lane
+// writes a row of its own, the store unit takes one cycle per lane and instruction, so
+// that half as many instructions of twice the width take half the time.
+__device__ __forceinline__ void st_global_v8(void *at, const uint32_t *w) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(at), "r"(w[0]), "r"(w[1]), "r"(w[2]),
+                 "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                 : "memory");
+}
+
 // Rows [valid, ROWS) of a tile of NCB swizzled column blocks (128 bytes a row, `cb`
 // bytes a block) set to zero by NT threads, t = 0 .. NT - 1. A TMA box that runs past a sequence's
 // end brings rows of the next sequence: they are replaced by the zeros that a

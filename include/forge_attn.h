@@ -258,7 +258,7 @@ forge_status forge_attn_decode(const void *q, const void *k_cache, const void *v
  *    follows the lengths that cu_seqlens holds at each replay. Lengths that do not ascend from
  *    0, or that pass `rows`, are reported as FORGE_ERR_INVALID_ARG by the next
  *    forge_attn_check; nothing is computed then.
- *  - o_res [rows][Hq][D] (dtype; may be NULL): the forward writes o's rounding residual,
+ *  - o_res [rows][Hq][D] (dtype, 32-byte aligned; may be NULL): the forward writes o's rounding residual,
  *    o - bf16(o) as bf16, there, and the backward, given it, takes Delta from o + o_res. Without it
  *    (NULL in the backward) Delta carries o's rounding, which shows in dq, dk and dsink where
  *    rows attend to few keys. With a sink, a forward that writes o_res also keeps P in two

@@ -40,7 +40,7 @@ def varlen(backward, **kw):
     (dict(window=-1), INVALID), (dict(scale=0.0), INVALID), (dict(softcap=float("nan")), INVALID),
     (dict(q=0), INVALID), (dict(k=A + 8), INVALID), (dict(cu=0), INVALID), (dict(cu=A + 2), INVALID),
     (dict(o=A + 4), INVALID), (dict(lse=A + 4), INVALID), (dict(sink=A + 1), INVALID), (dict(dtype=7), INVALID),
-    (dict(res=A + 8), INVALID),
+    (dict(res=A + 8), INVALID), (dict(res=A + 16), INVALID),
     (dict(qs=4 * 128 - 8), INVALID),                               # rows would overlap
     (dict(ks=2 * 128 + 4), INVALID),                               # not a multiple of 16 bytes
     (dict(vs=1 << 37), INVALID),
