@@ -19,6 +19,7 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
+import functools
 import math
 import os
 
@@ -543,7 +544,13 @@ def _here(device):
 # The helpers below are called once per layer and token, so that their host time counts. Each takes
 # arguments that are as they should be through one test (_is, _is_packed, _is_pool) and leaves the
 # explanation of what is not to the _check functions, which test the same things one by one.
-# They call the library without the raw binding in between for the same reason.
+# They call the library without the raw binding in between for the same reason, and ask for the
+# workspace of the same sizes on a device (its SM count counts) once.
+@functools.lru_cache(maxsize=1024)
+def _bytes(name, index, *sizes):
+    return int(getattr(library(), name)(*sizes))
+
+
 def _at(t):
     return None if t is None else t.data_ptr()
 
@@ -653,12 +660,12 @@ def attention_varlen_fwd(q, k, v, cu_seqlens, scale=None, window=0, softcap=0.0,
     scale = 1.0 / math.sqrt(D) if scale is None else float(scale)
     window, softcap, dt, n = int(window), float(softcap), dtype_code(q.dtype), cu_seqlens.numel() - 1
     with _scope(q.device, stream):
-        o = torch.empty((rows, Hq, D), dtype=q.dtype, device=q.device)
+        o = q.new_empty((rows, Hq, D))
         o_res = torch.empty_like(o) if return_residual and dt == FORGE_DTYPE_BF16 else None
-        lse = torch.empty((Hq, rows), dtype=torch.float32, device=q.device)
+        lse = q.new_empty((Hq, rows), dtype=torch.float32)
         L = library()
-        nbytes = L.forge_attn_varlen_fwd_workspace_size(n, rows, Hq, Hkv, D, dt)
-        ws = torch.empty(nbytes, dtype=torch.uint8, device=q.device)
+        nbytes = _bytes("forge_attn_varlen_fwd_workspace_size", q.get_device(), n, rows, Hq, Hkv, D, dt)
+        ws = q.new_empty(nbytes, dtype=torch.uint8)
         s = L.forge_attn_varlen_fwd(q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), _at(o_res), lse.data_ptr(),
                                     cu_seqlens.data_ptr(), n, rows, Hq, Hkv, D, qs, ks, vs, scale, window, softcap,
                                     _at(sink), 1, dt, ws.data_ptr(), nbytes, _here(q.device))
@@ -690,19 +697,18 @@ def attention_varlen_bwd(q, k, v, o, lse, dO, cu_seqlens, scale=None, window=0, 
 
 def _varlen_bwd(q, k, v, o, o_res, lse, dO, cu_seqlens, sink, scale, window, softcap, rows, Hq, Hkv, D, qs, ks, vs):
     """The call of attention_varlen_bwd on checked arguments, on the current device and stream."""
-    from torch import empty, float32, uint8
-    L, dtype, device, n = library(), q.dtype, q.device, cu_seqlens.shape[0] - 1
-    dt = dtype_code(dtype)
-    dq = empty((rows, Hq, D), dtype=dtype, device=device)
-    dk = empty((rows, Hkv, D), dtype=dtype, device=device)
-    dv = empty((rows, Hkv, D), dtype=dtype, device=device)
-    dsink = empty((Hq,), dtype=float32, device=device) if sink is not None else None
-    nbytes = L.forge_attn_varlen_bwd_workspace_size(n, rows, Hq, Hkv, D, dt)
-    ws = empty(nbytes, dtype=uint8, device=device)
+    import torch
+    L, n, dt = library(), cu_seqlens.shape[0] - 1, dtype_code(q.dtype)
+    dq = torch.empty_like(o)
+    dk = q.new_empty((rows, Hkv, D))
+    dv = torch.empty_like(dk)
+    dsink = torch.empty_like(sink) if sink is not None else None
+    nbytes = _bytes("forge_attn_varlen_bwd_workspace_size", q.get_device(), n, rows, Hq, Hkv, D, dt)
+    ws = q.new_empty(nbytes, dtype=torch.uint8)
     s = L.forge_attn_varlen_bwd(q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), _at(o_res), lse.data_ptr(),
                                 dO.data_ptr(), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), cu_seqlens.data_ptr(), n,
                                 rows, Hq, Hkv, D, qs, ks, vs, scale, window, softcap, _at(sink), _at(dsink), 1, dt,
-                                ws.data_ptr(), nbytes, _here(device))
+                                ws.data_ptr(), nbytes, _here(q.device))
     if s != FORGE_OK:
         raise ForgeError(s, "forge_attn_varlen_bwd")
     return dq, dk, dv, dsink
@@ -803,10 +809,10 @@ def attention_decode_paged(q, k_pages, v_pages, page_table, seq_lens, scale=None
     window, softcap, dt = int(window), float(softcap), dtype_code(q.dtype)
     with _scope(q.device, stream):
         o = torch.empty_like(q)
-        lse = torch.empty((B, Hq), dtype=torch.float32, device=q.device)
+        lse = q.new_empty((B, Hq), dtype=torch.float32)
         L = library()
-        nbytes = L.forge_attn_decode_paged_workspace_size(B, Hq, Hkv, D, dt)
-        ws = torch.empty(nbytes, dtype=torch.uint8, device=q.device)
+        nbytes = _bytes("forge_attn_decode_paged_workspace_size", dev, B, Hq, Hkv, D, dt)
+        ws = q.new_empty(nbytes, dtype=torch.uint8)
         s = L.forge_attn_decode_paged(q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), o.data_ptr(),
                                       lse.data_ptr(), page_table.data_ptr(), seq_lens.data_ptr(), B, Hq, Hkv, D, P, ps,
                                       width, stride, scale, window, softcap, _at(sink), dt, ws.data_ptr(), nbytes,
