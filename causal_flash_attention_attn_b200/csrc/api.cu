@@ -581,8 +581,9 @@ forge_status var_fwd_tc(const VarArgs &a, const VarSched &v, void *o, void *o_re
     } else {
         using C = Fwd2Tc<D>;
         // a forward whose backward will want dsink: P in two terms
-        auto *kernel = a.sink != nullptr && o_res != nullptr ? fwd2_tc_kernel<D, true, true, true>
-                                                             : fwd2_tc_kernel<D, true, true, false>;
+        const bool split = a.sink != nullptr && o_res != nullptr;
+        auto *kernel = a.softcap > 0.0f ? (split ? fwd2_tc_kernel<D, true, true, true, 1> : fwd2_tc_kernel<D, true, true, false, 1>)
+                                        : (split ? fwd2_tc_kernel<D, true, true, true, 0> : fwd2_tc_kernel<D, true, true, false, 0>);
         if (set_smem(kernel, C::SMEM) != FORGE_OK) return FORGE_ERR_CUDA;
         // one CTA an SM for every length: its items are handed out as CTAs get done
         // (one CTA per item was 218 against 211 us on 8K mixed rows, 28 heads, and 835

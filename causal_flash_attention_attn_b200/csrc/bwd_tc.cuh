@@ -49,6 +49,7 @@
 #pragma once
 
 #include "sm100.cuh"
+#include "tanh_poly.cuh"
 #include "varlen_item.cuh"
 
 namespace forge {
@@ -264,7 +265,8 @@ __device__ __forceinline__ void red_add_f32_hint(float *addr, float v, uint64_t 
 //   nl, nd: -LSE*log2(e) and -scale*Delta of the 32 columns (shared memory).
 // CAP and MASK are compile-time so each unrolled loop is one basic block; the
 // common case (neither) runs on packed f32x2 arithmetic.
-template <bool CAP, bool MASK>
+// POLY (with CAP): every score within tanh_poly2's range, which takes the tanh.
+template <bool CAP, bool MASK, bool POLY = false>
 __device__ __forceinline__ void bwd_p32(const uint32_t (&s)[32], const float *nl, const BwdParams &p, int kj, int q0,
                                         int W, uint32_t (&pk)[16], float (&g)[32]) {
     if constexpr (!CAP && !MASK) {
@@ -286,13 +288,22 @@ __device__ __forceinline__ void bwd_p32(const uint32_t (&s)[32], const float *nl
             }
         }
     } else {
+        float t_odd = 0.0f;
 #pragma unroll
         for (int c = 0; c < 32; c++) {
             const float x = __uint_as_float(s[c]);
             float pr, gg;
             const bool emu = !MASK && (c & 6) == 6;
             if constexpr (CAP) {
-                const float t = tanh_via_ex2(x * p.cap_in);
+                float t;
+                if constexpr (POLY) {
+                    t = t_odd;
+                    if (!(c & 1))
+                        f2_split(tanh_poly2(f2_mul(f2_make(x, __uint_as_float(s[c | 1])), f2_make(p.cap_in, p.cap_in))), t,
+                                 t_odd);
+                } else {
+                    t = tanh_via_ex2(x * p.cap_in);
+                }
                 const float y = fmaf(p.cap_out, t, nl[c]);
                 pr = emu ? exp2_poly(y) : ex2_approx(y);
                 gg = pr * (1.0f - t * t);
@@ -873,7 +884,10 @@ __global__ void __launch_bounds__(512, 1)
                     uint32_t sc[32], pk[16];
                     tmem_ld32(tmem + lane_base + C::COL_S + c0, sc);
                     tmem_ld_wait(sc);
-                    if (cap) {
+                    if (VAR && cap && tanh_poly_fits(sc, p.cap_in)) {
+                        if (mask) bwd_p32<true, true, true>(sc, nls + c0, p, kj, qb + c0, W, pk, g[c]);
+                        else bwd_p32<true, false, true>(sc, nls + c0, p, kj, qb + c0, W, pk, g[c]);
+                    } else if (cap) {
                         if (mask) bwd_p32<true, true>(sc, nls + c0, p, kj, qb + c0, W, pk, g[c]);
                         else bwd_p32<true, false>(sc, nls + c0, p, kj, qb + c0, W, pk, g[c]);
                     } else {

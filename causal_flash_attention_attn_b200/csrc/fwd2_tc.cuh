@@ -195,7 +195,9 @@ __device__ __forceinline__ void exp_chunk32_split(const uint32_t (&s)[32], uint6
 // O, and with its residual the backward's Delta, are accurate to ~2^-17 instead of
 // carrying P's rounding. dsink, an f32 gradient that is a sum of Delta over all rows, needs
 // that: 1.6e-3 of its norm off without, 7e-6 with it (1000 + 700 + 333 rows).
-template <int D, bool PERSIST, bool VAR = false, bool SPLIT = false>
+// CAP: -1 the score cap is a run-time choice; 0, 1 compiled without or with it (packed
+// sequences: the cap's code beside the plain path cost the plain one 2-3 %).
+template <int D, bool PERSIST, bool VAR = false, bool SPLIT = false, int CAP = -1>
 __global__ void __launch_bounds__(384, 1)
     fwd2_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                    const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmO,
@@ -458,7 +460,7 @@ __global__ void __launch_bounds__(384, 1)
         const uint32_t lane_base = (uint32_t)((warp % 4) * 32) << 16;
         const uint32_t tS = tmem + lane_base + C::col_s(x);
         const uint32_t tO = tmem + lane_base + C::col_o(x);
-        const bool cap = p.softcap > 0.0f;
+        const bool cap = CAP < 0 ? p.softcap > 0.0f : CAP > 0;
         const uint64_t sl2x2 = f2_make(p.scale_log2, p.scale_log2);
         int cnt = 0;  // KV tiles of this tile slot over the whole run (S_FULL phases)
         int slot0 = 0;  // ring slot of the current item's K(lo)
@@ -487,7 +489,10 @@ __global__ void __launch_bounds__(384, 1)
                 uint32_t s[4][32];
                 tmem_ld128x4(tS, s[0], s[1], s[2], s[3]);
                 tmem_ld_wait128x4(s[0], s[1], s[2], s[3]);
-                if (cap) {
+                if (VAR && cap) {
+#pragma unroll
+                    for (int q4 = 0; q4 < 4; q4++) cap_scores(s[q4], p.cap_in, p.cap_out);
+                } else if (cap) {
 #pragma unroll
                     for (int c = 0; c < 128; c++) {
                         const float v = __uint_as_float(s[c >> 5][c & 31]);

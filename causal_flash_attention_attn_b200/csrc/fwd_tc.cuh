@@ -27,6 +27,7 @@
 #pragma once
 
 #include "sm100.cuh"
+#include "tanh_poly.cuh"
 #include "varlen_item.cuh"
 
 namespace forge {
@@ -417,7 +418,10 @@ __global__ void __launch_bounds__(320, 1)
             // (the scale is folded into the exponent's FMA, and max commutes
             // with a positive scale)
             const bool cap = p.softcap > 0.0f;
-            if (cap) {
+            if (VAR && cap) {
+                cap_scores(s[0], p.cap_in, p.cap_out);
+                cap_scores(s[1], p.cap_in, p.cap_out);
+            } else if (cap) {
 #pragma unroll
                 for (int c = 0; c < 64; c++) {
                     const float x = __uint_as_float(s[c >> 5][c & 31]);
