@@ -581,9 +581,10 @@ forge_status var_fwd_tc(const VarArgs &a, const VarSched &v, void *o, void *o_re
     } else {
         using C = Fwd2Tc<D>;
         // a forward whose backward will want dsink: P in two terms
-        const bool split = a.sink != nullptr && o_res != nullptr;
-        auto *kernel = a.softcap > 0.0f ? (split ? fwd2_tc_kernel<D, true, true, true, 1> : fwd2_tc_kernel<D, true, true, false, 1>)
-                                        : (split ? fwd2_tc_kernel<D, true, true, true, 0> : fwd2_tc_kernel<D, true, true, false, 0>);
+        const bool split = a.sink != nullptr && o_res != nullptr, cap = a.softcap > 0.0f, win = a.window > 0;
+        auto *kernel = split ? (cap ? fwd2_tc_kernel<D, true, true, true, 1, 1> : fwd2_tc_kernel<D, true, true, true, 0, 1>)
+                       : cap ? (win ? fwd2_tc_kernel<D, true, true, false, 1, 1> : fwd2_tc_kernel<D, true, true, false, 1, 0>)
+                             : (win ? fwd2_tc_kernel<D, true, true, false, 0, 1> : fwd2_tc_kernel<D, true, true, false, 0, 0>);
         if (set_smem(kernel, C::SMEM) != FORGE_OK) return FORGE_ERR_CUDA;
         // one CTA an SM for every length: its items are handed out as CTAs get done
         // (one CTA per item was 218 against 211 us on 8K mixed rows, 28 heads, and 835
@@ -677,9 +678,10 @@ forge_status var_bwd(const VarArgs &a, const VarSched &v, const void *o, const v
         p.cap_in = a.softcap > 0.0f ? a.scale / a.softcap : 0.0f;
         p.cap_out = a.softcap * kLog2e;
         p.var = v;
-        if (set_smem(bwd_tc_kernel<D, true>, C::SMEM) != FORGE_OK) return FORGE_ERR_CUDA;
+        auto *kernel = a.softcap > 0.0f || a.window > 0 ? bwd_tc_kernel<D, true, false> : bwd_tc_kernel<D, true, true>;
+        if (set_smem(kernel, C::SMEM) != FORGE_OK) return FORGE_ERR_CUDA;
         const long long work = (long long)items * a.Hkv * C::NSPLIT;
-        s = launch_pdl(bwd_tc_kernel<D, true>, dim3((unsigned)(work < sm_count() ? work : sm_count())), dim3(C::THREADS),
+        s = launch_pdl(kernel, dim3((unsigned)(work < sm_count() ? work : sm_count())), dim3(C::THREADS),
                        C::SMEM, a.st, mq, mk, mv, mdo, macc, p);
         if (s != FORGE_OK) return s;
         return launch_pdl(varlen_finalize<D>, dim3(wave), dim3(256), 0, a.st,

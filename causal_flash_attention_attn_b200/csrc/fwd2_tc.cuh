@@ -195,9 +195,12 @@ __device__ __forceinline__ void exp_chunk32_split(const uint32_t (&s)[32], uint6
 // O, and with its residual the backward's Delta, are accurate to ~2^-17 instead of
 // carrying P's rounding. dsink, an f32 gradient that is a sum of Delta over all rows, needs
 // that: 1.6e-3 of its norm off without, 7e-6 with it (1000 + 700 + 333 rows).
-// CAP: -1 the score cap is a run-time choice; 0, 1 compiled without or with it (packed
-// sequences: the cap's code beside the plain path cost the plain one 2-3 %).
-template <int D, bool PERSIST, bool VAR = false, bool SPLIT = false, int CAP = -1>
+// CAP: -1 the score cap is a run-time choice; 0, 1 compiled without or with it. WIN: the
+// same for the window. The code of either beside the plain path costs the plain one
+// (8K mixed rows: 207 us with both at run time, 199 without the cap's, 195 without
+// the window's too; 16K rows, window 4096: 836 us, 795 without the cap's, 783 with one test
+// for the tiles that every row sees whole, which most tiles of a window are).
+template <int D, bool PERSIST, bool VAR = false, bool SPLIT = false, int CAP = -1, int WIN = -1>
 __global__ void __launch_bounds__(384, 1)
     fwd2_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                    const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmO,
@@ -475,7 +478,8 @@ __global__ void __launch_bounds__(384, 1)
             const Fwd2Item I = fwd2_item<C, VAR>(w, p);
             const int qb = pass % C::NQB;
             const bool has = (x == 0) || I.hasB;
-            const int W = VAR && p.window >= I.T ? 0 : p.window;  // a window that hides nothing is none
+            // a window that hides nothing is none
+            const int W = WIN == 0 || (VAR && p.window >= I.T) ? 0 : p.window;
             const int q0 = x ? I.qB0 : I.qA0;
             const int lox = x ? I.loB : I.loA, hix = x ? I.tB : I.tA;
             const int qi = q0 + row;
@@ -503,13 +507,15 @@ __global__ void __launch_bounds__(384, 1)
                 // [r0, r0 + 31] (warp-uniform): bit q of `dead` = no key of chunk q
                 // is visible to any of the rows, bit q of `part` = some are.
                 unsigned dead = 0, part = 0;
+                if (WIN != 1 || k0 + 127 > r0 || (W > 0 && k0 <= r0 + 31 - W)) {
 #pragma unroll
-                for (int q4 = 0; q4 < 4; q4++) {
-                    const int c0 = k0 + 32 * q4;
-                    const bool all_vis = (c0 + 31 <= r0) && (W == 0 || c0 > r0 + 31 - W);
-                    const bool none = (c0 > r0 + 31) || (W > 0 && c0 + 31 <= r0 - W);
-                    dead |= (unsigned)none << q4;
-                    part |= (unsigned)(!all_vis && !none) << q4;
+                    for (int q4 = 0; q4 < 4; q4++) {
+                        const int c0 = k0 + 32 * q4;
+                        const bool all_vis = (c0 + 31 <= r0) && (W == 0 || c0 > r0 + 31 - W);
+                        const bool none = (c0 > r0 + 31) || (W > 0 && c0 + 31 <= r0 - W);
+                        dead |= (unsigned)none << q4;
+                        part |= (unsigned)(!all_vis && !none) << q4;
+                    }
                 }
                 if (dead | part) {
 #pragma unroll
