@@ -456,7 +456,8 @@ forge_status check_var_sizes(int num_seqs, int rows, int Hq, int Hkv, int D, for
     forge_status s = check_sizes(1, Hq, Hkv, rows, D, dtype);
     if (s != FORGE_OK) return s;
     if (num_seqs < 1 || num_seqs > (1 << 20)) return FORGE_ERR_INVALID_ARG;
-    if (((long long)rows / 64 + num_seqs) * Hq * 2 > 0x7fffffffll) return FORGE_ERR_INVALID_ARG;  // grids
+    // items (with the parts of cut tiles, at most var_max_slots) times heads: grids and 32-bit counts
+    if (((long long)rows / 64 + num_seqs + 1188) * Hq > 0x7fffffffll) return FORGE_ERR_INVALID_ARG;
     return FORGE_OK;
 }
 

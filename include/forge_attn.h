@@ -266,8 +266,8 @@ forge_status forge_attn_decode(const void *q, const void *k_cache, const void *v
  *    rows, needs: give o_res wherever dsink matters. f32: neither written nor read.
  *  - sink, dsink: as in forge_attn_fwd_ext / forge_attn_bwd_ext. scale, window, softcap
  *    as in forge_attn_fwd (a window >= rows acts as off).
- *  - rows and num_seqs >= 1, num_seqs <= 2^20, (rows / 64 + num_seqs) * Hq < 2^30; the limits
- *    of the dense calls with B = 1, T = rows.
+ *  - rows and num_seqs >= 1, num_seqs <= 2^20, (rows / 64 + num_seqs + 1188) * Hq < 2^31; the
+ *    limits of the dense calls with B = 1, T = rows.
  * workspace: 256-byte aligned device memory of at least the given size, overwritten:
  * the schedule, and in the backward Delta and (bf16) an f32 dq accumulator whose sequences
  * are padded to 128 rows. dq (bf16) is summed with f32 atomics whose order differs
