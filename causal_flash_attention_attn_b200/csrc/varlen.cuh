@@ -223,6 +223,7 @@ __global__ void __launch_bounds__(256) varlen_preprocess(const T *__restrict__ o
                                                          const VarSched var) {
     constexpr int LPR = D / 8 < 32 ? D / 8 : 32;  // lanes per row
     constexpr int RPB = 256 / LPR;                // rows per pass of the block
+    constexpr int NR = sizeof(T) == 2 ? 4 : 2;
     griddep_launch_dependents();
     griddep_wait();
     const int work = var_count(var) * Hq, sub = threadIdx.x % LPR;
@@ -233,31 +234,39 @@ __global__ void __launch_bounds__(256) varlen_preprocess(const T *__restrict__ o
         const int n = min(var.unit, it.len - it.tile * var.unit);
         const size_t row0 = (size_t)it.row0 + (size_t)it.tile * var.unit;
         float *arow0 = acc == nullptr ? nullptr : acc + ((size_t)h * var.pad_rows + it.pad0 + (size_t)it.tile * var.unit) * D;
-        for (int r0 = 0; r0 < n; r0 += RPB) {
-            const int r = r0 + threadIdx.x / LPR;
-            const bool live = r < n;
-            const size_t at = ((row0 + (live ? r : 0)) * Hq + h) * D;  // every lane takes part in the shuffles
-            if (acc != nullptr && live)
-                for (int c = sub * 4; c < D; c += 4 * LPR)
-                    *reinterpret_cast<float4 *>(arow0 + (size_t)r * D + c) = make_float4(0.f, 0.f, 0.f, 0.f);
-            float sum = 0.0f;
+        // NR rows a lane at once, all their loads issued before the first is used
+        for (int r0 = threadIdx.x / LPR; r0 - (int)(threadIdx.x / LPR) < n; r0 += NR * RPB) {
+            float sum[NR];
+#pragma unroll
+            for (int e = 0; e < NR; e++) sum[e] = 0.0f;
 #pragma unroll
             for (int c = sub * 8; c < D; c += 8 * LPR) {
-                float a[8], b[8];
-                load8(o + at + c, a);
-                load8(dO + at + c, b);
-                if (o_res != nullptr) {
-                    float r[8];
-                    load8(o_res + at + c, r);
+                float a[NR][8], b[NR][8], x[NR][8];
 #pragma unroll
-                    for (int i = 0; i < 8; i++) a[i] += r[i];
+                for (int e = 0; e < NR; e++) {
+                    // every lane takes part in the shuffles below; rows past the end repeat the first
+                    const size_t at = ((row0 + (r0 + e * RPB < n ? r0 + e * RPB : 0)) * Hq + h) * D + c;
+                    load8(o + at, a[e]);
+                    load8(dO + at, b[e]);
+                    if (o_res != nullptr) load8(o_res + at, x[e]);
                 }
 #pragma unroll
-                for (int i = 0; i < 8; i++) sum = fmaf(a[i], b[i], sum);
+                for (int e = 0; e < NR; e++)
+#pragma unroll
+                    for (int i = 0; i < 8; i++) sum[e] = fmaf(o_res != nullptr ? a[e][i] + x[e][i] : a[e][i], b[e][i], sum[e]);
             }
 #pragma unroll
-            for (int off = LPR / 2; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
-            if (sub == 0 && live) delta[(size_t)h * var.rows + row0 + r] = sum;
+            for (int e = 0; e < NR; e++) {
+                const int r = r0 + e * RPB;
+#pragma unroll
+                for (int off = LPR / 2; off > 0; off >>= 1) sum[e] += __shfl_xor_sync(0xffffffffu, sum[e], off);
+                if (r >= n) continue;
+                if (sub == 0) delta[(size_t)h * var.rows + row0 + r] = sum[e];
+                if (acc != nullptr)
+#pragma unroll
+                    for (int c = sub * 4; c < D; c += 4 * LPR)
+                        *reinterpret_cast<float4 *>(arow0 + (size_t)r * D + c) = make_float4(0.f, 0.f, 0.f, 0.f);
+            }
         }
     }
 }
@@ -303,15 +312,22 @@ __global__ void __launch_bounds__(256) varlen_finalize(const float *__restrict__
         const int n = min(var.unit, it.len - it.tile * var.unit);
         const size_t row0 = (size_t)it.row0 + (size_t)it.tile * var.unit;
         const float *arow0 = acc + ((size_t)h * var.pad_rows + it.pad0 + (size_t)it.tile * var.unit) * D;
-        for (int i = threadIdx.x; i < n * CH; i += 256) {
-            const int r = i / CH, c = i % CH;
-            float f[8];
-            load8(arow0 + (size_t)r * D + c * 8, f);
-            uint4 u;
-            uint32_t *w = reinterpret_cast<uint32_t *>(&u);
+        constexpr int NC = 4;  // chunks a thread loads at once
+        for (int i0 = threadIdx.x; i0 < n * CH; i0 += NC * 256) {
+            float f[NC][8];
 #pragma unroll
-            for (int e = 0; e < 4; e++) w[e] = pack_bf16x2(f[2 * e], f[2 * e + 1]);
-            *reinterpret_cast<uint4 *>(dq + ((row0 + r) * Hq + h) * D + c * 8) = u;
+            for (int k = 0; k < NC; k++)
+                if (i0 + k * 256 < n * CH) load8(arow0 + (size_t)(i0 + k * 256) * 8, f[k]);
+#pragma unroll
+            for (int k = 0; k < NC; k++) {
+                const int i = i0 + k * 256, r = i / CH, c = i % CH;
+                if (i >= n * CH) break;
+                uint4 u;
+                uint32_t *w = reinterpret_cast<uint32_t *>(&u);
+#pragma unroll
+                for (int e = 0; e < 4; e++) w[e] = pack_bf16x2(f[k][2 * e], f[k][2 * e + 1]);
+                *reinterpret_cast<uint4 *>(dq + ((row0 + r) * Hq + h) * D + c * 8) = u;
+            }
         }
     }
 }
