@@ -24,6 +24,7 @@
 #include "sm100.cuh"
 #include "varlen.cuh"
 #include "varlen_f32.cuh"
+#include "varlen_fwd.cuh"
 
 namespace forge {
 namespace {
@@ -580,16 +581,14 @@ forge_status var_fwd_tc(const VarArgs &a, const VarSched &v, void *o, void *o_re
         return launch_pdl(fwd_tc_kernel<D, D, true>, dim3((unsigned)items), dim3(C::THREADS), C::SMEM, a.st, mq, mk, mv,
                           p);
     } else {
-        using C = Fwd2Tc<D>;
+        using C = VarFwdTc<D>;
         // a forward whose backward will want dsink: P in two terms
         const bool split = a.sink != nullptr && o_res != nullptr, cap = a.softcap > 0.0f, win = a.window > 0;
-        auto *kernel = split ? (cap ? fwd2_tc_kernel<D, true, true, true, 1, 1> : fwd2_tc_kernel<D, true, true, true, 0, 1>)
-                       : cap ? (win ? fwd2_tc_kernel<D, true, true, false, 1, 1> : fwd2_tc_kernel<D, true, true, false, 1, 0>)
-                             : (win ? fwd2_tc_kernel<D, true, true, false, 0, 1> : fwd2_tc_kernel<D, true, true, false, 0, 0>);
+        auto *kernel = split ? (cap ? varlen_fwd_tc<D, true, true, true> : varlen_fwd_tc<D, true, false, true>)
+                       : cap ? (win ? varlen_fwd_tc<D, false, true, true> : varlen_fwd_tc<D, false, true, false>)
+                             : (win ? varlen_fwd_tc<D, false, false, true> : varlen_fwd_tc<D, false, false, false>);
         if (set_smem(kernel, C::SMEM) != FORGE_OK) return FORGE_ERR_CUDA;
         // one CTA an SM for every length: its items are handed out as CTAs get done
-        // (one CTA per item was 218 against 211 us on 8K mixed rows, 28 heads, and 835
-        // against 827 us on 16K rows in three sequences, window 4096)
         return launch_pdl(kernel, dim3((unsigned)(items < sm_count() ? items : sm_count())), dim3(C::THREADS), C::SMEM,
                           a.st, mq, mk, mv, mo, p);
     }

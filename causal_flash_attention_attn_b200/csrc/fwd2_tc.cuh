@@ -68,10 +68,8 @@ struct Fwd2Tc {
     static constexpr int B_P_FULL = B_S_FULL + 2;         // [2]
     static constexpr int B_O_FINAL = B_P_FULL + 2;        // [2]
     static constexpr int B_O_EMPTY = B_O_FINAL + 2;       // [2] O_x read out of TMEM
-    static constexpr int B_ITEM = B_O_EMPTY + 2;          // [kVarRing] packed sequences: the next item's number is there
-    static constexpr int NBAR = B_ITEM + kVarRing;
+    static constexpr int NBAR = B_O_EMPTY + 2;
     static constexpr uint32_t OFF_TMEM_SLOT = 512, OFF_ABORT = 516;
-    static constexpr uint32_t OFF_ITEM = 528;             // [kVarRing] item numbers
     static constexpr int EMU_MASK = 7;                 // pairs with (c & 7) == 7 use the FMA-pipe exp2
     static_assert(NBAR * 8 <= 512, "control block");
     static_assert(SMEM <= 232448, "shared memory");
@@ -82,36 +80,22 @@ struct Fwd2Tc {
 // (pairs heaviest first); tile A sees KV tiles [loA, tA], tile B [loB, tB].
 struct Fwd2Item {
     int bh, hq, bkv, tA, tB, qA0, qB0, loA, loB, lo, hi;
-    int row0, T;  // the sequence's first row in the tensors and its length
     bool hasB;
 };
 
-// VAR: the pair comes from the schedule of a packed batch, heads innermost.
-template <class C, bool VAR>
+template <class C>
 __device__ __forceinline__ Fwd2Item fwd2_item(int w, const FwdParams &p) {
     Fwd2Item I;
-    int pr, num_qt = p.num_qt;
-    if constexpr (VAR) {
-        const VarItem it = var_item(p.var, w / p.Hq);
-        pr = it.tile;
-        I.bh = w % p.Hq;
-        I.row0 = it.row0;
-        I.T = it.len;
-        num_qt = (it.len + C::BM - 1) / C::BM;
-    } else {
-        const int nbh = p.B * p.Hq;
-        const int npairs = (p.num_qt + 1) / 2;
-        pr = npairs - 1 - w / nbh;
-        I.bh = w % nbh;
-        I.row0 = 0;
-        I.T = p.T;
-    }
+    const int nbh = p.B * p.Hq;
+    const int npairs = (p.num_qt + 1) / 2;
+    const int pr = npairs - 1 - w / nbh;
+    I.bh = w % nbh;
     const int b = I.bh / p.Hq;
     I.hq = I.bh % p.Hq;
     I.bkv = b * p.Hkv + I.hq / (p.Hq / p.Hkv);
     I.tA = 2 * pr;
     I.tB = 2 * pr + 1;
-    I.hasB = I.tB < num_qt;
+    I.hasB = I.tB < p.num_qt;
     I.qA0 = I.tA * C::BM;
     I.qB0 = I.tB * C::BM;
     I.loA = p.window > 0 ? max(0, I.qA0 - p.window + 1) / C::BN : 0;
@@ -163,44 +147,12 @@ __device__ __forceinline__ void exp_chunk32(const uint32_t (&s)[32], uint64_t sl
     }
 }
 
-// The same with P split into two bf16 terms, P = hi + lo (lo = bf16(P - hi)); every
-// exponential by MUFU (2^-22; the FMA-pipe one is within 3e-6 only).
-template <bool CAP>
-__device__ __forceinline__ void exp_chunk32_split(const uint32_t (&s)[32], uint64_t sl2x2, uint64_t negm2,
-                                                  uint64_t (&rs)[2], uint32_t (&hi)[16], uint32_t (&lo)[16]) {
-#pragma unroll
-    for (int c = 0; c < 16; c++) {
-        const uint64_t x2 = f2_make(__uint_as_float(s[2 * c]), __uint_as_float(s[2 * c + 1]));
-        float y0, y1;
-        f2_split(CAP ? f2_add(x2, negm2) : f2_fma(x2, sl2x2, negm2), y0, y1);
-        const float p0 = ex2_approx(y0), p1 = ex2_approx(y1);
-        rs[c & 1] = f2_add(rs[c & 1], f2_make(p0, p1));
-        hi[c] = pack_bf16x2(p0, p1);
-        const float2 h = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&hi[c]));
-        lo[c] = pack_bf16x2(p0 - h.x, p1 - h.y);
-    }
-}
-
 // Persistent: gridDim.x CTAs walk the work items (pairs of query tiles of one
 // head, heaviest first) in the snake order of snake_item; barrier phases count
 // KV tiles (or items) over the CTA's whole run and TMEM is allocated once.
 // PERSIST = false: one CTA per item (grid = number of items), compiled without
 // the work-item loop.
-// VAR: packed sequences. Items come from the schedule, the tensor maps cover
-// [heads][rows][D] views of the packed tensors, and the rows of the next sequence
-// that a sequence's last tiles bring along are kept out: K's by the causal mask,
-// V's by zeroing them in shared memory (the softmax warpgroup of the last tile,
-// before it hands its P to the MMA warp), O's by storing that tile row by row.
-// SPLIT: O += P V with P as two bf16 terms (P lo beside P hi in S's columns), so that
-// O, and with its residual the backward's Delta, are accurate to ~2^-17 instead of
-// carrying P's rounding. dsink, an f32 gradient that is a sum of Delta over all rows, needs
-// that: 1.6e-3 of its norm off without, 7e-6 with it (1000 + 700 + 333 rows).
-// CAP: -1 the score cap is a run-time choice; 0, 1 compiled without or with it. WIN: the
-// same for the window. The code of either beside the plain path costs the plain one
-// (8K mixed rows: 207 us with both at run time, 199 without the cap's, 195 without
-// the window's too; 16K rows, window 4096: 836 us, 795 without the cap's, 783 with one test
-// for the tiles that every row sees whole, which most tiles of a window are).
-template <int D, bool PERSIST, bool VAR = false, bool SPLIT = false, int CAP = -1, int WIN = -1>
+template <int D, bool PERSIST>
 __global__ void __launch_bounds__(384, 1)
     fwd2_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                    const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmO,
@@ -216,28 +168,10 @@ __global__ void __launch_bounds__(384, 1)
     auto bar = [&](int i) -> uint32_t { return sbase + 8u * (uint32_t)i; };
 
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-    int nitems = ((p.num_qt + 1) / 2) * p.B * p.Hq;
-    volatile int *sItem = reinterpret_cast<volatile int *>(smem_raw + C::OFF_ITEM);
+    const int W = p.window;
+    const int nitems = ((p.num_qt + 1) / 2) * p.B * p.Hq;
     auto item_of = [&](int pass) -> int {
-        if constexpr (PERSIST && VAR) {
-            // the number that the producer took; nitems or more: none left, -1: abort
-            if (pass == 0) return (int)blockIdx.x;
-            if (!mbar_wait(bar(C::B_ITEM + pass % kVarRing), (uint32_t)((pass / kVarRing) & 1), abort_flag)) return -1;
-            return sItem[pass % kVarRing];
-        } else {
-            return PERSIST ? snake_item(pass, (int)blockIdx.x, (int)gridDim.x) : (pass == 0 ? (int)blockIdx.x : nitems);
-        }
-    };
-    // the same by a whole warp, with one answer
-    auto item_of_warp = [&](int pass) -> int {
-        if constexpr (PERSIST && VAR) {
-            if (pass == 0) return (int)blockIdx.x;
-            if (!mbar_wait_warp(bar(C::B_ITEM + pass % kVarRing), (uint32_t)((pass / kVarRing) & 1), abort_flag))
-                return -1;
-            return sItem[pass % kVarRing];
-        } else {
-            return item_of(pass);
-        }
+        return PERSIST ? snake_item(pass, (int)blockIdx.x, (int)gridDim.x) : (pass == 0 ? (int)blockIdx.x : nitems);
     };
 
     if (threadIdx.x == 0) {
@@ -255,8 +189,6 @@ __global__ void __launch_bounds__(384, 1)
             mbar_init(bar(C::B_O_FINAL + x), 1);
             mbar_init(bar(C::B_O_EMPTY + x), 4);
         }
-        if constexpr (PERSIST && VAR)
-            for (int s = 0; s < kVarRing; s++) mbar_init(bar(C::B_ITEM + s), 1);
         *abort_flag = 0;
         fence_mbar_init();
     }
@@ -274,8 +206,7 @@ __global__ void __launch_bounds__(384, 1)
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
-    griddep_wait();  // the previous kernel's writes (q, k, v, max_logit, the schedule) are visible
-    if constexpr (VAR) nitems = var_count(p.var) * p.Hq;
+    griddep_wait();  // the previous kernel's writes (q, k, v, max_logit) are visible
 
     if (warp >= 8) {
         setmaxnreg_dec<PERSIST ? C::REG_CTRL : C::REG_CTRL_ONE>();
@@ -285,24 +216,12 @@ __global__ void __launch_bounds__(384, 1)
                 const uint64_t keep = policy_evict_last();
                 int issued = 0, q_issued = 0;  // ring slots and Q buffers loaded (for the abort drain)
                 bool ok = true;
-                if constexpr (PERSIST && VAR) mbar_arrive(bar(C::B_ITEM));  // pass 0
                 for (int pass = 0; ok && (PERSIST || pass == 0); pass++) {
                     const int w = item_of(pass);
-                    if (VAR && w < 0) {
-                        ok = false;
-                        break;
-                    }
                     if (w >= nitems) break;
-                    const Fwd2Item I = fwd2_item<C, VAR>(w, p);
-                    // packed sequences: the next item's number is on its way while this
-                    // one's queries are loaded
-                    int next = 0;
-                    if constexpr (PERSIST && VAR) {
-                        next = (int)gridDim.x + atomicAdd(p.var.next, 1);
-                    } else {
-                        // this CTA's last item: the next kernel may start launching
-                        if (item_of(pass + 1) >= nitems) griddep_launch_dependents();
-                    }
+                    const Fwd2Item I = fwd2_item<C>(w, p);
+                    // this CTA's last item: the next kernel may start launching
+                    if (item_of(pass + 1) >= nitems) griddep_launch_dependents();
                     // the item's queries once both O stores of the item that used this
                     // buffer NQB items ago have read it
                     const int qb = pass % C::NQB;
@@ -313,17 +232,10 @@ __global__ void __launch_bounds__(384, 1)
                     const uint32_t sQ = sQ0 + (uint32_t)qb * 2 * C::TILE;
                     mbar_arrive_expect_tx(bar(C::B_Q_FULL + qb), I.hasB ? 2 * C::TILE : C::TILE);
                     for (int c = 0; c < C::NCB; c++) {
-                        tma_load_3d(sQ + c * C::CB, &tmQ, bar(C::B_Q_FULL + qb), c * 64, I.row0 + I.qA0, I.bh);
-                        if (I.hasB)
-                            tma_load_3d(sQ + C::TILE + c * C::CB, &tmQ, bar(C::B_Q_FULL + qb), c * 64, I.row0 + I.qB0,
-                                        I.bh);
+                        tma_load_3d(sQ + c * C::CB, &tmQ, bar(C::B_Q_FULL + qb), c * 64, I.qA0, I.bh);
+                        if (I.hasB) tma_load_3d(sQ + C::TILE + c * C::CB, &tmQ, bar(C::B_Q_FULL + qb), c * 64, I.qB0, I.bh);
                     }
                     q_issued++;
-                    if constexpr (PERSIST && VAR) {
-                        sItem[(pass + 1) % kVarRing] = next;
-                        mbar_arrive(bar(C::B_ITEM + (pass + 1) % kVarRing));
-                        if (next >= nitems) griddep_launch_dependents();
-                    }
                     // ring slots in order K(lo), V(lo), K(lo+1), V(lo+1), ...
                     for (int j = I.lo; ok && j <= I.hi; j++) {
                         for (int kv = 0; kv < 2 && ok; kv++) {
@@ -336,7 +248,7 @@ __global__ void __launch_bounds__(384, 1)
                             mbar_arrive_expect_tx(bar(C::B_KV_FULL + st), C::TILE);
                             for (int c = 0; c < C::NCB; c++)
                                 tma_load_3d_hint(sKV + st * C::TILE + c * C::CB, kv ? &tmV : &tmK,
-                                                 bar(C::B_KV_FULL + st), c * 64, I.row0 + j * C::BN, I.bkv, keep);
+                                                 bar(C::B_KV_FULL + st), c * 64, j * C::BN, I.bkv, keep);
                             issued++;
                         }
                     }
@@ -367,12 +279,8 @@ __global__ void __launch_bounds__(384, 1)
                 int pass = 0;
                 for (; ok && (PERSIST || pass == 0); pass++) {
                     const int w = item_of(pass);
-                    if (VAR && w < 0) {
-                        ok = false;
-                        break;
-                    }
                     if (w >= nitems) break;
-                    const Fwd2Item I = fwd2_item<C, VAR>(w, p);
+                    const Fwd2Item I = fwd2_item<C>(w, p);
                     const int qb = pass % C::NQB;
                     const uint32_t sQ = sQ0 + (uint32_t)qb * 2 * C::TILE;
                     // KV range of each tile ([lo_x, hi_x]; empty for a missing tile B)
@@ -393,12 +301,6 @@ __global__ void __launch_bounds__(384, 1)
                         for (int kk = 0; kk < C::BN / 16; kk++)
                             mma_ts(tmem + C::col_o(x), tmem + C::col_s(x) + kk * 8, sdesc_step(dv, kk * 2048), ID_PV,
                                    (acc || kk > 0) ? 1u : 0u);
-                        if constexpr (SPLIT) {
-#pragma unroll
-                            for (int kk = 0; kk < C::BN / 16; kk++)
-                                mma_ts(tmem + C::col_o(x), tmem + C::col_s(x) + 64 + kk * 8, sdesc_step(dv, kk * 2048),
-                                       ID_PV, 1u);
-                        }
                     };
                     if (!(ok = mbar_wait(bar(C::B_Q_FULL + qb), (uint32_t)((pass / C::NQB) & 1), abort_flag))) break;
                     if (!(ok = wait_full(slot0))) break;
@@ -463,23 +365,16 @@ __global__ void __launch_bounds__(384, 1)
         const uint32_t lane_base = (uint32_t)((warp % 4) * 32) << 16;
         const uint32_t tS = tmem + lane_base + C::col_s(x);
         const uint32_t tO = tmem + lane_base + C::col_o(x);
-        const bool cap = CAP < 0 ? p.softcap > 0.0f : CAP > 0;
+        const bool cap = p.softcap > 0.0f;
         const uint64_t sl2x2 = f2_make(p.scale_log2, p.scale_log2);
         int cnt = 0;  // KV tiles of this tile slot over the whole run (S_FULL phases)
-        int slot0 = 0;  // ring slot of the current item's K(lo)
         bool ok = true;
         for (int pass = 0; ok && (PERSIST || pass == 0); pass++) {
-            const int w = item_of_warp(pass);
-            if (VAR && w < 0) {
-                ok = false;
-                break;
-            }
+            const int w = item_of(pass);
             if (w >= nitems) break;
-            const Fwd2Item I = fwd2_item<C, VAR>(w, p);
+            const Fwd2Item I = fwd2_item<C>(w, p);
             const int qb = pass % C::NQB;
             const bool has = (x == 0) || I.hasB;
-            // a window that hides nothing is none
-            const int W = WIN == 0 || (VAR && p.window >= I.T) ? 0 : p.window;
             const int q0 = x ? I.qB0 : I.qA0;
             const int lox = x ? I.loB : I.loA, hix = x ? I.tB : I.tA;
             const int qi = q0 + row;
@@ -493,10 +388,7 @@ __global__ void __launch_bounds__(384, 1)
                 uint32_t s[4][32];
                 tmem_ld128x4(tS, s[0], s[1], s[2], s[3]);
                 tmem_ld_wait128x4(s[0], s[1], s[2], s[3]);
-                if (VAR && cap) {
-#pragma unroll
-                    for (int q4 = 0; q4 < 4; q4++) cap_scores(s[q4], p.cap_in, p.cap_out);
-                } else if (cap) {
+                if (cap) {
 #pragma unroll
                     for (int c = 0; c < 128; c++) {
                         const float v = __uint_as_float(s[c >> 5][c & 31]);
@@ -507,15 +399,13 @@ __global__ void __launch_bounds__(384, 1)
                 // [r0, r0 + 31] (warp-uniform): bit q of `dead` = no key of chunk q
                 // is visible to any of the rows, bit q of `part` = some are.
                 unsigned dead = 0, part = 0;
-                if (WIN != 1 || k0 + 127 > r0 || (W > 0 && k0 <= r0 + 31 - W)) {
 #pragma unroll
-                    for (int q4 = 0; q4 < 4; q4++) {
-                        const int c0 = k0 + 32 * q4;
-                        const bool all_vis = (c0 + 31 <= r0) && (W == 0 || c0 > r0 + 31 - W);
-                        const bool none = (c0 > r0 + 31) || (W > 0 && c0 + 31 <= r0 - W);
-                        dead |= (unsigned)none << q4;
-                        part |= (unsigned)(!all_vis && !none) << q4;
-                    }
+                for (int q4 = 0; q4 < 4; q4++) {
+                    const int c0 = k0 + 32 * q4;
+                    const bool all_vis = (c0 + 31 <= r0) && (W == 0 || c0 > r0 + 31 - W);
+                    const bool none = (c0 > r0 + 31) || (W > 0 && c0 + 31 <= r0 - W);
+                    dead |= (unsigned)none << q4;
+                    part |= (unsigned)(!all_vis && !none) << q4;
                 }
                 if (dead | part) {
 #pragma unroll
@@ -566,16 +456,7 @@ __global__ void __launch_bounds__(384, 1)
                 // 32 scores -> 16 packed P columns; P column c holds scores 2c, 2c+1.
                 // Masked scores are -inf and need the MUFU exp2 (the FMA-pipe one
                 // is only valid for finite arguments); chunks no row sees are 0.
-                if constexpr (SPLIT) {
-#pragma unroll
-                    for (int q4 = 0; q4 < 4; q4++) {
-                        uint32_t pk[16], lo16[16];
-                        if (cap) exp_chunk32_split<true>(s[q4], sl2x2, negm2, rs, pk, lo16);
-                        else exp_chunk32_split<false>(s[q4], sl2x2, negm2, rs, pk, lo16);
-                        tmem_st16(tS + 16 * q4, pk);
-                        tmem_st16(tS + 64 + 16 * q4, lo16);
-                    }
-                } else if (dead | part) {
+                if (dead | part) {
 #pragma unroll
                     for (int q4 = 0; q4 < 4; q4++) {
                         uint32_t pk[16];
@@ -605,20 +486,6 @@ __global__ void __launch_bounds__(384, 1)
                     }
                 }
                 tmem_st_wait();
-                if constexpr (VAR) {
-                    // the sequence's last V tile: thread r zeroes row r if it lies past
-                    // the end. Only this tile slot (the pair's last tile) reads it, and
-                    // it is not released before the PV that waits for this warp.
-                    const int end = I.T - k0;
-                    if (end < C::BN) {
-                        const int slotV = slot0 + 2 * (j - I.lo) + 1;
-                        if (!(ok = mbar_wait_warp(bar(C::B_KV_FULL + slotV % C::NSTAGE),
-                                                  (uint32_t)((slotV / C::NSTAGE) & 1), abort_flag)))
-                            break;
-                        zero_tail_rows<128, C::NCB, 128>(sKV + (uint32_t)(slotV % C::NSTAGE) * C::TILE, C::CB, end, row);
-                        fence_proxy_async_smem();
-                    }
-                }
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(bar(C::B_P_FULL + x));
@@ -644,22 +511,11 @@ __global__ void __launch_bounds__(384, 1)
                     tmem_ld32(tO + c0, o);
                     tmem_ld_wait(o);
                     uint32_t w16[16];
-                    if (VAR && p.o_res != nullptr) {
-                        uint32_t lo16[16];
-                        o_pairs32(o, inv_l, w16, lo16);
-                        if (qi < I.T) {
-                            __nv_bfloat16 *dst = p.o_res + ((size_t)(I.row0 + qi) * p.Hq + I.bh) * D + c0;
-                            st_global_v8(dst, lo16);
-                            st_global_v8(dst + 16, lo16 + 8);
-                        }
-                    } else {
 #pragma unroll
-                        for (int i = 0; i < 16; i++) {
-                            float a, bb;
-                            f2_split(f2_mul(f2_make(__uint_as_float(o[2 * i]), __uint_as_float(o[2 * i + 1])), inv2), a,
-                                     bb);
-                            w16[i] = pack_bf16x2(a, bb);
-                        }
+                    for (int i = 0; i < 16; i++) {
+                        float a, bb;
+                        f2_split(f2_mul(f2_make(__uint_as_float(o[2 * i]), __uint_as_float(o[2 * i + 1])), inv2), a, bb);
+                        w16[i] = pack_bf16x2(a, bb);
                     }
                     const uint32_t rowaddr = sO + (uint32_t)(c0 / 64) * C::CB + (uint32_t)row * 128u;
                     const uint32_t ch0 = (uint32_t)((c0 % 64) / 8);
@@ -676,34 +532,19 @@ __global__ void __launch_bounds__(384, 1)
             if (has) {
                 fence_proxy_async_smem();
                 named_barrier_sync(1 + x, 128);
-                if (VAR && q0 + C::BM > I.T) {
-                    // a box would write into the next sequence: the rows up to the end,
-                    // D / 8 chunks of 16 bytes each, one chunk a thread at a time
-                    for (int i = row; i < (I.T - q0) * (D / 8); i += 128) {
-                        const int r = i / (D / 8), ch = i % (D / 8);
-                        uint4 w4;
-                        asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
-                                     : "=r"(w4.x), "=r"(w4.y), "=r"(w4.z), "=r"(w4.w)
-                                     : "r"(sO + (uint32_t)(ch / 8) * C::CB + (uint32_t)r * 128u +
-                                           (((uint32_t)(ch % 8) ^ (uint32_t)(r & 7)) << 4)));
-                        *reinterpret_cast<uint4 *>(p.o + ((size_t)(I.row0 + q0 + r) * p.Hq + I.bh) * D + ch * 8) = w4;
-                    }
-                    named_barrier_sync(1 + x, 128);  // the buffer is read before it is released below
-                } else if (row == 0) {
-                    for (int cb = 0; cb < C::NCB; cb++)
-                        tma_store_3d(&tmO, sO + cb * C::CB, cb * 64, I.row0 + q0, I.bh);
+                if (row == 0) {
+                    for (int cb = 0; cb < C::NCB; cb++) tma_store_3d(&tmO, sO + cb * C::CB, cb * 64, q0, I.bh);
                     bulk_commit();
                     bulk_wait_read<0>();
                 }
-                if (qi < I.T) p.lse[(size_t)I.bh * (VAR ? p.var.rows : p.T) + I.row0 + qi] = (m + __log2f(l)) * kLn2;
-                if (!VAR && p.max_logit) {
+                if (qi < p.T) p.lse[(size_t)I.bh * p.T + qi] = (m + __log2f(l)) * kLn2;
+                if (p.max_logit) {
                     const float r = warp_max_f32(qi < p.T ? mraw * kLn2 : -INFINITY);
                     if (lane == 0) atomic_max_f32(p.max_logit + I.bh, r);
                 }
             }
             // the Q buffer is free for the item NQB ahead once both tiles' stores read it
             if (row == 0) mbar_arrive(bar(C::B_Q_EMPTY + qb));
-            slot0 += 2 * (I.hi - I.lo + 1);
         }
     }
 

@@ -259,9 +259,13 @@ def test_equal_lengths_give_the_dense_call(D, T):
         return x.view(B, T, -1, D).transpose(1, 2).contiguous()
     do, dl = fa.attention_fwd(dense(q), dense(k), dense(v))
     ddq, ddk, ddv = fa.attention_bwd(dense(q), dense(k), dense(v), do, dl, dense(dO))
-    # the same forward on the same tiles in the same order; the packed backward may cut a key
+    # the packed forward at head dims 64 and 128 splits a tile's columns between two warps, which take
+    # another exponential where only one half is masked; the packed backward may cut a key
     # tile's queries into parts, whose sums then add up in another order
-    assert torch.equal(dense(o), do) and torch.equal(lse.view(Hq, B, T).transpose(0, 1), dl)
+    if D == 256:
+        assert torch.equal(dense(o), do) and torch.equal(lse.view(Hq, B, T).transpose(0, 1), dl)
+    check_close("o", dense(o), do.double().cpu().numpy(), "bf16")
+    check_close("lse", lse.view(Hq, B, T).transpose(0, 1), dl.double().cpu().numpy(), "bf16")
     check_close("dk", dense(dk), ddk.double().cpu().numpy(), "bf16")
     check_close("dv", dense(dv), ddv.double().cpu().numpy(), "bf16")
     check_close("dq", dense(dq), ddq.double().cpu().numpy(), "bf16")
