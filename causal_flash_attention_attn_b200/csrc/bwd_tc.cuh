@@ -362,7 +362,7 @@ __device__ __forceinline__ void bwd_store_ds(const uint32_t (&dk)[16], int c0, i
 template <class C>
 __device__ __forceinline__ void bwd_mma_kq(uint32_t d_tmem, uint32_t sA, uint32_t sB) {
     constexpr uint32_t ID = idesc_bf16_f32(128, C::BM, false, false);
-    const uint64_t da = sdesc_sw128(opaque_u32(sA), 16, 1024), db = sdesc_sw128(opaque_u32(sB), 16, 1024);
+    const uint64_t da = sdesc_sw128(sA, 16, 1024), db = sdesc_sw128(sB, 16, 1024);
 #pragma unroll
     for (int kk = 0; kk < C::D / 16; kk++) {
         const uint32_t oa = (kk >> 2) * C::CBK + (kk & 3) * 32;
@@ -374,7 +374,7 @@ __device__ __forceinline__ void bwd_mma_kq(uint32_t d_tmem, uint32_t sA, uint32_
 template <class C>
 __device__ __forceinline__ void bwd_mma_dv(uint32_t tmem, uint32_t sdO_h, bool first) {
     constexpr uint32_t ID = idesc_bf16_f32(128, C::DH, false, true);
-    const uint64_t db = sdesc_sw128(opaque_u32(sdO_h), C::CBQ, 1024);
+    const uint64_t db = sdesc_sw128(sdO_h, C::CBQ, 1024);
 #pragma unroll
     for (int kk = 0; kk < C::BM / 16; kk++)
         mma_ts(tmem + C::COL_DV, tmem + C::col_p(kk), sdesc_step(db, kk * 2048), ID,
@@ -384,7 +384,7 @@ __device__ __forceinline__ void bwd_mma_dv(uint32_t tmem, uint32_t sdO_h, bool f
 template <class C>
 __device__ __forceinline__ void bwd_mma_dk(uint32_t tmem, uint32_t sdS, uint32_t sQ_h, bool first) {
     constexpr uint32_t ID = idesc_bf16_f32(128, C::DH, false, true);
-    const uint64_t da = sdesc_sw128(opaque_u32(sdS), 16, 1024), db = sdesc_sw128(opaque_u32(sQ_h), C::CBQ, 1024);
+    const uint64_t da = sdesc_sw128(sdS, 16, 1024), db = sdesc_sw128(sQ_h, C::CBQ, 1024);
 #pragma unroll
     for (int kk = 0; kk < C::BM / 16; kk++) {
         const uint32_t oa = (kk >> 2) * C::CBK + (kk & 3) * 32;
@@ -397,8 +397,8 @@ template <class C>
 __device__ __forceinline__ void bwd_mma_dq(uint32_t tmem, uint32_t sdS, uint32_t sK, uint32_t sK_h) {
     constexpr uint32_t ID =
         C::DQT ? idesc_bf16_f32(128, C::BM, true, true) : idesc_bf16_f32(128, C::D, true, true);
-    const uint64_t ds_mn = sdesc_sw128(opaque_u32(sdS), C::CBK, 1024);
-    const uint64_t dk_mn = sdesc_sw128(opaque_u32(C::DQT ? sK_h : sK), C::CBK, 1024);
+    const uint64_t ds_mn = sdesc_sw128(sdS, C::CBK, 1024);
+    const uint64_t dk_mn = sdesc_sw128(C::DQT ? sK_h : sK, C::CBK, 1024);
 #pragma unroll
     for (int kk = 0; kk < C::BN / 16; kk++) {
         if constexpr (C::DQT) {
@@ -684,15 +684,24 @@ __global__ void __launch_bounds__(512, 1)
                 if (C::QSHADOW && qsh_issued > 0)
                     mbar_wait_drain(bar(C::B_QSH_FULL), (uint32_t)((qsh_issued - 1) & 1), 200000000ull);
             }
-        } else if (warp == C::W_MMA && lane == 0) {
+        } else if (warp == C::W_MMA) {
             // ------------------------------------------------------ MMA issuer
+            // The whole warp walks the schedule and one elected lane issues, so that
+            // addresses and descriptors are known to be equal across the warp (against a
+            // branch that only lane 0 enters: head dim 256, capped, 3000 + 905 + 191 rows
+            // 284 -> 268 us; 128, 8K mixed rows 551 -> 547).
+            const bool lead = elect_one();
+            const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
+            auto commit = [&](int b) {
+                if (lead) tc_commit(bar(b));
+            };
             // S^T(j) = K Q(j)^T once stage j % QST holds Q(j) (j counts steps over all items)
             // (fixed: one phase bit for each barrier of cleared stages; ragged: the step's
             // query tile runs past the sequence's end)
             uint32_t fixed = 0;
             auto wait_fix = [&](int b) -> bool {
                 const uint32_t bit = 1u << (b - C::B_KV_FIX);
-                const bool done = mbar_wait(bar(b), (fixed & bit) ? 1u : 0u, abort_flag);
+                const bool done = mbar_wait_warp(bar(b), (fixed & bit) ? 1u : 0u, abort_flag);
                 fixed ^= bit;
                 return done;
             };
@@ -700,7 +709,7 @@ __global__ void __launch_bounds__(512, 1)
                 if (VAR && ragged) {
                     if (!wait_fix(C::B_Q_FIX + j % C::QST)) return false;
                 } else {
-                    if (!mbar_wait(bar(C::B_Q_FULL + j % C::QST), (uint32_t)((j / C::QST) & 1), abort_flag)) return false;
+                    if (!mbar_wait_warp(bar(C::B_Q_FULL + j % C::QST), (uint32_t)((j / C::QST) & 1), abort_flag)) return false;
                 }
                 tc_fence_after();
                 return true;
@@ -709,7 +718,7 @@ __global__ void __launch_bounds__(512, 1)
             bool ok = true;
             int gs = 0, pass = 0;
             for (; ok; pass++) {
-                const int w = item_of(pass);
+                const int w = item_of_warp(pass);
                 if (VAR && w < 0) {
                     ok = false;
                     break;
@@ -723,7 +732,7 @@ __global__ void __launch_bounds__(512, 1)
                 if (VAR && I.T - I.k0 < C::BN) {
                     if (!(ok = wait_fix(C::B_KV_FIX + kvs))) break;
                 } else {
-                    if (!(ok = mbar_wait(bar(C::B_KV_FULL + kvs), (uint32_t)((pass / C::NKV) & 1), abort_flag))) break;
+                    if (!(ok = mbar_wait_warp(bar(C::B_KV_FULL + kvs), (uint32_t)((pass / C::NKV) & 1), abort_flag))) break;
                 }
                 tc_fence_after();
                 // step order of the item, one step ahead: which query tiles are ragged
@@ -731,15 +740,15 @@ __global__ void __launch_bounds__(512, 1)
                 auto ragged = [&]() -> bool { return VAR && I.T - sp.m * C::BM < C::BM; };
                 bool now = ragged();  // this step's
                 if (!(ok = wait_q(gs, now))) break;
-                bwd_mma_kq<C>(tmem + C::COL_S, sK, sQ0 + (gs % C::QST) * C::TQ);
-                tc_commit(bar(C::B_S_FULL));
+                if (lead) bwd_mma_kq<C>(tm + C::COL_S, sK, sQ0 + (gs % C::QST) * C::TQ);
+                commit(C::B_S_FULL);
                 // in the aliased layout dP^T overwrites the previous dQ^T: wait for its drain
                 if (C::DQ_ALIAS && gs > 0) {
-                    if (!(ok = mbar_wait(bar(C::B_DQ_FREE), (uint32_t)((gs - 1) & 1), abort_flag))) break;
+                    if (!(ok = mbar_wait_warp(bar(C::B_DQ_FREE), (uint32_t)((gs - 1) & 1), abort_flag))) break;
                     tc_fence_after();
                 }
-                bwd_mma_kq<C>(tmem + C::COL_DP, sV, sdO0 + (gs % C::QST) * C::TQ);
-                tc_commit(bar(C::B_DP_FULL));
+                if (lead) bwd_mma_kq<C>(tm + C::COL_DP, sV, sdO0 + (gs % C::QST) * C::TQ);
+                commit(C::B_DP_FULL);
                 for (int i = 0; i < I.steps; i++, gs++) {
                     const int st = gs % C::QST;
                     const uint32_t sQ = sQ0 + st * C::TQ, sdO = sdO0 + st * C::TQ;
@@ -750,17 +759,17 @@ __global__ void __launch_bounds__(512, 1)
                         now = more && ragged();  // from here on the next step's
                     }
                     // dV += P^T dO, P^T from TMEM (phase A of step gs)
-                    if (!(ok = mbar_wait(bar(C::B_P_FULL), (uint32_t)(gs & 1), abort_flag))) break;
+                    if (!(ok = mbar_wait_warp(bar(C::B_P_FULL), (uint32_t)(gs & 1), abort_flag))) break;
                     tc_fence_after();
                     // the first dV and dK of an item overwrite the accumulators: the
                     // previous item's must have been read out
                     if (i == 0 && pass > 0) {
-                        if (!(ok = mbar_wait(bar(C::B_EPI_DONE), (uint32_t)((pass - 1) & 1), abort_flag))) break;
+                        if (!(ok = mbar_wait_warp(bar(C::B_EPI_DONE), (uint32_t)((pass - 1) & 1), abort_flag))) break;
                         tc_fence_after();
                     }
-                    bwd_mma_dv<C>(tmem, sdO + h_q, i == 0);
+                    if (lead) bwd_mma_dv<C>(tm, sdO + h_q, i == 0);
                     // with the Q shadow, dV(gs) is the stage's last reader
-                    if constexpr (C::QSHADOW) tc_commit(bar(C::B_Q_EMPTY + st));
+                    if constexpr (C::QSHADOW) commit(C::B_Q_EMPTY + st);
                     // S^T(gs + 1) over S^T(gs) / P^T(gs): phase A has read S^T(gs), and
                     // dV(gs) is ahead of it on the tensor cores. It runs while the compute
                     // warps form dS of step gs. With a single Q/dO stage Q(gs + 1) can
@@ -768,62 +777,62 @@ __global__ void __launch_bounds__(512, 1)
                     // after dQ(gs).
                     if (EARLY_S && more) {
                         if (!(ok = wait_q(gs + 1, now))) break;
-                        bwd_mma_kq<C>(tmem + C::COL_S, sK, sQ0 + ((gs + 1) % C::QST) * C::TQ);
-                        tc_commit(bar(C::B_S_FULL));
+                        if (lead) bwd_mma_kq<C>(tm + C::COL_S, sK, sQ0 + ((gs + 1) % C::QST) * C::TQ);
+                        commit(C::B_S_FULL);
                     }
                     // dK += dS^T Q, then dQ (phase B of step gs). dK goes first: Q(gs + 2)
                     // (or, with one stage, Q(gs + 1)) can be loaded once the products that
                     // read Q(gs) have completed. (Issuing dQ first, so that its copy-out
                     // overlaps dK, measured slower: 0.76 against 0.68 ms on the 4K GQA
                     // layer.)
-                    if (!(ok = mbar_wait(bar(C::B_DS_FULL), (uint32_t)(gs & 1), abort_flag))) break;
+                    if (!(ok = mbar_wait_warp(bar(C::B_DS_FULL), (uint32_t)(gs & 1), abort_flag))) break;
                     tc_fence_after();
                     if constexpr (C::QSHADOW) {
                         if (VAR && here) {
                             if (!(ok = wait_fix(C::B_QSH_FIX))) break;
                         } else {
-                            if (!(ok = mbar_wait(bar(C::B_QSH_FULL), (uint32_t)(gs & 1), abort_flag))) break;
+                            if (!(ok = mbar_wait_warp(bar(C::B_QSH_FULL), (uint32_t)(gs & 1), abort_flag))) break;
                         }
                         tc_fence_after();
-                        bwd_mma_dk<C>(tmem, sdS, sQsh, i == 0);
-                        tc_commit(bar(C::B_QSH_EMPTY));
+                        if (lead) bwd_mma_dk<C>(tm, sdS, sQsh, i == 0);
+                        commit(C::B_QSH_EMPTY);
                     } else {
-                        bwd_mma_dk<C>(tmem, sdS, sQ + h_q, i == 0);
-                        tc_commit(bar(C::B_Q_EMPTY + st));  // Q, dO of this step read by every product issued
+                        if (lead) bwd_mma_dk<C>(tm, sdS, sQ + h_q, i == 0);
+                        commit(C::B_Q_EMPTY + st);  // Q, dO of this step read by every product issued
                     }
                     // the drain warps must have emptied the previous dQ (in the aliased
                     // layout they did so before dP^T(gs) was issued)
                     if (!C::DQ_ALIAS && gs > 0) {
-                        if (!(ok = mbar_wait(bar(C::B_DQ_FREE), (uint32_t)((gs - 1) & 1), abort_flag))) break;
+                        if (!(ok = mbar_wait_warp(bar(C::B_DQ_FREE), (uint32_t)((gs - 1) & 1), abort_flag))) break;
                         tc_fence_after();
                     }
-                    bwd_mma_dq<C>(tmem, sdS, sK, sK + h_k);
-                    tc_commit(bar(C::B_DQ_FULL));
-                    tc_commit(bar(C::B_DS_EMPTY));
+                    if (lead) bwd_mma_dq<C>(tm, sdS, sK, sK + h_k);
+                    commit(C::B_DQ_FULL);
+                    commit(C::B_DS_EMPTY);
                     if (!EARLY_S && more) {
                         if (!(ok = wait_q(gs + 1, now))) break;
-                        bwd_mma_kq<C>(tmem + C::COL_S, sK, sQ0 + ((gs + 1) % C::QST) * C::TQ);
-                        tc_commit(bar(C::B_S_FULL));
+                        if (lead) bwd_mma_kq<C>(tm + C::COL_S, sK, sQ0 + ((gs + 1) % C::QST) * C::TQ);
+                        commit(C::B_S_FULL);
                     }
                     if (more) {
                         // dP^T(gs + 1): phase B has read dP^T(gs); in the aliased layout it
                         // also overwrites dQ^T(gs), so wait for the drain warps
                         if (C::DQ_ALIAS) {
-                            if (!(ok = mbar_wait(bar(C::B_DQ_FREE), (uint32_t)(gs & 1), abort_flag))) break;
+                            if (!(ok = mbar_wait_warp(bar(C::B_DQ_FREE), (uint32_t)(gs & 1), abort_flag))) break;
                             tc_fence_after();
                         }
-                        bwd_mma_kq<C>(tmem + C::COL_DP, sV, sdO0 + ((gs + 1) % C::QST) * C::TQ);
-                        tc_commit(bar(C::B_DP_FULL));
+                        if (lead) bwd_mma_kq<C>(tm + C::COL_DP, sV, sdO0 + ((gs + 1) % C::QST) * C::TQ);
+                        commit(C::B_DP_FULL);
                     }
                 }
                 if (!ok) break;
-                tc_commit(bar(C::B_KV_EMPTY + kvs));  // K, V of this item read by every product issued
-                tc_commit(bar(C::B_KDONE));           // dK, dV of this item final
+                commit(C::B_KV_EMPTY + kvs);  // K, V of this item read by every product issued
+                commit(C::B_KDONE);           // dK, dV of this item final
             }
             if (!ok) {
                 // let every product issued finish before TMEM is released
-                tc_commit(bar(C::B_KDONE));
-                mbar_wait_drain(bar(C::B_KDONE), (uint32_t)(pass & 1), 200000000ull);
+                commit(C::B_KDONE);
+                if (lead) mbar_wait_drain(bar(C::B_KDONE), (uint32_t)(pass & 1), 200000000ull);
             }
         } else if (VAR && warp > C::W_MMA) {
             // -------------------- packed sequences: zero the rows past the end

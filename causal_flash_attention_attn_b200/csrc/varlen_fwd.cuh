@@ -10,13 +10,15 @@
 // here: two share a tile's rows and split its 128 columns, 64 scores a thread, four warps on
 // each SM sub-partition instead of two for the exponentials. The halves exchange only the
 // row's maximum (shared memory, one barrier of 64 threads a tile) and, at the end, its sum.
-// MEASURED
+// Then the products pace the tile pair, and how they are issued matters: see the MMA issuer.
+// 16,384 tokens, 32 / 8 heads, D 128, window 4096: two softmax warpgroups 775 us, four 764,
+// with the products issued by an elected lane 707 us (1.0 PFLOP/s of the entries needed).
 //
 // Roles (640 threads): warps 0-15 softmax (tile warp / 8, column half warp / 4 % 2, TMEM lanes
 // 32 (warp % 4)..), warp 16 TMA producer, warp 17 MMA issuer and TMEM owner, warps 18-19 idle
-// (they complete the fifth warpgroup). TMEM: S_A, S_B (128 columns each; P overwrites its
-// S as bf16: half h's 64 keys in columns 32 h.., written after both halves have read their
-// scores, i.e. behind the exchange), O_A, O_B (D columns each). MMA order per KV tile j:
+// (they complete the fifth warpgroup). TMEM: S_A, S_B (128 columns each; the P of each column
+// half overwrites that half's own scores as bf16, so neither half waits for the other to have
+// read its scores), O_A, O_B (D columns each). MMA order per KV tile j:
 // PV_A(j), QK_A(j+1), PV_B(j), QK_B(j+1); QK_x(j+1) is committed after PV_x(j), so that a
 // softmax warp that sees S_x(j+1) may rescale O_x.
 //
@@ -256,19 +258,28 @@ __global__ void __launch_bounds__(640, 1)
             }
         } else if (warp == C::W_MMA) {
             // ---------------------------------------------------------- MMA issuer
-            if (lane == 0) {
+            // The whole warp walks the schedule and one elected lane issues, so that addresses
+            // and descriptors are known to be equal across the warp. Inside a branch that only
+            // lane 0 enters they are not, and issuing a 128 x 128 x 16 product took 90-110
+            // cycles against the 64 that it computes (16K windowed prompt 793 -> 707 us, 8K
+            // mixed rows 194 -> 174 us).
+            {
+                const bool lead = elect_one();
+                const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
                 constexpr uint32_t ID_QK = idesc_bf16_f32(128, 128, false, false);
                 constexpr uint32_t ID_PV = idesc_bf16_f32(128, D, false, true);
                 auto wait_full = [&](int slot) -> bool {
-                    return mbar_wait(bar(C::B_KV_FULL + slot % C::NSTAGE), (uint32_t)((slot / C::NSTAGE) & 1), abort_flag);
+                    return mbar_wait_warp(bar(C::B_KV_FULL + slot % C::NSTAGE), (uint32_t)((slot / C::NSTAGE) & 1), abort_flag);
                 };
-                auto release = [&](int slot) { tc_commit(bar(C::B_KV_EMPTY + slot % C::NSTAGE)); };
+                auto release = [&](int slot) {
+                    if (lead) tc_commit(bar(C::B_KV_EMPTY + slot % C::NSTAGE));
+                };
                 int slot0 = 0;          // ring slot of the current item's K(lo)
                 int cnt0 = 0, cnt1 = 0;  // PVs issued per tile over the whole run (P_FULL phases)
                 bool ok = true;
                 int pass = 0;
                 for (; ok; pass++) {
-                    const int w = item_of(pass);
+                    const int w = item_of_warp(pass);
                     if (w < 0) {
                         ok = false;
                         break;
@@ -280,29 +291,35 @@ __global__ void __launch_bounds__(640, 1)
                     // KV range of each tile ([lo_x, hi_x]; empty for a missing tile B)
                     const int lo0 = I.loA, hi0 = I.tA, lo1 = I.loB, hi1 = I.hasB ? I.tB : -1;
                     auto issue_qk = [&](int x, int slot) {
-                        const uint64_t dq = sdesc_sw128(opaque_u32(sQ + (uint32_t)x * C::TILE), 16, 1024);
-                        const uint64_t dk = sdesc_sw128(opaque_u32(sKV + (slot % C::NSTAGE) * C::TILE), 16, 1024);
+                        const uint64_t dq = sdesc_sw128(sQ + (uint32_t)x * C::TILE, 16, 1024);
+                        const uint64_t dk = sdesc_sw128(sKV + (uint32_t)(slot % C::NSTAGE) * C::TILE, 16, 1024);
+                        if (lead) {
 #pragma unroll
-                        for (int kk = 0; kk < D / 16; kk++) {
-                            const uint32_t off = (kk >> 2) * C::CB + (kk & 3) * 32;
-                            mma_ss(tmem + C::col_s(x), sdesc_step(dq, off), sdesc_step(dk, off), ID_QK, kk > 0);
+                            for (int kk = 0; kk < D / 16; kk++) {
+                                const uint32_t off = (kk >> 2) * C::CB + (kk & 3) * 32;
+                                mma_ss(tm + C::col_s(x), sdesc_step(dq, off), sdesc_step(dk, off), ID_QK, kk > 0);
+                            }
+                            tc_commit(bar(C::B_S_FULL + x));
                         }
-                        tc_commit(bar(C::B_S_FULL + x));
+                        __syncwarp();
                     };
                     auto issue_pv = [&](int x, int slot, bool acc) {
-                        const uint64_t dv = sdesc_sw128(opaque_u32(sKV + (slot % C::NSTAGE) * C::TILE), C::CB, 1024);
-#pragma unroll
-                        for (int kk = 0; kk < C::BN / 16; kk++)
-                            mma_ts(tmem + C::col_o(x), tmem + C::col_p(x, kk), sdesc_step(dv, kk * 2048), ID_PV,
-                                   (acc || kk > 0) ? 1u : 0u);
-                        if constexpr (SPLIT) {
+                        const uint64_t dv = sdesc_sw128(sKV + (uint32_t)(slot % C::NSTAGE) * C::TILE, C::CB, 1024);
+                        if (lead) {
 #pragma unroll
                             for (int kk = 0; kk < C::BN / 16; kk++)
-                                mma_ts(tmem + C::col_o(x), tmem + C::col_p(x, kk) + 32, sdesc_step(dv, kk * 2048), ID_PV,
-                                       1u);
+                                mma_ts(tm + C::col_o(x), tm + C::col_p(x, kk), sdesc_step(dv, kk * 2048), ID_PV,
+                                       (acc || kk > 0) ? 1u : 0u);
+                            if constexpr (SPLIT) {
+#pragma unroll
+                                for (int kk = 0; kk < C::BN / 16; kk++)
+                                    mma_ts(tm + C::col_o(x), tm + C::col_p(x, kk) + 32, sdesc_step(dv, kk * 2048), ID_PV,
+                                           1u);
+                            }
                         }
+                        __syncwarp();
                     };
-                    if (!(ok = mbar_wait(bar(C::B_Q_FULL + qb), (uint32_t)((pass / C::NQB) & 1), abort_flag))) break;
+                    if (!(ok = mbar_wait_warp(bar(C::B_Q_FULL + qb), (uint32_t)((pass / C::NQB) & 1), abort_flag))) break;
                     if (!(ok = wait_full(slot0))) break;
                     tc_fence_after();
                     if (I.lo >= lo0 && I.lo <= hi0) issue_qk(0, slot0);
@@ -319,12 +336,12 @@ __global__ void __launch_bounds__(640, 1)
                             bool &first = x ? first1 : first0;
                             int &cx = x ? cnt1 : cnt0;
                             if (ok && j >= lox && j <= hix) {
-                                if (!(ok = mbar_wait(bar(C::B_P_FULL + x), (uint32_t)(cx & 1), abort_flag))) break;
+                                if (!(ok = mbar_wait_warp(bar(C::B_P_FULL + x), (uint32_t)(cx & 1), abort_flag))) break;
                                 tc_fence_after();
                                 // the first PV of an item overwrites O_x: the previous
                                 // item's O_x must have been read out
                                 if (first && pass > 0) {
-                                    if (!(ok = mbar_wait(bar(C::B_O_EMPTY + x), (uint32_t)((pass - 1) & 1), abort_flag)))
+                                    if (!(ok = mbar_wait_warp(bar(C::B_O_EMPTY + x), (uint32_t)((pass - 1) & 1), abort_flag)))
                                         break;
                                     tc_fence_after();
                                 }
@@ -348,10 +365,12 @@ __global__ void __launch_bounds__(640, 1)
                     if (!ok) break;
                     slot0 += 2 * (I.hi - I.lo + 1);
                     // O_FINAL fires once every MMA of the item (and before) has completed
-                    tc_commit(bar(C::B_O_FINAL + 0));
-                    tc_commit(bar(C::B_O_FINAL + 1));
+                    if (lead) {
+                        tc_commit(bar(C::B_O_FINAL + 0));
+                        tc_commit(bar(C::B_O_FINAL + 1));
+                    }
                 }
-                if (!ok) {
+                if (!ok && lead) {
                     tc_commit(bar(C::B_O_FINAL + 0));
                     mbar_wait_drain(bar(C::B_O_FINAL + 0), (uint32_t)(pass & 1), 200000000ull);
                 }

@@ -7,6 +7,13 @@
 
 namespace forge {
 
+// One lane of a converged warp, always the same.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t x;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(x));
+    return x != 0;
+}
+
 struct alignas(16) VarItem {
     int row0;  // first row of the sequence in the packed tensors
     int len;   // rows of the sequence
