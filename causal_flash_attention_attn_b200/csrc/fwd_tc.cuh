@@ -323,7 +323,13 @@ __global__ void __launch_bounds__(320, 1)
         }
     } else if (warp == C::W_MMA) {
         // ---------------------------------------------------------- MMA issuer
-        if (lane == 0) {
+        // (one elected lane of the converged warp issues: see bwd_tc_kernel)
+        {
+            const bool lead = elect_one();
+            const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
+            auto commit = [&](int b) {
+                if (lead) tc_commit(bar(b));
+            };
             constexpr uint32_t ID_QK = idesc_bf16_f32(128, 128, false, false);
             constexpr uint32_t ID_PV = idesc_bf16_f32(128, DV, false, true);
             int stage = 0;
@@ -335,46 +341,48 @@ __global__ void __launch_bounds__(320, 1)
                 }
             };
             auto qk = [&](int buf) -> bool {
-                if (!mbar_wait(bar(C::B_KV_FULL + stage), ph, abort_flag)) return false;
+                if (!mbar_wait_warp(bar(C::B_KV_FULL + stage), ph, abort_flag)) return false;
                 tc_fence_after();
                 const uint32_t sK = sKV + stage * C::SLOT;
-                const uint32_t dS = tmem + (buf ? C::COL_S1 : C::COL_S0);
+                const uint32_t dS = tm + (buf ? C::COL_S1 : C::COL_S0);
+                const uint64_t dq = sdesc_sw128(sQ, 16, 1024), dk = sdesc_sw128(sK, 16, 1024);
 #pragma unroll
-                for (int kk = 0; kk < DK / 16; kk++) {
+                for (int kk = 0; lead && kk < DK / 16; kk++) {
                     const uint32_t off = (kk >> 2) * C::CB + (kk & 3) * 32;
-                    mma_ss(dS, sdesc_sw128(sQ + off, 16, 1024), sdesc_sw128(sK + off, 16, 1024), ID_QK, kk > 0);
+                    mma_ss(dS, sdesc_step(dq, off), sdesc_step(dk, off), ID_QK, kk > 0);
                 }
-                tc_commit(bar(C::B_S_FULL + buf));
-                tc_commit(bar(C::B_KV_EMPTY + stage));
+                commit(C::B_S_FULL + buf);
+                commit(C::B_KV_EMPTY + stage);
                 next();
                 return true;
             };
             auto pv = [&](int buf, bool acc) -> bool {
-                if (!mbar_wait(bar(C::B_KV_FULL + stage), ph, abort_flag)) return false;
+                if (!mbar_wait_warp(bar(C::B_KV_FULL + stage), ph, abort_flag)) return false;
                 tc_fence_after();
                 const uint32_t sV = sKV + stage * C::SLOT;
-                const uint32_t aP = tmem + (buf ? C::COL_S1 : C::COL_S0);
+                const uint32_t aP = tm + (buf ? C::COL_S1 : C::COL_S0);
+                const uint64_t dv = sdesc_sw128(sV, C::CB, 1024);
 #pragma unroll
-                for (int kk = 0; kk < C::BN / 16; kk++)
-                    mma_ts(tmem + C::COL_O, aP + kk * 8, sdesc_sw128(sV + kk * 2048, C::CB, 1024), ID_PV,
+                for (int kk = 0; lead && kk < C::BN / 16; kk++)
+                    mma_ts(tm + C::COL_O, aP + kk * 8, sdesc_step(dv, kk * 2048), ID_PV,
                            (acc || kk > 0) ? 1u : 0u);
                 if constexpr (C::PSPLIT) {
                     // low parts of P live in columns [64, 128) of the same S buffer
 #pragma unroll
-                    for (int kk = 0; kk < C::BN / 16; kk++)
-                        mma_ts(tmem + C::COL_O, aP + 64 + kk * 8, sdesc_sw128(sV + kk * 2048, C::CB, 1024), ID_PV, 1u);
+                    for (int kk = 0; lead && kk < C::BN / 16; kk++)
+                        mma_ts(tm + C::COL_O, aP + 64 + kk * 8, sdesc_step(dv, kk * 2048), ID_PV, 1u);
                 }
-                tc_commit(bar(C::B_O_READY));
-                tc_commit(bar(C::B_KV_EMPTY + stage));
+                commit(C::B_O_READY);
+                commit(C::B_KV_EMPTY + stage);
                 next();
                 return true;
             };
-            bool ok = mbar_wait(bar(C::B_Q), 0, abort_flag);
+            bool ok = mbar_wait_warp(bar(C::B_Q), 0, abort_flag);
             if (ok) ok = qk(0);
             if (ok && n > 1) ok = qk(1);
             for (int u = 0; ok && u < n; u++) {
                 const int buf = u & 1;
-                ok = mbar_wait(bar(C::B_P_FULL + buf), (uint32_t)((u >> 1) & 1), abort_flag);
+                ok = mbar_wait_warp(bar(C::B_P_FULL + buf), (uint32_t)((u >> 1) & 1), abort_flag);
                 if (!ok) break;
                 tc_fence_after();
                 ok = pv(buf, u > 0);
@@ -383,8 +391,8 @@ __global__ void __launch_bounds__(320, 1)
             // Whether or not the loop finished, O_FINAL fires once every MMA
             // issued so far has completed (the softmax warps or the abort path
             // wait on it before tensor memory is released).
-            tc_commit(bar(C::B_O_FINAL));
-            if (!ok) mbar_wait_drain(bar(C::B_O_FINAL), 0, 200000000ull);
+            commit(C::B_O_FINAL);
+            if (!ok && lead) mbar_wait_drain(bar(C::B_O_FINAL), 0, 200000000ull);
         }
     } else if (warp < 8) {
         // ------------------------------------- softmax (warps 0..7, two column halves)
