@@ -67,7 +67,8 @@ struct VarFwdTc {
     static constexpr int B_KV_EMPTY = B_KV_FULL + NSTAGE;
     static constexpr int B_S_FULL = B_KV_EMPTY + NSTAGE;  // [2]
     static constexpr int B_P_FULL = B_S_FULL + 2;         // [2] eight warps
-    static constexpr int B_O_FINAL = B_P_FULL + 2;        // [2]
+    static constexpr int B_P_HALF = B_P_FULL + 2;         // [2] the first 32 keys of each column half: eight warps
+    static constexpr int B_O_FINAL = B_P_HALF + 2;        // [2]
     static constexpr int B_O_EMPTY = B_O_FINAL + 2;       // [2] O_x read out of TMEM, eight warps
     static constexpr int B_ITEM = B_O_EMPTY + 2;          // [kVarRing] the next item's number is there
     static constexpr int NBAR = B_ITEM + kVarRing;
@@ -165,6 +166,7 @@ __global__ void __launch_bounds__(640, 1)
         for (int x = 0; x < 2; x++) {
             mbar_init(bar(C::B_S_FULL + x), 1);
             mbar_init(bar(C::B_P_FULL + x), 8);
+            mbar_init(bar(C::B_P_HALF + x), 8);
             mbar_init(bar(C::B_O_FINAL + x), 1);
             mbar_init(bar(C::B_O_EMPTY + x), 8);
         }
@@ -303,14 +305,17 @@ __global__ void __launch_bounds__(640, 1)
                         }
                         __syncwarp();
                     };
-                    auto issue_pv = [&](int x, int slot, bool acc) {
+                    // P V over the keys of chunk c (0 or 1) of both column halves
+                    auto issue_pv = [&](int x, int slot, int c, bool acc) {
                         const uint64_t dv = sdesc_sw128(sKV + (uint32_t)(slot % C::NSTAGE) * C::TILE, C::CB, 1024);
                         if (lead) {
 #pragma unroll
-                            for (int kk = 0; kk < C::BN / 16; kk++)
+                            for (int i = 0; i < 4; i++) {
+                                const int kk = (i >> 1) * 4 + 2 * c + (i & 1);
                                 mma_ts(tm + C::col_o(x), tm + C::col_p(x, kk), sdesc_step(dv, kk * 2048), ID_PV,
-                                       (acc || kk > 0) ? 1u : 0u);
-                            if constexpr (SPLIT) {
+                                       (acc || c > 0 || i > 0) ? 1u : 0u);
+                            }
+                            if (SPLIT && c == 1) {
 #pragma unroll
                                 for (int kk = 0; kk < C::BN / 16; kk++)
                                     mma_ts(tm + C::col_o(x), tm + C::col_p(x, kk) + 32, sdesc_step(dv, kk * 2048), ID_PV,
@@ -336,7 +341,7 @@ __global__ void __launch_bounds__(640, 1)
                             bool &first = x ? first1 : first0;
                             int &cx = x ? cnt1 : cnt0;
                             if (ok && j >= lox && j <= hix) {
-                                if (!(ok = mbar_wait_warp(bar(C::B_P_FULL + x), (uint32_t)(cx & 1), abort_flag))) break;
+                                if (!(ok = mbar_wait_warp(bar(C::B_P_HALF + x), (uint32_t)(cx & 1), abort_flag))) break;
                                 tc_fence_after();
                                 // the first PV of an item overwrites O_x: the previous
                                 // item's O_x must have been read out
@@ -345,7 +350,10 @@ __global__ void __launch_bounds__(640, 1)
                                         break;
                                     tc_fence_after();
                                 }
-                                issue_pv(x, slotV, !first);
+                                issue_pv(x, slotV, 0, !first);
+                                if (!(ok = mbar_wait_warp(bar(C::B_P_FULL + x), (uint32_t)(cx & 1), abort_flag))) break;
+                                tc_fence_after();
+                                issue_pv(x, slotV, 1, true);
                                 first = false;
                                 cx++;
                             }
@@ -498,6 +506,18 @@ __global__ void __launch_bounds__(640, 1)
                 const float msub = (m == -INFINITY) ? 0.0f : m;
                 const uint64_t negm2 = f2_make(-msub, -msub);
                 uint64_t rs[2] = {f2_make(0.0f, 0.0f), f2_make(0.0f, 0.0f)};
+                // the sequence's last V tile: its rows past the end become zeros. Only this
+                // tile slot (the pair's last tile) reads it, and it is not released before
+                // the PV that waits for these warps.
+                const int end = I.T - j * C::BN;
+                if (end < C::BN) {
+                    const int slotV = slot0 + 2 * (j - I.lo) + 1;
+                    if (!(ok = mbar_wait_warp(bar(C::B_KV_FULL + slotV % C::NSTAGE), (uint32_t)((slotV / C::NSTAGE) & 1),
+                                              abort_flag)))
+                        break;
+                    zero_tail_rows<128, C::NCB, 256>(sKV + (uint32_t)(slotV % C::NSTAGE) * C::TILE, C::CB, end, t);
+                    fence_proxy_async_smem();
+                }
                 // The scores again from TMEM, chunk by chunk (64 held over the exchange would
                 // not fit the registers). Masked scores are -inf and need the MUFU exp2 (the
                 // FMA-pipe one is only valid for finite arguments); chunks no row sees are 0.
@@ -524,23 +544,11 @@ __global__ void __launch_bounds__(640, 1)
                         exp_chunk32<CAP, true, C::EMU_MASK>(s, sl2x2, negm2, rs, pk);
                     }
                     tmem_st16(tS + 16 * q2, pk);
+                    tmem_st_wait();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(bar((q2 ? C::B_P_FULL : C::B_P_HALF) + x));
                 }
-                tmem_st_wait();
-                // the sequence's last V tile: its rows past the end become zeros. Only this
-                // tile slot (the pair's last tile) reads it, and it is not released before
-                // the PV that waits for these warps.
-                const int end = I.T - j * C::BN;
-                if (end < C::BN) {
-                    const int slotV = slot0 + 2 * (j - I.lo) + 1;
-                    if (!(ok = mbar_wait_warp(bar(C::B_KV_FULL + slotV % C::NSTAGE), (uint32_t)((slotV / C::NSTAGE) & 1),
-                                              abort_flag)))
-                        break;
-                    zero_tail_rows<128, C::NCB, 256>(sKV + (uint32_t)(slotV % C::NSTAGE) * C::TILE, C::CB, end, t);
-                    fence_proxy_async_smem();
-                }
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(bar(C::B_P_FULL + x));
                 float a0, a1, a2, a3;
                 f2_split(rs[0], a0, a1);
                 f2_split(rs[1], a2, a3);
