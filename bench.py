@@ -81,9 +81,9 @@ def _strip_comments(text):
 # shared instruction wrappers. A traffic figure stands only while these are
 # unchanged (the launch configuration lives beside the kernel, in its traits).
 KERNEL_SOURCES = {
-    "bwd_tc_kernel": ("bwd_tc.cuh", "sm100.cuh"),
+    "bwd_tc_kernel": ("bwd_tc.cuh", "varlen_item.cuh", "tanh_poly.cuh", "sm100.cuh"),
     "fwd2_tc_kernel": ("fwd2_tc.cuh", "fwd_tc.cuh", "sm100.cuh"),
-    "fwd_tc_kernel": ("fwd_tc.cuh", "sm100.cuh"),
+    "fwd_tc_kernel": ("fwd_tc.cuh", "varlen_item.cuh", "tanh_poly.cuh", "sm100.cuh"),
     "decode_split": ("decode.cuh", "sm100.cuh"),
     "decode_split_warp": ("decode.cuh", "sm100.cuh"),
     "bwd_dkdv_tc_kernel": ("bwd_dkv.cuh", "bwd_tc.cuh", "fwd_tc.cuh", "sm100.cuh"),
