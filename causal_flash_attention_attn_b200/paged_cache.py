@@ -158,15 +158,24 @@ class PagedCache:
         return (torch.tensor(rows, dtype=torch.int32).to(device),
                 torch.tensor([self._lens[s] for s in seqs], dtype=torch.int32).to(device))
 
+    def _on(self, stream):
+        """The scope in which a call's tables are made: they belong to the stream that reads them, or
+        the memory could be given away before the call has run."""
+        from . import _NOTHING, _scope
+        return _NOTHING if stream is None else _scope(self.k_pages.device, stream)
+
     def append(self, layer, k, v, seqs, starts, cu_seqlens=None, stream=None):
         """Write new tokens of one layer at the positions that extend() returned (paged_append)."""
         import torch
         from . import paged_append
-        starts = torch.tensor(list(starts), dtype=torch.int32).to(self.k_pages.device)
-        paged_append(k, v, self.k_pages[layer], self.v_pages[layer], self.tables(seqs)[0], starts, cu_seqlens, stream)
+        with self._on(stream):
+            starts = torch.tensor(list(starts), dtype=torch.int32).to(self.k_pages.device)
+            table = self.tables(seqs)[0]
+        paged_append(k, v, self.k_pages[layer], self.v_pages[layer], table, starts, cu_seqlens, stream)
 
     def decode(self, layer, q, seqs, stream=None, **options):
         """attention_decode_paged of one new query per sequence; options: scale, window, softcap, sink."""
         from . import attention_decode_paged
-        table, lens = self.tables(seqs)
+        with self._on(stream):
+            table, lens = self.tables(seqs)
         return attention_decode_paged(q, self.k_pages[layer], self.v_pages[layer], table, lens, stream=stream, **options)

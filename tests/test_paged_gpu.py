@@ -334,3 +334,31 @@ def test_a_serving_run():
         if i == 14:
             cache.free(seqs.pop(0))
     assert fa.forge_attn_check() == fa.FORGE_OK
+
+
+def test_cache_calls_on_another_stream_keep_their_tables():
+    # the tables that append and decode build must not be given away while the stream that reads
+    # them is still busy; another tensor of their sizes would hold no page number
+    side, Hkv, D, n = torch.cuda.Stream(), 2, 64, 5
+    g = torch.Generator().manual_seed(4)
+    k, v = (torch.randn(n * 7, Hkv, D, generator=g).bfloat16().to(DEV) for _ in range(2))
+    q = torch.randn(n, 4, D, generator=g).bfloat16().to(DEV)
+    cu = torch.arange(n + 1, dtype=torch.int32, device=DEV) * 7
+    out = []
+    for stream in (None, side):
+        cache = fa.PagedCache(32, Hkv, D, page_size=16)
+        seqs = [cache.new() for _ in range(n)]
+        starts = cache.extend(seqs, [7] * n)
+        if stream is not None:
+            stream.wait_stream(torch.cuda.current_stream())
+            with torch.cuda.stream(stream):
+                torch.cuda._sleep(50_000_000)
+        cache.append(0, k, v, seqs, starts, cu, stream=stream)
+        junk = [torch.full((m,), 1 << 20, dtype=torch.int32, device=DEV) for m in (n, n) * 4]
+        o, lse = cache.decode(0, q, seqs, stream=stream)
+        junk += [torch.full((m,), 1 << 20, dtype=torch.int32, device=DEV) for m in (n, n) * 4]
+        torch.cuda.synchronize()
+        out.append((o, lse))
+        del junk
+    assert torch.equal(out[0][0], out[1][0]) and torch.equal(out[0][1], out[1][1])
+    assert fa.forge_attn_check() == fa.FORGE_OK
