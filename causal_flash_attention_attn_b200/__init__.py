@@ -736,11 +736,15 @@ def _attention_varlen_function():
                 return o
 
             @staticmethod
+            @torch.autograd.function.once_differentiable
             def backward(ctx, dO):
                 # the forward has checked everything but dO, which autograd gives o's type
                 # and shape, with the device and the stream of the forward current
                 q, k, v, o, o_res, lse, cu_seqlens, sink = ctx.saved_tensors
-                dq, dk, dv, dsink = _varlen_bwd(q, k, v, o, o_res, lse, dO.contiguous(), cu_seqlens, sink, *ctx.args)
+                dO = dO.contiguous()
+                if dO.data_ptr() % 16:  # a part of another tensor's gradient may start anywhere
+                    dO = dO.clone()
+                dq, dk, dv, dsink = _varlen_bwd(q, k, v, o, o_res, lse, dO, cu_seqlens, sink, *ctx.args)
                 return dq, dk, dv, None, dsink, None, None, None
 
         _attention_varlen_fn = ForgeAttentionVarlen
@@ -749,7 +753,9 @@ def _attention_varlen_function():
 
 def attention_varlen(q, k, v, cu_seqlens, scale=None, window=0, softcap=0.0, sink=None):
     """attention_varlen_fwd with autograd: o, and gradients for q, k, v (and sink) through the
-    library's backward. The lengths must not change between the forward and its backward."""
+    library's backward (once: there are no second derivatives). The lengths must not change between the
+    forward and its backward. Capture a forward together with its backward, on one stream, while no
+    graph of an earlier call on the same leaves is alive."""
     scale = 1.0 / math.sqrt(q.shape[-1]) if scale is None else float(scale)
     return _attention_varlen_function().apply(q, k, v, cu_seqlens, sink, scale, int(window), float(softcap))
 

@@ -410,3 +410,19 @@ def test_calls_on_two_streams_at_once():
         (o, lse), (dq, dk, dv) = want[i % 4], grads[i % 4]
         assert torch.equal(x[0], o) and torch.equal(x[1], lse) and torch.equal(x[3], dk) and torch.equal(x[4], dv)
     assert fa.forge_attn_check() == fa.FORGE_OK
+
+
+def test_a_gradient_that_starts_anywhere_and_no_second_derivative():
+    # o behind a single element: its gradient is a dense part of the whole one's, 2 bytes off
+    q, k, v, dO, _, cu = make("bf16", [70, 33], 0, 4, 2, 64, 0.0, False, False)
+    x = [t.clone().requires_grad_() for t in (q, k, v)]
+    one = torch.zeros(1, dtype=q.dtype, device=DEV)
+    both = torch.cat([one, fa.attention_varlen(*x, cu).flatten()])
+    got = torch.autograd.grad(both, x, torch.cat([one, dO.flatten()]))
+    o, lse, o_res = fa.attention_varlen_fwd(q, k, v, cu, return_residual=True)
+    want = fa.attention_varlen_bwd(q, k, v, o, lse, dO, cu, o_res=o_res)
+    check_close("dq", got[0], want[0].double().cpu().numpy(), "bf16")
+    assert torch.equal(got[1], want[1]) and torch.equal(got[2], want[2])
+    g = torch.autograd.grad(fa.attention_varlen(*x, cu).float().square().sum(), x, create_graph=True)
+    with pytest.raises(RuntimeError):
+        g[0].float().sum().backward()
