@@ -10,17 +10,23 @@
 // here: two share a tile's rows and split its 128 columns, 64 scores a thread, four warps on
 // each SM sub-partition instead of two for the exponentials. The halves exchange only the
 // row's maximum (shared memory, one barrier of 64 threads a tile) and, at the end, its sum.
-// Then the products pace the tile pair, and how they are issued matters: see the MMA issuer.
+// Then the products pace the tile pair, and how they are issued matters (see the MMA issuer).
+// P is handed over in two chunks, the first 32 keys of both halves and the other 32, so that
+// half of P V runs under the second chunk's exponentials.
 // 16,384 tokens, 32 / 8 heads, D 128, window 4096: two softmax warpgroups 775 us, four 764,
-// with the products issued by an elected lane 707 us (1.0 PFLOP/s of the entries needed).
+// with the products issued by an elected lane 700, with P in two chunks 687 (1.04 PFLOP/s of
+// the entries needed). A tile's chain is now, in cycles: row maximum 440, exchange 250,
+// exponentials 1250, store and hand-off 400, products 1024, commit 400, with the tensor cores
+// busy for 2048 of 3800 a pair. Forming the first chunk's exponentials before the other half's
+// maximum is there, and again if it moved a row, measured slower (687 -> 728: spills).
 //
 // Roles (640 threads): warps 0-15 softmax (tile warp / 8, column half warp / 4 % 2, TMEM lanes
 // 32 (warp % 4)..), warp 16 TMA producer, warp 17 MMA issuer and TMEM owner, warps 18-19 idle
 // (they complete the fifth warpgroup). TMEM: S_A, S_B (128 columns each; the P of each column
 // half overwrites that half's own scores as bf16, so neither half waits for the other to have
 // read its scores), O_A, O_B (D columns each). MMA order per KV tile j:
-// PV_A(j), QK_A(j+1), PV_B(j), QK_B(j+1); QK_x(j+1) is committed after PV_x(j), so that a
-// softmax warp that sees S_x(j+1) may rescale O_x.
+// PV_A(j) in its two chunks, QK_A(j+1), PV_B(j), QK_B(j+1); QK_x(j+1) is committed after
+// PV_x(j), so that a softmax warp that sees S_x(j+1) may rescale O_x.
 //
 // Rows of the next sequence that a sequence's last tiles bring along are kept out: K's by the
 // causal mask, V's by zeroing them in shared memory (the softmax warps of the last tile, before
