@@ -9,7 +9,7 @@
 // Roles (320 threads):
 //   warp 8   TMA producer: Q once, then K/V tiles through an NSTAGE ring in the
 //            order the MMA warp consumes them: K0 K1 | V0 K2 | V1 K3 | ...
-//   warp 9   MMA issuer (one thread) and TMEM owner (512 columns):
+//   warp 9   MMA issuer (one elected lane) and TMEM owner (512 columns):
 //            S_b = Q K_j^T into S buffer b = j % 2 (128 columns each), then
 //            O += P_j V_j with P read from tensor memory (it overwrites S_b).
 //            Two S buffers let QK^T of tile j+1 run while tile j is in softmax.
