@@ -426,3 +426,33 @@ def test_a_gradient_that_starts_anywhere_and_no_second_derivative():
     g = torch.autograd.grad(fa.attention_varlen(*x, cu).float().square().sum(), x, create_graph=True)
     with pytest.raises(RuntimeError):
         g[0].float().sum().backward()
+
+
+def test_captured_autograd_step():
+    q, k, v, dO, _, cu = make("bf16", [200, 1, 155], 0, 4, 2, 128, 0.0, False, False)
+    x = [t.clone().requires_grad_() for t in (q, k, v)]
+
+    def step():
+        o = fa.attention_varlen(*x, cu, window=90)
+        o.backward(dO)
+        return o.detach()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step()
+    torch.cuda.current_stream().wait_stream(side)
+    for t in x:
+        t.grad = None
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        out = step()
+    for t, new in zip(x, (0.5 * q, k + 1, -v)):
+        t.data.copy_(new)
+        t.grad.zero_()  # the captured pass wrote its gradient here and adds nothing on a replay
+    graph.replay()
+    torch.cuda.synchronize()
+    o, lse, o_res = fa.attention_varlen_fwd(*[t.detach() for t in x], cu, window=90, return_residual=True)
+    want = fa.attention_varlen_bwd(*[t.detach() for t in x], o, lse, dO, cu, window=90, o_res=o_res)
+    assert torch.equal(out, o)
+    check_close("dq", x[0].grad, want[0].double().cpu().numpy(), "bf16")
+    assert torch.equal(x[1].grad, want[1]) and torch.equal(x[2].grad, want[2])
