@@ -959,21 +959,21 @@ __global__ void __launch_bounds__(512, 1)
         // -------------------------------- dQ drain (warps 8..11), dK (and dV) epilogue
         const int t = threadIdx.x - 32 * C::W_DRAIN;  // TMEM lane of this thread
         const uint32_t lane_base = (uint32_t)((warp - C::W_DRAIN) * 32) << 16;
+        // With staged dQ the four warps meet at barriers, so they go through the same items
+        // and leave together: a wait that ran out travels in `ok` to the next step's barrier.
         bool ok = true;
         int gs = 0;
-        for (int pass = 0; ok; pass++) {
-            const int w = item_of_warp(pass);
-            if (VAR && w < 0) {
-                ok = false;
-                break;
-            }
-            if (w >= nitems) break;
+        for (int pass = 0, w = (int)blockIdx.x; w < nitems; pass++, w = VAR ? sItem[pass % kVarRing] : item_of(pass)) {
             const BwdItem I = bwd_item<C, VAR>(w, p);
             BwdStep sp(I, p.q_desc);
             for (int i = 0; i < I.steps; i++, gs++, sp.next(I, G, p.q_desc)) {
                 const int g = sp.g, m = sp.m;
                 const int bhq = I.b * p.Hq + I.hkv * G + g;
-                if (!(ok = mbar_wait_warp(bar(C::B_DQ_FULL), (uint32_t)(gs & 1), abort_flag))) break;
+                if (ok) ok = mbar_wait_warp(bar(C::B_DQ_FULL), (uint32_t)(gs & 1), abort_flag);
+                // (the next item's number, read by the loop's step, was published behind this
+                // one's first loads)
+                if (VAR && i == 0) ok = ok && item_of_warp(pass + 1) >= 0;
+                if (!C::BULK_DQ && !ok) break;
                 tc_fence_after();
                 // this thread's dQ values: a query row's DH columns, or (transposed)
                 // a head-dim column's BM rows, in 32-column TMEM loads
@@ -996,7 +996,7 @@ __global__ void __launch_bounds__(512, 1)
                     // that last read it (NSTG steps ago) has read its source.
                     const uint32_t stg = sStg + (uint32_t)(gs % C::NSTG) * C::STG;
                     if (t == 0) bulk_wait_read<C::NSTG - 1>();
-                    named_barrier_sync(1, 128);
+                    if (!(ok = named_barrier_all(1, 128, ok))) break;
                     // thread t = query row t; v = the 64 head-dim values of that row
                     const uint32_t row = stg + (uint32_t)t * 128u;
 #pragma unroll
@@ -1035,7 +1035,10 @@ __global__ void __launch_bounds__(512, 1)
             }
             if (!ok) break;
             // epilogue of the item: dK rows (and dV rows where the drain warps take them)
-            if (!(ok = mbar_wait_warp(bar(C::B_KDONE), (uint32_t)(pass & 1), abort_flag))) break;
+            if (!(ok = mbar_wait_warp(bar(C::B_KDONE), (uint32_t)(pass & 1), abort_flag))) {
+                if (C::BULK_DQ) continue;  // to the next item's first barrier
+                break;
+            }
             tc_fence_after();
             const BwdItem E = VAR ? bwd_item<C, VAR>(w, p) : I;
             const int kj = E.k0 + t;

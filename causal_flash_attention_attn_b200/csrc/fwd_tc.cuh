@@ -411,10 +411,8 @@ __global__ void __launch_bounds__(320, 1)
         for (int u = 0; u < n; u++) {
             const int buf = u & 1;
             const int k0 = (lo + u) * C::BN + hf * 64;  // first key of this half
-            if (!mbar_wait_warp(bar(C::B_S_FULL + buf), (uint32_t)((u >> 1) & 1), abort_flag)) {
-                ok = false;
-                break;
-            }
+            // (a wait that ran out: both warps of the rows leave behind their next barrier)
+            if (ok) ok = mbar_wait_warp(bar(C::B_S_FULL + buf), (uint32_t)((u >> 1) & 1), abort_flag);
             tc_fence_after();
             const uint32_t tS = tmem + lane_base + (buf ? C::COL_S1 : C::COL_S0);
             uint32_t s[2][32];
@@ -452,7 +450,7 @@ __global__ void __launch_bounds__(320, 1)
             // the row max over both halves: exchange through shared memory (both
             // halves have read all their scores, so P may go over S after this)
             xmax[(buf * 2 + hf) * 128 + row] = mh;
-            named_barrier_sync(pair_bar, 64);
+            if (!(ok = named_barrier_all(pair_bar, 64, ok))) break;
             float mx = fmaxf(mh, xmax[(buf * 2 + (hf ^ 1)) * 128 + row]);
             if (!cap) mx *= p.scale_log2;
             mraw = fmaxf(mraw, mx);
@@ -461,10 +459,7 @@ __global__ void __launch_bounds__(320, 1)
             const float factor = moved ? ex2_approx(m - m_new) : 1.0f;
             if (__any_sync(0xffffffffu, moved && u > 0)) {
                 // rescale this half's O columns once PV of the previous tile has landed
-                if (!mbar_wait_warp(bar(C::B_O_READY), (uint32_t)((u - 1) & 1), abort_flag)) {
-                    ok = false;
-                    break;
-                }
+                ok = mbar_wait_warp(bar(C::B_O_READY), (uint32_t)((u - 1) & 1), abort_flag);
                 tc_fence_after();
                 const float f = (moved && u > 0) ? factor : 1.0f;
 #pragma unroll 1
@@ -509,11 +504,9 @@ __global__ void __launch_bounds__(320, 1)
                 const int end = T - (lo + u) * C::BN;
                 if (end < C::BN) {
                     const int load = n > 1 ? min(2 * u + 2, n + u) : 1;
-                    if (!mbar_wait_warp(bar(C::B_KV_FULL + load % C::NSTAGE), (uint32_t)((load / C::NSTAGE) & 1),
-                                        abort_flag)) {
-                        ok = false;
-                        break;
-                    }
+                    if (ok)
+                        ok = mbar_wait_warp(bar(C::B_KV_FULL + load % C::NSTAGE), (uint32_t)((load / C::NSTAGE) & 1),
+                                            abort_flag);
                     zero_tail_rows<C::BN, C::NCBV, 256>(sKV + (uint32_t)(load % C::NSTAGE) * C::SLOT, C::CB, end,
                                                         (int)threadIdx.x);
                     fence_proxy_async_smem();
@@ -525,11 +518,11 @@ __global__ void __launch_bounds__(320, 1)
             l = l * factor + rs;
         }
         if (ok) ok = mbar_wait_warp(bar(C::B_O_FINAL), 0, abort_flag);
+        // both halves' row sums
+        xsum[hf * 128 + row] = l;
+        ok = named_barrier_all(pair_bar, 64, ok);
         if (ok) {
             tc_fence_after();
-            // both halves' row sums
-            xsum[hf * 128 + row] = l;
-            named_barrier_sync(pair_bar, 64);
             const float lt = l + xsum[(hf ^ 1) * 128 + row];
             const float inv_l = 1.0f / lt;
             const int qc = min(qi, T - 1);

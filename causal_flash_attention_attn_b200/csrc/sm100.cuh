@@ -161,6 +161,23 @@ __device__ __forceinline__ void bulk_wait() {
 __device__ __forceinline__ void named_barrier_sync(uint32_t id, uint32_t nthreads) {
     asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(nthreads) : "memory");
 }
+// The same barrier, which also gives every member one answer: whether all of them came with
+// `ok`. A bounded wait may run out for one warp of a group and be met for another (a phase that
+// completes after the abort flag is raised, between their looks at it); a warp that left then
+// would leave the others at the barrier for good. So no member of a group leaves on its own: it
+// brings its answer to the group's next barrier, and all go on or all leave.
+__device__ __forceinline__ bool named_barrier_all(uint32_t id, uint32_t nthreads, bool ok) {
+    uint32_t all;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
+        "setp.ne.u32 q, %3, 0;\n\t"
+        "bar.red.and.pred p, %1, %2, q;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(all)
+        : "r"(id), "r"(nthreads), "r"((uint32_t)ok)
+        : "memory");
+    return all != 0;
+}
 __device__ __forceinline__ uint64_t policy_evict_last() {
     uint64_t p;
     asm volatile("createpolicy.fractional.L2::evict_last.b64 %0, 1.0;" : "=l"(p));

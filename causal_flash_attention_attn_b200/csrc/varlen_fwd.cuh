@@ -403,17 +403,14 @@ __global__ void __launch_bounds__(640, 1)
         const uint64_t sl2x2 = f2_make(p.scale_log2, p.scale_log2);
         int cnt = 0;    // KV tiles of this tile slot over the whole run (S_FULL phases)
         int slot0 = 0;  // ring slot of the current item's K(lo)
-        bool ok = true;
-        for (int pass = 0; ok; pass++) {
-            const int w = item_of_warp(pass);
-            if (w < 0) {
-                ok = false;
-                break;
-            }
-            if (w >= nitems) break;
+        // The warps of a tile go through the same items and leave together: a wait that ran
+        // out for one of them travels in `ok` to the pair's barriers and from there to the
+        // tile's, which ends every item.
+        for (int pass = 0, w = (int)blockIdx.x; w < nitems; pass++, w = sItem[pass % kVarRing]) {
             const VarFwdItem I = varlen_fwd_item(w, p);
             const int qb = pass % C::NQB;
             const bool has = (x == 0) || I.hasB;
+            bool ok = true;
             // a window that hides nothing is none
             const int W = !WIN || p.window >= I.T ? 0 : p.window;
             const int q0 = x ? I.qB0 : I.qA0;
@@ -424,7 +421,7 @@ __global__ void __launch_bounds__(640, 1)
             float l = p.sink && hf == 0 ? 1.0f : 0.0f;  // the sink's 1 counts once
             for (int j = lox; has && j <= hix; j++, cnt++) {
                 const int k0 = j * C::BN + 64 * hf;  // first key of this half
-                if (!(ok = mbar_wait_warp(bar(C::B_S_FULL + x), (uint32_t)(cnt & 1), abort_flag))) break;
+                if (ok) ok = mbar_wait_warp(bar(C::B_S_FULL + x), (uint32_t)(cnt & 1), abort_flag);
                 tc_fence_after();
                 // classes of the two 32-key chunks for this warp's 32 rows (warp-uniform):
                 // bit q of `dead` = no key of chunk q is visible to any of the rows, bit q
@@ -482,7 +479,7 @@ __global__ void __launch_bounds__(640, 1)
                 // behind the next barrier.
                 float *xm = xmax + (x * 2 + (cnt & 1)) * 256 + row;
                 xm[128 * hf] = best;
-                named_barrier_sync(pair_bar, 64);
+                if (!(ok = named_barrier_all(pair_bar, 64, ok))) break;
                 best = fmaxf(best, xm[128 * (hf ^ 1)]);
                 if constexpr (!CAP) best *= p.scale_log2;
                 const float m_new = (best > m + 8.0f) ? best : m;
@@ -518,9 +515,8 @@ __global__ void __launch_bounds__(640, 1)
                 const int end = I.T - j * C::BN;
                 if (end < C::BN) {
                     const int slotV = slot0 + 2 * (j - I.lo) + 1;
-                    if (!(ok = mbar_wait_warp(bar(C::B_KV_FULL + slotV % C::NSTAGE), (uint32_t)((slotV / C::NSTAGE) & 1),
-                                              abort_flag)))
-                        break;
+                    ok = mbar_wait_warp(bar(C::B_KV_FULL + slotV % C::NSTAGE), (uint32_t)((slotV / C::NSTAGE) & 1),
+                                        abort_flag);
                     zero_tail_rows<128, C::NCB, 256>(sKV + (uint32_t)(slotV % C::NSTAGE) * C::TILE, C::CB, end, t);
                     fence_proxy_async_smem();
                 }
@@ -560,8 +556,9 @@ __global__ void __launch_bounds__(640, 1)
                 f2_split(rs[1], a2, a3);
                 l = l * factor + ((a0 + a1) + (a2 + a3));
             }
-            if (!ok) break;
-            if (!(ok = mbar_wait_warp(bar(C::B_O_FINAL + x), (uint32_t)(pass & 1), abort_flag))) break;
+            // (the next item's number, read by the loop's step, was published behind this one's queries)
+            ok = ok && item_of_warp(pass + 1) >= 0 &&
+                 mbar_wait_warp(bar(C::B_O_FINAL + x), (uint32_t)(pass & 1), abort_flag);
             tc_fence_after();
             // Stage this tile's O (bf16) in its Q buffer, which every MMA of the item has
             // finished reading once O_FINAL fired, in the 128-byte-swizzled layout of the O
@@ -569,7 +566,7 @@ __global__ void __launch_bounds__(640, 1)
             const uint32_t sO = sQ0 + (uint32_t)qb * 2 * C::TILE + (uint32_t)x * C::TILE;
             if (has) {
                 xsum[(x * 2 + hf) * 128 + row] = l;
-                named_barrier_sync(pair_bar, 64);
+                ok = named_barrier_all(pair_bar, 64, ok);
                 l += xsum[(x * 2 + (hf ^ 1)) * 128 + row];
                 const float inv_l = 1.0f / l;
                 const uint64_t inv2 = f2_make(inv_l, inv_l);
@@ -608,9 +605,9 @@ __global__ void __launch_bounds__(640, 1)
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(bar(C::B_O_EMPTY + x));
+            if (has) fence_proxy_async_smem();
+            if (!named_barrier_all(tile_bar, 256, ok)) break;
             if (has) {
-                fence_proxy_async_smem();
-                named_barrier_sync(tile_bar, 256);
                 if (q0 + C::BM > I.T) {
                     // a box would write into the next sequence: the rows up to the end,
                     // D / 8 chunks of 16 bytes each, one chunk a thread at a time
