@@ -347,6 +347,12 @@ __global__ void __launch_bounds__(384, 1)
                     }
                     if (!ok) break;
                     slot0 += 2 * (I.hi - I.lo + 1);
+                    // tile B's warps have left the item before even where this one gives them
+                    // nothing to do (no PV waits for them then): a wait by parity must not fall
+                    // two phases behind
+                    if (!I.hasB && pass > 0 &&
+                        !(ok = mbar_wait(bar(C::B_O_EMPTY + 1), (uint32_t)((pass - 1) & 1), abort_flag)))
+                        break;
                     // O_FINAL fires once every MMA of the item (and before) has completed
                     tc_commit(bar(C::B_O_FINAL + 0));
                     tc_commit(bar(C::B_O_FINAL + 1));

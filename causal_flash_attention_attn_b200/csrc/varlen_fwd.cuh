@@ -378,6 +378,13 @@ __global__ void __launch_bounds__(640, 1)
                     }
                     if (!ok) break;
                     slot0 += 2 * (I.hi - I.lo + 1);
+                    // Every O_FINAL phase of a tile comes behind its O_EMPTY of the item before, as the
+                    // first PV sees to where there is one: else tile B's warps, which have nothing
+                    // to do in a run of items without a tile B, could fall two phases behind, and a
+                    // wait by parity would not see the phase that it waits for.
+                    if (!I.hasB && pass > 0 &&
+                        !(ok = mbar_wait_warp(bar(C::B_O_EMPTY + 1), (uint32_t)((pass - 1) & 1), abort_flag)))
+                        break;
                     // O_FINAL fires once every MMA of the item (and before) has completed
                     if (lead) {
                         tc_commit(bar(C::B_O_FINAL + 0));

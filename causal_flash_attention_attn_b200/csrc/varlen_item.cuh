@@ -64,9 +64,12 @@ __device__ __forceinline__ VarItem var_item_part(const VarSched &v, int i) {
 // words, each with a barrier on which every role waits (pass p >= 1: word and barrier
 // p % kVarRing, phase (p / kVarRing) & 1, the barriers of pass 0 completed at the start).
 // No role releases a word. The thread publishes pass p + 1 when it has issued the first
-// loads of pass p, for which the buffers of pass p - 2 (or p - 1) must have been freed:
-// by then every product of pass p - 2 is done, hence every role has finished pass p - 3, and
-// the word to be written, last used for pass p + 1 - kVarRing = p - 7, has been read.
+// loads of pass p, for which the buffers of pass p - 2 (or p - 1) must have been freed. By
+// then the products of pass p - 2 are done, and with them every role has finished pass p - 3:
+// in the backward each step waits for all of its warps; in the forward the last commit of
+// a pass (O_FINAL) waits until all warps of both tiles have left the pass before it
+// (O_EMPTY), whether or not the pass has a tile B. So the word to be written, last used for
+// pass p + 1 - kVarRing = p - 7, has been read.
 constexpr int kVarRing = 8;
 __device__ __forceinline__ int var_count(const VarSched &v) {
     int n;
