@@ -101,6 +101,7 @@ struct BwdTc {
     static constexpr uint32_t OFF_ITEM = 352;  // [kVarRing] packed sequences: item numbers
     static constexpr uint32_t OFF_REQ = 384;   // [NREQ] packed sequences: requests to clear rows
     static constexpr uint32_t OFF_TMEM_SLOT = 416, OFF_ABORT = 420;
+    static constexpr uint32_t OFF_BEAT = 424;  // packed sequences: steps that the load warp has begun
     // LSE and Delta rows of a step, in slot (step % 2): with one Q/dO stage the
     // next step's rows arrive while phase B still reads this step's Delta
     static constexpr uint32_t OFF_LSE = 512;                        // [2][BM] f32, -LSE * log2(e)
@@ -488,6 +489,7 @@ __global__ void __launch_bounds__(512, 1)
     // load warp took; nitems or more: none left, -1: abort
     volatile int *sItem = reinterpret_cast<volatile int *>(ctrl_p + C::OFF_ITEM);
     volatile int *sReq = reinterpret_cast<volatile int *>(ctrl_p + C::OFF_REQ);
+    volatile int *sBeat = reinterpret_cast<volatile int *>(ctrl_p + C::OFF_BEAT);
     // (item_of: by one thread; item_of_warp: by a whole warp, with one answer)
     auto item_of = [&](int pass) -> int {
         if constexpr (VAR) {
@@ -537,6 +539,7 @@ __global__ void __launch_bounds__(512, 1)
             for (int s = 0; s < kVarRing; s++) mbar_init(bar(C::B_ITEM + s), 1);
         }
         *abort_flag = 0;
+        if constexpr (VAR) *sBeat = 0;
         fence_mbar_init();
     }
     if (warp == C::W_LOAD && lane == 0) {
@@ -612,6 +615,7 @@ __global__ void __launch_bounds__(512, 1)
                 if (VAR && I.T - I.k0 < C::BN) request(0, kvs, (uint32_t)((pass / C::NKV) & 1), I.T - I.k0);
                 BwdStep sp(I, p.q_desc);
                 for (int i = 0; i < I.steps; i++, gs++, sp.next(I, G, p.q_desc)) {
+                    if (VAR && lane == 0) *sBeat = gs;
                     const int st = gs % C::QST;
                     const uint32_t ph = (uint32_t)((gs / C::QST) & 1);
                     const int g = sp.g, m = sp.m;
@@ -839,7 +843,9 @@ __global__ void __launch_bounds__(512, 1)
             // (warp 14: K, Q, the Q shadow's first 64 columns; warp 15: V, dO, its others)
             const uint32_t second = warp == C::W_MMA + 1 ? 0u : 1u;
             for (int n = 0;; n++) {
-                if (!mbar_wait_warp(bar(C::B_REQ + n % C::NREQ), (uint32_t)((n / C::NREQ) & 1), abort_flag)) break;
+                // (a request comes only where a sequence ends inside a tile, which may be further
+                // off than the wait's limit, so that the limit runs from the load warp's last step)
+                if (!mbar_wait_warp(bar(C::B_REQ + n % C::NREQ), (uint32_t)((n / C::NREQ) & 1), abort_flag, sBeat)) break;
                 const int r = sReq[n % C::NREQ];
                 if (r < 0) break;
                 const int kind = r >> 16, stage = (r >> 12) & 15, valid = r & 255;

@@ -68,15 +68,23 @@ __device__ __forceinline__ uint32_t mbar_try_wait(uint32_t bar, uint32_t parity)
 // Bounded wait for the phase of parity `parity` to complete. Returns false if
 // the CTA's abort flag is (or becomes) set, or if the limit runs out; in the
 // latter case it records FORGE_ERR_TIMEOUT and sets the abort flag so the other
-// roles of the CTA stop too.
+// roles of the CTA stop too. beat: a word that another role of the CTA keeps changing while
+// it gets on (nullptr = none); for waits whose event may be further off than the limit
+// (one that only some work items bring), the limit then runs from its last change.
 __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatile int *abort_flag,
-                                          unsigned long long limit_ns) {
+                                          unsigned long long limit_ns, const volatile int *beat = nullptr) {
     if (mbar_try_wait(bar, parity)) return true;
-    const uint64_t t0 = globaltimer_ns();
+    uint64_t t0 = globaltimer_ns();
+    int seen = beat != nullptr ? *beat : 0;
     while (true) {
         if (mbar_try_wait(bar, parity)) return true;
         if (*abort_flag) return false;
         if (globaltimer_ns() - t0 > limit_ns) {
+            if (beat != nullptr && *beat != seen) {
+                seen = *beat;
+                t0 = globaltimer_ns();
+                continue;
+            }
             record_status(kStatusTimeout);
             if (atomicCAS(&g_timeout_info[0], 0u, 1u + (bar & 0xFFFFFu)) == 0u) {
                 g_timeout_info[1] = blockIdx.x;
@@ -106,6 +114,10 @@ __device__ __forceinline__ void mbar_wait_drain(uint32_t bar, uint32_t parity, u
 // wait: every lane of the warp gets the same answer.
 __device__ __forceinline__ bool mbar_wait_warp(uint32_t bar, uint32_t parity, volatile int *abort_flag) {
     return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag));
+}
+__device__ __forceinline__ bool mbar_wait_warp(uint32_t bar, uint32_t parity, volatile int *abort_flag,
+                                               const volatile int *beat) {
+    return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag, kWaitLimitNs, beat));
 }
 
 // -------------------------------------------------------------------------- TMA

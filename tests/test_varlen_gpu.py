@@ -456,3 +456,40 @@ def test_captured_autograd_step():
     assert torch.equal(out, o)
     check_close("dq", x[0].grad, want[0].double().cpu().numpy(), "bf16")
     assert torch.equal(x[1].grad, want[1]) and torch.equal(x[2].grad, want[2])
+
+
+def test_a_backward_that_takes_longer_than_a_wait_may():
+    """2^20 rows of one sequence: about three seconds, with no tile that a sequence's end cuts, whose
+    rows two warps of every CTA stand by to clear. Compared on the first 128 rows (which see only
+    one another) and on the last 128 keys (which only the last 128 queries see), with the bounds of
+    `roundings`: u of each term for P and dS and u for the output. lse is the call's (f32, up to ~20 in
+    log2 units: P within 1e-5 of its value, u = 4e-3), and so is Delta, from o + o_res (u^2)."""
+    T, n, Hq, D, u = 1 << 20, 128, 4, 128, 2.0 ** -8
+    g = torch.Generator(device=DEV).manual_seed(2)
+    q, dO = (torch.randn(T, Hq, D, generator=g, device=DEV, dtype=torch.bfloat16) for _ in range(2))
+    k, v = (torch.randn(T, 1, D, generator=g, device=DEV, dtype=torch.bfloat16) for _ in range(2))
+    cu = torch.tensor([0, T], dtype=torch.int32, device=DEV)
+    o, lse, o_res = fa.attention_varlen_fwd(q, k, v, cu, return_residual=True)
+    start, end = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+    start.record()
+    dq, dk, dv = fa.attention_varlen_bwd(q, k, v, o, lse, dO, cu, o_res=o_res)
+    end.record()
+    assert fa.forge_attn_check() == fa.FORGE_OK
+    print(f"backward {start.elapsed_time(end) / 1e3:.2f} s")
+    assert all(bool(torch.isfinite(x).all()) for x in (o, dq, dk, dv, lse))
+    for at, names in ((slice(0, n), ("o", "dq")), (slice(T - n, T), ("dk", "dv"))):
+        qh, dh = (x[at].double().transpose(0, 1) for x in (q, dO))
+        kh, vh = (x[at].double().transpose(0, 1) for x in (k, v))
+        p = (qh @ kh.transpose(1, 2) / math.sqrt(D) - lse[:, at].double()[:, :, None]).exp().tril()
+        whole = (o[at].double() + o_res[at].double()).transpose(0, 1)
+        ds = p * (dh @ vh.transpose(1, 2) - (dh * whole).sum(2, keepdim=True)) / math.sqrt(D)
+        eds = u * ds.abs() + p * u * u * (dh * whole).abs().sum(2, keepdim=True) / math.sqrt(D)
+        pt, dst = p.transpose(1, 2), ds.transpose(1, 2)
+        want = dict(o=(o, p @ vh, p @ vh.abs()), dq=(dq, ds @ kh, eds @ kh.abs() / u),
+                    dk=(dk, (dst @ qh).sum(0, True), (eds.transpose(1, 2) @ qh.abs()).sum(0, True) / u),
+                    dv=(dv, (pt @ dh).sum(0, True), (pt @ dh.abs()).sum(0, True)))
+        for name in names:
+            got, ref, terms = want[name]
+            err = (got[at].double().transpose(0, 1) - ref).abs()
+            tol = 1.05 * u * (ref.abs() + terms) + 1e-30
+            assert bool((err <= tol).all()), (name, float((err / tol).max()))
