@@ -424,7 +424,18 @@ __global__ void __launch_bounds__(320, 1)
             // (the scale is folded into the exponent's FMA, and max commutes
             // with a positive scale)
             const bool cap = p.softcap > 0.0f;
+            const int kt0 = (lo + u) * C::BN;
+            const bool need_mask = (kt0 + C::BN - 1 > q0) || (W > 0 && kt0 <= q0 + C::BM - 1 - W);
             if (VAR && cap) {
+                // the warp's scores choose the tanh's form together: masked ones and those of rows
+                // past the end, which may hold another sequence's values, have no say in it
+                if (need_mask || q0 + C::BM > T) {
+#pragma unroll
+                    for (int c = 0; c < 64; c++) {
+                        const int kj = k0 + c;
+                        if (!(kj <= qi && (W == 0 || kj > qi - W) && qi < T)) s[c >> 5][c & 31] = 0u;
+                    }
+                }
                 cap_scores(s[0], p.cap_in, p.cap_out);
                 cap_scores(s[1], p.cap_in, p.cap_out);
             } else if (cap) {
@@ -434,8 +445,6 @@ __global__ void __launch_bounds__(320, 1)
                     s[c >> 5][c & 31] = __float_as_uint(p.cap_out * tanh_via_ex2(x * p.cap_in));
                 }
             }
-            const int kt0 = (lo + u) * C::BN;
-            const bool need_mask = (kt0 + C::BN - 1 > q0) || (W > 0 && kt0 <= q0 + C::BM - 1 - W);
             if (need_mask) {
 #pragma unroll
                 for (int c = 0; c < 64; c++) {

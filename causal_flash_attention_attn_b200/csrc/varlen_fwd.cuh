@@ -446,15 +446,29 @@ __global__ void __launch_bounds__(640, 1)
                 }
                 // scores of chunk q2 as the softmax sees them
                 auto finish = [&](uint32_t(&s)[32], int q2) {
-                    if constexpr (CAP) cap_scores(s, p.cap_in, p.cap_out);
+                    uint32_t vm = ~0u;
                     if (dead | part) {
                         // bit c of vm: key k0 + 32 q2 + c is visible to row qi, i.e. lo_c < c <= hi_c
                         const int hi_c = qi - (k0 + 32 * q2);
-                        uint32_t vm = hi_c < 0 ? 0u : (hi_c >= 31 ? ~0u : (~0u >> (31 - hi_c)));
+                        vm = hi_c < 0 ? 0u : (hi_c >= 31 ? ~0u : (~0u >> (31 - hi_c)));
                         if (W > 0) {
                             const int lo_c = hi_c - W;
                             vm &= lo_c < 0 ? ~0u : (lo_c >= 31 ? 0u : (~0u << (lo_c + 1)));
                         }
+                    }
+                    if constexpr (CAP) {
+                        // the warp's scores choose the tanh's form together: masked ones and
+                        // those of rows past the end, which may hold another sequence's values,
+                        // have no say in it
+                        if ((dead | part) || r0 + 31 >= I.T) {
+                            const uint32_t keep = qi < I.T ? vm : 0u;
+#pragma unroll
+                            for (int c = 0; c < 32; c++)
+                                if (!((keep >> c) & 1u)) s[c] = 0u;
+                        }
+                        cap_scores(s, p.cap_in, p.cap_out);
+                    }
+                    if (dead | part) {
 #pragma unroll
                         for (int c = 0; c < 32; c++)
                             if (!((vm >> c) & 1u)) s[c] = __float_as_uint(-INFINITY);

@@ -493,3 +493,33 @@ def test_a_backward_that_takes_longer_than_a_wait_may():
             err = (got[at].double().transpose(0, 1) - ref).abs()
             tol = 1.05 * u * (ref.abs() + terms) + 1e-30
             assert bool((err <= tol).all()), (name, float((err / tol).max()))
+
+
+@pytest.mark.parametrize("D,Hq,Hkv", [(64, 3, 3), (128, 4, 2), (256, 2, 1)])
+@pytest.mark.parametrize("W,sink", [(0, False), (70, True)])
+@pytest.mark.parametrize("poison", [float("nan"), float("inf"), -3.0e38, 300.0])
+def test_one_sequences_values_stay_in_it_with_a_cap(D, Hq, Hkv, W, sink, poison):
+    # a capped score takes one of two forms of the tanh (1e-7 apart), by its size and its
+    # neighbours' in the tile: only scores of its own sequence may have a say
+    lens = [100, 200, 61, 300, 5]
+    q, k, v, dO, sk, cu = make("bf16", lens, 9, Hq, Hkv, D, 0.0, sink, False)
+    clean = raw(q, k, v, dO, sk, cu, W, 50.0, 0, res=True)
+    rest = torch.ones(sum(lens) + 9, dtype=torch.bool, device=DEV)
+    rest[sum(lens):] = False
+    for b in (1, 3):
+        rest[int(cu[b]):int(cu[b + 1])] = False
+    for x in (q, k, v, dO):
+        x[~rest] = poison
+    o, lse, dq, dk, dv, _ = raw_unchecked(q, k, v, dO, sk, cu, W, 50.0)
+    assert torch.equal(o[rest], clean[0][rest]) and torch.equal(lse[:, rest], clean[1][:, rest])
+    assert torch.equal(dk[rest], clean[3][rest]) and torch.equal(dv[rest], clean[4][rest])
+    check_close("dq", dq[rest], clean[2][rest].double().cpu().numpy(), "bf16")
+
+
+def raw_unchecked(q, k, v, dO, sk, cu, W, C):
+    """As raw(.., res=True), through the helpers and without its check of o_res (poisoned rows have none)."""
+    o, lse, o_res = fa.attention_varlen_fwd(q, k, v, cu, window=W, softcap=C, sink=sk, return_residual=True)
+    g = fa.attention_varlen_bwd(q, k, v, o, lse, dO, cu, window=W, softcap=C, sink=sk, o_res=o_res)
+    torch.cuda.synchronize()
+    assert fa.forge_attn_check() == fa.FORGE_OK
+    return (o, lse, *g[:3], None)
