@@ -499,8 +499,8 @@ __global__ void __launch_bounds__(kPdThreads, PdCfg<T_, D>::PER_SM) decode_paged
     }
     PdIter at = ld;
 
-    // The page of this warp's step of the iterator's unit; -1 = nothing visible there
-    // (or a page outside the pool, which is reported and read as if it were).
+    // The page of this warp's step of the iterator's unit; -1 = nothing visible there, or a
+    // page outside the pool, which is reported and taken as holding no visible key.
     auto page_of = [&](const PdIter &i) -> int {
         const int key0 = (i.s.u0 + i.j) * C::UNIT + warp * C::KS;
         if (key0 >= i.s.len || key0 + C::KS <= i.s.first) return -1;
@@ -539,6 +539,7 @@ __global__ void __launch_bounds__(kPdThreads, PdCfg<T_, D>::PER_SM) decode_paged
     };
     long long to_load = hi - lo;
     int pg = page_of(ld);
+    unsigned held = 0;  // bit s: stage s holds keys of a page (not just zeros)
     auto issue = [&](int stage) {
         if (to_load > 0) {
             const PdIter now = ld;
@@ -548,6 +549,7 @@ __global__ void __launch_bounds__(kPdThreads, PdCfg<T_, D>::PER_SM) decode_paged
                 pg = page_of(ld);  // one step ahead of its use
             }
             load(now, page_now, stage);
+            held = (held & ~(1u << stage)) | ((unsigned)(page_now >= 0) << stage);
         }
         cp_async_commit();  // an empty group keeps the count
     };
@@ -566,12 +568,13 @@ __global__ void __launch_bounds__(kPdThreads, PdCfg<T_, D>::PER_SM) decode_paged
             if (!C::BF) __syncthreads();
             fresh = false;
         }
+        const int end = (held >> stage) & 1u ? at.s.len : 0;  // no page: no visible key
         cp_async_wait<C::STAGES - 2>();
         __syncwarp();  // every lane's copies of this stage, and all reads of the stage refilled next
         issue(stage == 0 ? C::STAGES - 1 : stage - 1);
         const int key0 = (at.s.u0 + at.j) * C::UNIT + warp * C::KS;
         const uint32_t sK = ring + (uint32_t)(stage * 2 * C::STEP);
-        acc.step(p, sK, sK + C::STEP, key0, at.s.first, at.s.len, G, sP, sQ);
+        acc.step(p, sK, sK + C::STEP, key0, at.s.first, end, G, sP, sQ);
         stage = stage + 1 == C::STAGES ? 0 : stage + 1;
 
         const bool pair_end = at.j + 1 == at.s.nu;

@@ -362,3 +362,39 @@ def test_cache_calls_on_another_stream_keep_their_tables():
         del junk
     assert torch.equal(out[0][0], out[1][0]) and torch.equal(out[0][1], out[1][1])
     assert fa.forge_attn_check() == fa.FORGE_OK
+
+
+@pytest.mark.parametrize("dtype,Hq,Hkv,D", [("bf16", 8, 2, 128), ("bf16", 3, 3, 64), ("bf16", 16, 1, 256),
+                                            ("f32", 8, 2, 128), ("f32", 2, 2, 64), ("f32", 12, 1, 256)])
+@pytest.mark.parametrize("W,C,use_sink", [(0, 0.0, False), (0, 0.0, True), (90, 30.0, True)])
+def test_a_bad_page_holds_no_visible_key(dtype, Hq, Hkv, D, W, C, use_sink):
+    # sequences with a bad page first, inside, last, everywhere, and none, against f64 without those keys
+    lens, ps = [100, 300, 33, 70, 90, 1500], 16
+    kp, vp, table = pool(dtype, lens, ps, Hkv, D, seed=7)
+    bad = table.clone()
+    gone = {0: [0], 1: [5, 6, 18], 2: [2], 3: list(range(5)), 5: [0, 40, 41, 93]}
+    for b, pages in gone.items():
+        for i, at in enumerate(pages):
+            bad[b, at] = (-1, kp.shape[0], 1 << 30)[i % 3]
+    g = torch.Generator().manual_seed(3)
+    q = torch.randn(len(lens), Hq, D, generator=g).to(TDT[dtype]).to(DEV)
+    sink = torch.tensor(np.linspace(-0.5, 3.0, Hq), dtype=torch.float32, device=DEV) if use_sink else None
+    sl = torch.tensor(lens, dtype=torch.int32, device=DEV)
+    got = fa.attention_decode_paged(q, kp, vp, bad, sl, window=W, softcap=C, sink=sink)
+    assert fa.forge_attn_check() == fa.FORGE_ERR_INVALID_ARG
+    o, lse = torch.zeros(len(lens), Hq, D, dtype=torch.float64), torch.zeros(len(lens), Hq, dtype=torch.float64)
+    for b, n in enumerate(lens):
+        at = torch.tensor([t for t in range(max(0, n - W) if W else 0, n) if t // ps not in gone.get(b, [])], dtype=torch.long)
+        where = table[b].cpu().long()[at // ps], slice(None), at % ps
+        k, v = (x.double().cpu()[where].repeat_interleave(Hq // Hkv, 1) for x in (kp, vp))
+        s = torch.einsum("thd,hd->ht", k, q[b].double().cpu()) / math.sqrt(D)
+        s = C * torch.tanh(s / C) if C else s
+        if use_sink:
+            s = torch.cat([s, sink.double().cpu()[:, None]], 1)
+        if s.shape[1] == 0:
+            lse[b] = -math.inf
+            continue
+        lse[b] = torch.logsumexp(s, 1)
+        o[b] = torch.einsum("ht,thd->hd", torch.exp(s - lse[b][:, None])[:, :len(at)], v)
+    check_decode(got, (o, lse), dtype)
+    assert not bool(got[0][3].any())
