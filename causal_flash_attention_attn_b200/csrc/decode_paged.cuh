@@ -410,18 +410,19 @@ struct PdWarpF32 {
 };
 
 // o and lse of one (sequence, head) from the unnormalised o, the max (log2 units)
-// and the sum; the sink (natural units) joins the sum here, once.
+// and the sum; the sink (natural units) joins the sum here, once. A sum of 0: nothing is
+// visible. A NaN among the visible scores makes the sum, and so both results, NaN.
 __device__ __forceinline__ float pd_total(float M, float l, const PdParams &p, int hq, float &scale_o, float &lse) {
     if (p.sink != nullptr) {
         const float sk = p.sink[hq] * kLog2e;
         const float M2 = fmaxf(M, sk);
         const float f = M == -INFINITY ? 0.0f : ex2_approx(M - M2);
         l = l * f + (sk == -INFINITY ? 0.0f : ex2_approx(sk - M2));
-        scale_o = l > 0.0f ? f / l : 0.0f;
-        lse = l > 0.0f ? (M2 + __log2f(l)) * kLn2 : -INFINITY;
+        scale_o = l != 0.0f ? f / l : 0.0f;
+        lse = l != 0.0f ? (M2 + __log2f(l)) * kLn2 : -INFINITY;
     } else {
-        scale_o = l > 0.0f ? 1.0f / l : 0.0f;
-        lse = l > 0.0f ? (M + __log2f(l)) * kLn2 : -INFINITY;
+        scale_o = l != 0.0f ? 1.0f / l : 0.0f;
+        lse = l != 0.0f ? (M + __log2f(l)) * kLn2 : -INFINITY;
     }
     return l;
 }
@@ -589,8 +590,9 @@ __global__ void __launch_bounds__(kPdThreads, PdCfg<T_, D>::PER_SM) decode_paged
                 float M = -INFINITY, l = 0.0f;
                 for (int w = 0; w < kPdWarps; w++) M = fmaxf(M, sM[w * kPdMaxG + r]);
                 for (int w = 0; w < kPdWarps; w++) {
-                    const float mw = sM[w * kPdMaxG + r];
-                    if (mw != -INFINITY) l += sL[w * kPdMaxG + r] * ex2_approx(mw - M);
+                    // (a maximum of -inf: the sum is 0, or NaN if all of the warp's scores were)
+                    const float mw = sM[w * kPdMaxG + r], lw = sL[w * kPdMaxG + r];
+                    l += mw == -INFINITY ? lw : lw * ex2_approx(mw - M);
                 }
                 sM[r] = M;  // rows of warp 0: read by this thread alone
                 sL[r] = l;

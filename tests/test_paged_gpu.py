@@ -398,3 +398,28 @@ def test_a_bad_page_holds_no_visible_key(dtype, Hq, Hkv, D, W, C, use_sink):
         o[b] = torch.einsum("ht,thd->hd", torch.exp(s - lse[b][:, None])[:, :len(at)], v)
     check_decode(got, (o, lse), dtype)
     assert not bool(got[0][3].any())
+
+
+@pytest.mark.parametrize("dtype,Hq,Hkv,D", [("bf16", 8, 2, 128), ("f32", 4, 2, 64)])
+@pytest.mark.parametrize("use_sink", [False, True])
+def test_a_nan_among_the_visible_keys_shows_in_o_and_lse(dtype, Hq, Hkv, D, use_sink):
+    # in one KV head: a NaN key (one of many, all of a warp's step, the only one) makes o and lse NaN, a NaN
+    # value o alone; the other head and the other sequences are as they were
+    lens, ps, G = [300, 300, 1, 40, 300, 5000], 16, Hq // Hkv
+    kp, vp, table = pool(dtype, lens, ps, Hkv, D, seed=11)
+    g = torch.Generator().manual_seed(5)
+    q = torch.randn(len(lens), Hq, D, generator=g).to(TDT[dtype]).to(DEV)
+    sink = torch.tensor(np.linspace(-0.5, 3.0, Hq), dtype=torch.float32, device=DEV) if use_sink else None
+    sl = torch.tensor(lens, dtype=torch.int32, device=DEV)
+    want = fa.attention_decode_paged(q, kp, vp, table, sl, sink=sink)
+    for b, rows in ((0, [37]), (1, range(32, 48)), (2, [0]), (5, [4321])):
+        for t in rows:
+            kp[int(table[b, t // ps]), 0, t % ps, 3] = float("nan")
+    vp[int(table[4, 2]), 0, 5] = float("nan")
+    o, lse = fa.attention_decode_paged(q, kp, vp, table, sl, sink=sink)
+    assert fa.forge_attn_check() == fa.FORGE_OK
+    hit = torch.tensor([0, 1, 2, 5], device=DEV)
+    assert bool(torch.isnan(lse[hit, :G]).all()) and bool(torch.isnan(o[hit, :G]).all())
+    assert bool(torch.isnan(o[4, :G]).all()) and torch.equal(lse[4], want[1][4])
+    assert torch.equal(o[3], want[0][3]) and torch.equal(lse[3], want[1][3])
+    assert torch.equal(o[:, G:], want[0][:, G:]) and torch.equal(lse[:, G:], want[1][:, G:])
