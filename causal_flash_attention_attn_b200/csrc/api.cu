@@ -1385,7 +1385,8 @@ forge_status forge_attn_paged_append(const void *k, const void *v, void *k_pages
     // few tokens: one a block, so that they spread over the SMs
     const int per_sm = rows / (4 * sm_count());
     p.tokens = per_sm < 1 ? 1 : per_sm > kAppendTokens ? kAppendTokens : per_sm;
-    return launch_pdl(paged_append, dim3((unsigned)((rows + p.tokens - 1) / p.tokens)), dim3(kAppendThreads), 0,
+    const unsigned blocks = (unsigned)((rows + p.tokens - 1) / p.tokens) + (cu_seqlens != nullptr ? 1 : 0);
+    return launch_pdl(paged_append, dim3(blocks), dim3(kAppendThreads), 0,
                       static_cast<cudaStream_t>(stream), p);
 }
 

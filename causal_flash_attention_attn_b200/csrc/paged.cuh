@@ -39,6 +39,15 @@ __global__ void __launch_bounds__(kAppendThreads, 6) paged_append(const __grid_c
     griddep_launch_dependents();
     griddep_wait();
     const int t0 = blockIdx.x * p.tokens, n = min(p.tokens, p.rows - t0);
+    if (n <= 0) {
+        // a block of its own (cu != nullptr) looks all lengths over: they have to ascend from 0 and
+        // not pass `rows`, or tokens would be left out or taken for another sequence's
+        for (int b = threadIdx.x; b <= p.num_seqs; b += kAppendThreads) {
+            const int at = p.cu[b], next = b < p.num_seqs ? p.cu[b + 1] : p.rows;
+            if (at > next || (b == 0 && at != 0)) record_status(kStatusInvalidArg);
+        }
+        return;
+    }
     const long long head = (long long)p.page * p.chunks * 16;  // bytes between a page's heads
     const int per = 2 * p.Hkv * p.chunks, side = max(1, kAppendThreads / per);
     const int t1 = (int)threadIdx.x / per;  // which of the tokens side by side

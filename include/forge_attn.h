@@ -314,7 +314,9 @@ forge_status forge_attn_varlen_bwd(const void *q, const void *k, const void *v, 
  *   elements between rows, a multiple of 16 bytes) at positions starts[b], starts[b] + 1, ...
  *   of their sequences. cu_seqlens [num_seqs + 1] as above (rows at or behind the last
  *   entry are skipped), or NULL: rows = num_seqs, one token each. A token whose place is bad
- *   is skipped and reported. Two sequences' tables must not share a page that is written.
+ *   is skipped and reported. Lengths that do not ascend from 0, or that pass `rows`, are
+ *   reported; which of the tokens are written then is not defined, none outside the pool. Two
+ *   sequences' tables must not share a page that is written.
  *
  * forge_attn_paged_copy: page src[i] onto page dst[i] for i = 0 .. n - 1, for K and V, in
  *   each of num_layers layers whose pools lie layer_stride elements apart. src and dst are

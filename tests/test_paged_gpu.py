@@ -423,3 +423,29 @@ def test_a_nan_among_the_visible_keys_shows_in_o_and_lse(dtype, Hq, Hkv, D, use_
     assert bool(torch.isnan(o[4, :G]).all()) and torch.equal(lse[4], want[1][4])
     assert torch.equal(o[3], want[0][3]) and torch.equal(lse[3], want[1][3])
     assert torch.equal(o[:, G:], want[0][:, G:]) and torch.equal(lse[:, G:], want[1][:, G:])
+
+
+@pytest.mark.parametrize("cu", [[0, 5, 3], [0, 5, 3, 8], [1, 4, 8], [0, 4, 9], [0, -1, 8], [0, 1 << 30, 8], [0] * 300 + [9]])
+def test_append_reports_lengths_that_do_not_ascend(cu):
+    n, rows, ps = len(cu) - 1, 8, 16
+    kp, vp = (torch.zeros(2 * n, 1, ps, 64, device=DEV) for _ in range(2))
+    k = torch.ones(rows, 1, 64, device=DEV)
+    table = torch.arange(2 * n, dtype=torch.int32, device=DEV).view(n, 2)
+    starts = torch.zeros(n, dtype=torch.int32, device=DEV)
+    fa.paged_append(k, k, kp, vp, table, starts, torch.tensor(cu, dtype=torch.int32, device=DEV))
+    assert fa.forge_attn_check() == fa.FORGE_ERR_INVALID_ARG and fa.forge_attn_check() == fa.FORGE_OK
+
+
+@pytest.mark.parametrize("cu", [[0, 8], [0, 0, 3, 3, 8], [0, 2], [0, 0]])
+def test_append_takes_empty_sequences_and_rows_behind_the_last(cu):
+    n, rows, ps = len(cu) - 1, 8, 16
+    kp, vp = (torch.zeros(n, 1, ps, 64, device=DEV) for _ in range(2))
+    k = torch.arange(1, rows + 1, device=DEV, dtype=torch.float32).view(rows, 1, 1).expand(rows, 1, 64).contiguous()
+    table = torch.arange(n, dtype=torch.int32, device=DEV).view(n, 1)
+    starts = torch.zeros(n, dtype=torch.int32, device=DEV)
+    fa.paged_append(k, -k, kp, vp, table, starts, torch.tensor(cu, dtype=torch.int32, device=DEV))
+    assert fa.forge_attn_check() == fa.FORGE_OK
+    want = torch.zeros_like(kp)
+    for b in range(n):
+        want[b, 0, :cu[b + 1] - cu[b]] = k[cu[b]:cu[b + 1], 0]
+    assert torch.equal(kp, want) and torch.equal(vp, -want)
