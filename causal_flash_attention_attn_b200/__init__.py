@@ -725,8 +725,6 @@ def _attention_varlen_function():
         class ForgeAttentionVarlen(torch.autograd.Function):
             @staticmethod
             def forward(ctx, q, k, v, cu_seqlens, sink, scale, window, softcap):
-                if not any(ctx.needs_input_grad):
-                    return attention_varlen_fwd(q, k, v, cu_seqlens, scale, window, softcap, sink=sink)[0]
                 o, lse, o_res = attention_varlen_fwd(q, k, v, cu_seqlens, scale, window, softcap, sink=sink,
                                                      return_residual=True)
                 ctx.save_for_backward(q, k, v, o, o_res, lse, cu_seqlens, sink)
@@ -756,6 +754,11 @@ def attention_varlen(q, k, v, cu_seqlens, scale=None, window=0, softcap=0.0, sin
     library's backward (once: there are no second derivatives). The lengths must not change between the
     forward and its backward. Capture a forward together with its backward, on one stream, while no
     graph of an earlier call on the same leaves is alive."""
+    import torch
+    # (a Function's forward cannot tell: inside it grad mode is off, and needs_input_grad says only
+    # which inputs require one)
+    if not (torch.is_grad_enabled() and any(x is not None and x.requires_grad for x in (q, k, v, sink))):
+        return attention_varlen_fwd(q, k, v, cu_seqlens, scale, window, softcap, sink=sink)[0]
     scale = 1.0 / math.sqrt(q.shape[-1]) if scale is None else float(scale)
     return _attention_varlen_function().apply(q, k, v, cu_seqlens, sink, scale, int(window), float(softcap))
 

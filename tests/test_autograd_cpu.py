@@ -75,3 +75,25 @@ def test_no_grad_inputs_run_the_forward_only():
     q, k, v = (x.detach() for x in (leaf((1, 2, 5, 4), 10), leaf((1, 2, 5, 4), 11), leaf((1, 2, 5, 4), 12)))
     o = fa.attention(q, k, v)
     assert not o.requires_grad and [c[0] for c in calls] == ["fwd"]
+
+
+class Forward(Exception):
+    pass
+
+
+@pytest.mark.parametrize("leaves", ["q", "sink", "none"])
+@pytest.mark.parametrize("mode", ["grad", "no_grad", "inference"])
+def test_packed_call_runs_the_training_forward_only_for_a_gradient(monkeypatch, leaves, mode):
+    asked = []
+
+    def fake(q, k, v, cu_seqlens, scale=None, window=0, softcap=0.0, stream=None, *, sink=None, return_residual=False):
+        asked.append((scale, window, softcap, sink is not None, return_residual))
+        raise Forward
+    monkeypatch.setattr(fa, "attention_varlen_fwd", fake)
+    x, sink = torch.zeros(5, 2, 64), torch.zeros(2)
+    q = x.clone().requires_grad_(leaves == "q")
+    sink.requires_grad_(leaves == "sink")
+    scope = {"grad": torch.enable_grad, "no_grad": torch.no_grad, "inference": torch.inference_mode}[mode]
+    with scope(), pytest.raises(Forward):
+        fa.attention_varlen(q, x, x, torch.tensor([0, 5]), 0.3, 7, 2.0, sink)
+    assert asked == [(0.3, 7, 2.0, True, mode == "grad" and leaves != "none")]

@@ -523,3 +523,16 @@ def raw_unchecked(q, k, v, dO, sk, cu, W, C):
     torch.cuda.synchronize()
     assert fa.forge_attn_check() == fa.FORGE_OK
     return (o, lse, *g[:3], None)
+
+
+@pytest.mark.parametrize("D,Hq,Hkv", [(64, 3, 3), (128, 4, 2), (256, 2, 1)])
+def test_without_grad_mode_the_call_is_the_plain_forward(D, Hq, Hkv):
+    q, k, v, _, sk, cu = make("bf16", [130, 300, 7], 0, Hq, Hkv, D, 0.0, True, False)
+    x = [t.clone().requires_grad_() for t in (q, k, v, sk)]
+    want = fa.attention_varlen_fwd(q, k, v, cu, window=90, sink=sk)[0]
+    for scope in (torch.no_grad, torch.inference_mode):
+        with scope():
+            o = fa.attention_varlen(*x[:3], cu, window=90, sink=x[3])
+        assert not o.requires_grad and torch.equal(o, want)
+    o = fa.attention_varlen(q, k, v, cu, window=90, sink=sk)
+    assert not o.requires_grad and torch.equal(o, want)
