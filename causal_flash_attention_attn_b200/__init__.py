@@ -25,7 +25,8 @@ import os
 
 __all__ = [
     "FORGE_OK", "FORGE_ERR_INVALID_ARG", "FORGE_ERR_UNSUPPORTED", "FORGE_ERR_WORKSPACE",
-    "FORGE_ERR_CUDA", "FORGE_ERR_TIMEOUT", "FORGE_DTYPE_F32", "FORGE_DTYPE_BF16", "ForgeError",
+    "FORGE_ERR_CUDA", "FORGE_ERR_TIMEOUT", "FORGE_DTYPE_F32", "FORGE_DTYPE_BF16", "FORGE_VARLEN_CLEAR_TAIL",
+    "FORGE_VARLEN_SINK_FIXED", "ForgeError",
     "library", "library_path", "forge_attn_fwd", "forge_attn_bwd", "forge_attn_bwd_workspace_size",
     "forge_attn_bwd_noalloc", "forge_attn_fwd_ext", "forge_attn_bwd_ext", "forge_attn_decode",
     "forge_attn_decode_workspace_size", "attention_decode", "forge_attn_fwd_dkv", "forge_attn_bwd_dkv",
@@ -48,6 +49,8 @@ FORGE_ERR_CUDA = 4
 FORGE_ERR_TIMEOUT = 5
 FORGE_DTYPE_F32 = 0
 FORGE_DTYPE_BF16 = 1
+FORGE_VARLEN_CLEAR_TAIL = 1
+FORGE_VARLEN_SINK_FIXED = 0x100
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 library_path = os.path.join(_HERE, "libforge_attn.so")
@@ -257,11 +260,11 @@ def forge_attn_varlen_fwd_workspace_size(num_seqs, rows, Hq, Hkv, D, dtype) -> i
 
 
 def forge_attn_varlen_fwd(q, k, v, o, o_res, lse, cu_seqlens, num_seqs, rows, Hq, Hkv, D, q_stride, k_stride, v_stride,
-                          scale, window, softcap, sink, clear_tail, dtype, workspace, workspace_bytes,
+                          scale, window, softcap, sink, flags, dtype, workspace, workspace_bytes,
                           stream=None) -> int:
     return library().forge_attn_varlen_fwd(_ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(o_res), _ptr(lse),
                                            _ptr(cu_seqlens), num_seqs, rows, Hq, Hkv, D, int(q_stride), int(k_stride), int(v_stride), float(scale),
-                                           int(window), float(softcap), _ptr(sink), int(clear_tail), int(dtype),
+                                           int(window), float(softcap), _ptr(sink), int(flags), int(dtype),
                                            _ptr(workspace), int(workspace_bytes), _stream(stream))
 
 
@@ -270,12 +273,12 @@ def forge_attn_varlen_bwd_workspace_size(num_seqs, rows, Hq, Hkv, D, dtype) -> i
 
 
 def forge_attn_varlen_bwd(q, k, v, o, o_res, lse, dO, dq, dk, dv, cu_seqlens, num_seqs, rows, Hq, Hkv, D, q_stride, k_stride,
-                          v_stride, scale, window, softcap, sink, dsink, clear_tail, dtype, workspace, workspace_bytes,
+                          v_stride, scale, window, softcap, sink, dsink, flags, dtype, workspace, workspace_bytes,
                           stream=None) -> int:
     return library().forge_attn_varlen_bwd(_ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(o_res), _ptr(lse), _ptr(dO), _ptr(dq), _ptr(dk),
                                            _ptr(dv), _ptr(cu_seqlens), num_seqs, rows, Hq, Hkv, D, int(q_stride),
                                            int(k_stride), int(v_stride), float(scale), int(window), float(softcap),
-                                           _ptr(sink), _ptr(dsink), int(clear_tail), int(dtype), _ptr(workspace),
+                                           _ptr(sink), _ptr(dsink), int(flags), int(dtype), _ptr(workspace),
                                            int(workspace_bytes), _stream(stream))
 
 
@@ -647,11 +650,12 @@ def _check_packed(what, q, k, v, cu_seqlens, sink):
 
 
 def attention_varlen_fwd(q, k, v, cu_seqlens, scale=None, window=0, softcap=0.0, stream=None, *, sink=None,
-                         return_residual=False):
+                         return_residual=False, sink_fixed=False):
     """Causal attention over packed sequences: q [rows,Hq,D], k, v [rows,Hkv,D] (bf16 or f32; their rows
     may lie apart), cu_seqlens int32 [num_seqs + 1] on the device, from 0. Returns (o [rows,Hq,D], lse
     [Hq,rows]), or (o, lse, o_res) with return_residual: o's rounding residual for the backward (None in
-    f32). Rows behind the last sequence get zeros, lse -inf there. Nothing synchronises; bad cu_seqlens
+    f32), and with a sink P in two terms for dsink, unless sink_fixed says that no gradient of the sink
+    will be asked for. Rows behind the last sequence get zeros, lse -inf there. Nothing synchronises; bad cu_seqlens
     are reported by forge_attn_check."""
     import torch
     what = "attention_varlen_fwd"
@@ -666,9 +670,10 @@ def attention_varlen_fwd(q, k, v, cu_seqlens, scale=None, window=0, softcap=0.0,
         L = library()
         nbytes = _bytes("forge_attn_varlen_fwd_workspace_size", q.get_device(), n, rows, Hq, Hkv, D, dt)
         ws = q.new_empty(nbytes, dtype=torch.uint8)
+        flags = FORGE_VARLEN_CLEAR_TAIL | (FORGE_VARLEN_SINK_FIXED if sink_fixed else 0)
         s = L.forge_attn_varlen_fwd(q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), _at(o_res), lse.data_ptr(),
                                     cu_seqlens.data_ptr(), n, rows, Hq, Hkv, D, qs, ks, vs, scale, window, softcap,
-                                    _at(sink), 1, dt, ws.data_ptr(), nbytes, _here(q.device))
+                                    _at(sink), flags, dt, ws.data_ptr(), nbytes, _here(q.device))
     if s != FORGE_OK:
         raise ForgeError(s, "forge_attn_varlen_fwd")
     return (o, lse, o_res) if return_residual else (o, lse)
@@ -677,7 +682,7 @@ def attention_varlen_fwd(q, k, v, cu_seqlens, scale=None, window=0, softcap=0.0,
 def attention_varlen_bwd(q, k, v, o, lse, dO, cu_seqlens, scale=None, window=0, softcap=0.0, stream=None, *,
                          sink=None, o_res=None):
     """Backward of attention_varlen_fwd (its o and lse, and o_res if it returned one; dO contiguous).
-    Returns (dq, dk, dv), or (dq, dk, dv, dsink [Hq]) with a sink; zeros in the rows behind the last
+    Returns (dq, dk, dv), or (dq, dk, dv, dsink [Hq]) with a sink (which is needed for dsink only); zeros in the rows behind the last
     sequence."""
     import torch
     what = "attention_varlen_bwd"
@@ -725,9 +730,11 @@ def _attention_varlen_function():
         class ForgeAttentionVarlen(torch.autograd.Function):
             @staticmethod
             def forward(ctx, q, k, v, cu_seqlens, sink, scale, window, softcap):
+                # a sink that requires no gradient: no second term of P, no dsink
+                trained = sink if ctx.needs_input_grad[4] else None
                 o, lse, o_res = attention_varlen_fwd(q, k, v, cu_seqlens, scale, window, softcap, sink=sink,
-                                                     return_residual=True)
-                ctx.save_for_backward(q, k, v, o, o_res, lse, cu_seqlens, sink)
+                                                     return_residual=True, sink_fixed=trained is None)
+                ctx.save_for_backward(q, k, v, o, o_res, lse, cu_seqlens, trained)
                 rows, Hq, D = q.shape
                 ctx.args = (scale, window, softcap, rows, Hq, k.shape[1], D,
                             *((x.stride(0) if rows > 1 else x.shape[1] * D) for x in (q, k, v)))
@@ -750,8 +757,8 @@ def _attention_varlen_function():
 
 
 def attention_varlen(q, k, v, cu_seqlens, scale=None, window=0, softcap=0.0, sink=None):
-    """attention_varlen_fwd with autograd: o, and gradients for q, k, v (and sink) through the
-    library's backward (once: there are no second derivatives). The lengths must not change between the
+    """attention_varlen_fwd with autograd: o, and gradients for q, k, v (and sink, if it requires one)
+    through the library's backward (once: there are no second derivatives). The lengths must not change between the
     forward and its backward. Capture a forward together with its backward, on one stream, while no
     graph of an earlier call on the same leaves is alive."""
     import torch

@@ -516,6 +516,9 @@ VarSched var_sched(const VarArgs &a, const VarLayout &l, void *ws, bool backward
     return v;
 }
 
+bool sink_is_fixed(int flags) { return flags > 0 && (flags & FORGE_VARLEN_SINK_FIXED) != 0; }
+bool clears_tail(int flags) { return (sink_is_fixed(flags) ? flags & ~FORGE_VARLEN_SINK_FIXED : flags) != 0; }
+
 // Launches varlen_plan; tail: up to three tensors of `heads` x D elements a row
 // whose rows behind the last sequence are cleared.
 forge_status run_plan(const VarArgs &a, const VarSched &v, bool backward, void *const (&tail)[3],
@@ -548,7 +551,7 @@ forge_status run_plan(const VarArgs &a, const VarSched &v, bool backward, void *
     return launch_pdl(varlen_plan, dim3(clear ? 33 : 1), dim3(kPlanThreads), 0, a.st, p);
 }
 
-FwdParams var_fwd_params(const VarArgs &a, const VarSched &v, void *o, void *o_res, float *lse) {
+FwdParams var_fwd_params(const VarArgs &a, const VarSched &v, void *o, void *o_res, float *lse, bool sink_fixed) {
     FwdParams p = {};
     p.o = static_cast<__nv_bfloat16 *>(o);
     p.lse = lse;
@@ -560,11 +563,13 @@ FwdParams var_fwd_params(const VarArgs &a, const VarSched &v, void *o, void *o_r
     p.sink = a.sink;
     p.var = v;
     p.o_res = static_cast<__nv_bfloat16 *>(o_res);
+    // a forward whose backward will want dsink
+    p.for_dsink = a.sink != nullptr && o_res != nullptr && !sink_fixed;
     return p;
 }
 
 template <int D>
-forge_status var_fwd_tc(const VarArgs &a, const VarSched &v, void *o, void *o_res, float *lse) {
+forge_status var_fwd_tc(const VarArgs &a, const VarSched &v, void *o, void *o_res, float *lse, bool sink_fixed) {
     CUtensorMap mq, mk, mv, mo;
     if (!make_map_rows(&mq, a.q, D, a.rows, a.Hq, a.q_stride, 128) ||
         !make_map_rows(&mk, a.k, D, a.rows, a.Hkv, a.k_stride, 128) ||
@@ -573,7 +578,7 @@ forge_status var_fwd_tc(const VarArgs &a, const VarSched &v, void *o, void *o_re
         t_last_cuda_error = "cuTensorMapEncodeTiled failed";
         return FORGE_ERR_CUDA;
     }
-    const FwdParams p = var_fwd_params(a, v, o, o_res, lse);
+    const FwdParams p = var_fwd_params(a, v, o, o_res, lse, sink_fixed);
     const long long items = (long long)v.max_items * a.Hq;
     if constexpr (D == 256) {
         using C = FwdTc<D>;
@@ -582,9 +587,8 @@ forge_status var_fwd_tc(const VarArgs &a, const VarSched &v, void *o, void *o_re
                           p);
     } else {
         using C = VarFwdTc<D>;
-        // a forward whose backward will want dsink: P in two terms
-        const bool split = a.sink != nullptr && o_res != nullptr, cap = a.softcap > 0.0f, win = a.window > 0;
-        auto *kernel = split ? (cap ? varlen_fwd_tc<D, true, true, true> : varlen_fwd_tc<D, true, false, true>)
+        const bool cap = a.softcap > 0.0f, win = a.window > 0;
+        auto *kernel = p.for_dsink ? (cap ? varlen_fwd_tc<D, true, true, true> : varlen_fwd_tc<D, true, false, true>)
                        : cap ? (win ? varlen_fwd_tc<D, false, true, true> : varlen_fwd_tc<D, false, true, false>)
                              : (win ? varlen_fwd_tc<D, false, false, true> : varlen_fwd_tc<D, false, false, false>);
         if (set_smem(kernel, C::SMEM) != FORGE_OK) return FORGE_ERR_CUDA;
@@ -1246,7 +1250,7 @@ size_t forge_attn_varlen_bwd_workspace_size(int num_seqs, int rows, int Hq, int 
 forge_status forge_attn_varlen_fwd(const void *q, const void *k, const void *v, void *o, void *o_res, float *lse,
                                    const int *cu_seqlens, int num_seqs, int rows, int Hq, int Hkv, int D,
                                    size_t q_stride, size_t k_stride, size_t v_stride, float scale, int window,
-                                   float softcap, const float *sink, int clear_tail, forge_dtype dtype,
+                                   float softcap, const float *sink, int flags, forge_dtype dtype,
                                    void *workspace, size_t workspace_bytes, void *stream) {
     VarArgs a = {q, k, v, cu_seqlens, num_seqs, rows, Hq, Hkv, D, q_stride, k_stride, v_stride, scale, window, softcap,
                  sink, dtype, static_cast<cudaStream_t>(stream)};
@@ -1260,9 +1264,9 @@ forge_status forge_attn_varlen_fwd(const void *q, const void *k, const void *v, 
     const VarSched sched = var_sched(a, var_layout(num_seqs, rows, Hq, Hkv, D, dtype, false), workspace, false);
     void *const tail[3] = {o, nullptr, nullptr};
     const int heads[3] = {Hq, 0, 0};
-    if ((s = run_plan(a, sched, false, tail, heads, lse, clear_tail != 0)) != FORGE_OK) return s;
+    if ((s = run_plan(a, sched, false, tail, heads, lse, clears_tail(flags))) != FORGE_OK) return s;
     if (dtype == FORGE_DTYPE_BF16) {
-        FORGE_DISPATCH_D(D, return var_fwd_tc<kD>(a, sched, o, o_res, lse);)
+        FORGE_DISPATCH_D(D, return var_fwd_tc<kD>(a, sched, o, o_res, lse, sink_is_fixed(flags));)
     } else {
         FORGE_DISPATCH_D(D, return var_fwd_f32<kD>(a, sched, o, lse);)
     }
@@ -1273,7 +1277,7 @@ forge_status forge_attn_varlen_bwd(const void *q, const void *k, const void *v, 
                                    const float *lse, const void *dO, void *dq, void *dk, void *dv, const int *cu_seqlens, int num_seqs,
                                    int rows, int Hq, int Hkv, int D, size_t q_stride, size_t k_stride, size_t v_stride,
                                    float scale, int window, float softcap, const float *sink, float *dsink,
-                                   int clear_tail, forge_dtype dtype, void *workspace, size_t workspace_bytes,
+                                   int flags, forge_dtype dtype, void *workspace, size_t workspace_bytes,
                                    void *stream) {
     VarArgs a = {q, k, v, cu_seqlens, num_seqs, rows, Hq, Hkv, D, q_stride, k_stride, v_stride, scale, window, softcap,
                  sink, dtype, static_cast<cudaStream_t>(stream)};
@@ -1294,7 +1298,7 @@ forge_status forge_attn_varlen_bwd(const void *q, const void *k, const void *v, 
     float *acc = dtype == FORGE_DTYPE_BF16 ? reinterpret_cast<float *>(static_cast<char *>(workspace) + l.acc) : nullptr;
     void *const tail[3] = {dq, dk, dv};
     const int heads[3] = {Hq, Hkv, Hkv};
-    if ((s = run_plan(a, sched, true, tail, heads, nullptr, clear_tail != 0)) != FORGE_OK) return s;
+    if ((s = run_plan(a, sched, true, tail, heads, nullptr, clears_tail(flags))) != FORGE_OK) return s;
     if (dtype == FORGE_DTYPE_BF16) {
         FORGE_DISPATCH_D(D, return var_bwd<__nv_bfloat16, kD>(a, sched, o, o_res, lse, dO, dq, dk, dv, dsink, delta, acc);)
     } else {

@@ -195,6 +195,7 @@ struct FwdParams {
     // row's softmax is peaked (simulated on 16 capped keys at sigma 2: dq and dk off by
     // 0.0042 instead of 0.0024, of which 0.0023 are the roundings of dS and of dq, dk).
     __nv_bfloat16 *o_res;
+    bool for_dsink;  // VAR: the backward will form dsink from this o and o_res
 };
 
 // 32 f32 values of o times f, as bf16 pairs (hi), and the residuals' pairs (lo)
@@ -487,7 +488,7 @@ __global__ void __launch_bounds__(320, 1)
             uint32_t pk[32];
             float rs;
             // no FMA-pipe exponentials (3e-6) where dsink will be formed from O
-            const bool mufu = need_mask || (VAR && p.sink != nullptr && p.o_res != nullptr);
+            const bool mufu = need_mask || (VAR && p.for_dsink);
             if (cap) {
                 rs = mufu ? fwd_exp_half<true, false, C::PSPLIT>(s, pk, p.scale_log2, msub)
                                : fwd_exp_half<true, true, C::PSPLIT>(s, pk, p.scale_log2, msub);

@@ -253,7 +253,7 @@ forge_status forge_attn_decode(const void *q, const void *k_cache, const void *v
  *    of 16 bytes), so that q, k and v may be parts of one projection's output. o, dO,
  *    dq, dk, dv and lse are dense.
  *  - Rows at or behind cu_seqlens[num_seqs] are not read. Outputs there are left as they
- *    were (clear_tail = 0), or set to zero, lse to -inf (clear_tail != 0).
+ *    were (flags = 0), or set to zero, lse to -inf (FORGE_VARLEN_CLEAR_TAIL).
  *  - The lengths are read on the device: nothing synchronises, and a captured call
  *    follows the lengths that cu_seqlens holds at each replay. Lengths that do not ascend from
  *    0, or that pass `rows`, are reported as FORGE_ERR_INVALID_ARG by the next
@@ -263,7 +263,9 @@ forge_status forge_attn_decode(const void *q, const void *k_cache, const void *v
  *    (NULL in the backward) Delta carries o's rounding, which shows in dq, dk and dsink where
  *    rows attend to few keys. With a sink, a forward that writes o_res also keeps P in two
  *    bf16 terms (o accurate to ~2^-17 before its rounding), which dsink, a sum of Delta over all
- *    rows, needs: give o_res wherever dsink matters. f32: neither written nor read.
+ *    rows, needs: give o_res wherever dsink matters. That costs the forward 43 %, so a sink that
+ *    is not trained is best said to be fixed (FORGE_VARLEN_SINK_FIXED added to the forward's
+ *    flags: P in one term, o and lse as without o_res). f32: neither written nor read.
  *  - sink, dsink: as in forge_attn_fwd_ext / forge_attn_bwd_ext. scale, window, softcap
  *    as in forge_attn_fwd (a window >= rows acts as off).
  *  - rows and num_seqs >= 1, num_seqs <= 2^20, (rows / 64 + num_seqs + 1188) * Hq < 2^31; the
@@ -274,18 +276,22 @@ forge_status forge_attn_decode(const void *q, const void *k_cache, const void *v
  * between calls; o, lse, dk, dv and everything in f32 are the same on every call. The backward
  * takes o and lse as forge_attn_varlen_fwd wrote them.
  */
+enum {
+    FORGE_VARLEN_CLEAR_TAIL = 1,     /* (any flags but the ones below count as this one) */
+    FORGE_VARLEN_SINK_FIXED = 0x100
+};
 size_t forge_attn_varlen_fwd_workspace_size(int num_seqs, int rows, int Hq, int Hkv, int D, forge_dtype dtype);
 forge_status forge_attn_varlen_fwd(const void *q, const void *k, const void *v, void *o, void *o_res, float *lse,
                                    const int *cu_seqlens, int num_seqs, int rows, int Hq, int Hkv, int D,
                                    size_t q_stride, size_t k_stride, size_t v_stride, float scale, int window,
-                                   float softcap, const float *sink, int clear_tail, forge_dtype dtype,
+                                   float softcap, const float *sink, int flags, forge_dtype dtype,
                                    void *workspace, size_t workspace_bytes, void *stream);
 size_t forge_attn_varlen_bwd_workspace_size(int num_seqs, int rows, int Hq, int Hkv, int D, forge_dtype dtype);
 forge_status forge_attn_varlen_bwd(const void *q, const void *k, const void *v, const void *o, const void *o_res,
                                    const float *lse, const void *dO, void *dq, void *dk, void *dv, const int *cu_seqlens, int num_seqs,
                                    int rows, int Hq, int Hkv, int D, size_t q_stride, size_t k_stride, size_t v_stride,
                                    float scale, int window, float softcap, const float *sink, float *dsink,
-                                   int clear_tail, forge_dtype dtype, void *workspace, size_t workspace_bytes,
+                                   int flags, forge_dtype dtype, void *workspace, size_t workspace_bytes,
                                    void *stream);
 
 /*

@@ -84,10 +84,12 @@ class Forward(Exception):
 @pytest.mark.parametrize("leaves", ["q", "sink", "none"])
 @pytest.mark.parametrize("mode", ["grad", "no_grad", "inference"])
 def test_packed_call_runs_the_training_forward_only_for_a_gradient(monkeypatch, leaves, mode):
-    asked = []
+    asked, fixed = [], []
 
-    def fake(q, k, v, cu_seqlens, scale=None, window=0, softcap=0.0, stream=None, *, sink=None, return_residual=False):
+    def fake(q, k, v, cu_seqlens, scale=None, window=0, softcap=0.0, stream=None, *, sink=None, return_residual=False,
+             sink_fixed=False):
         asked.append((scale, window, softcap, sink is not None, return_residual))
+        fixed.append(sink_fixed)
         raise Forward
     monkeypatch.setattr(fa, "attention_varlen_fwd", fake)
     x, sink = torch.zeros(5, 2, 64), torch.zeros(2)
@@ -97,3 +99,4 @@ def test_packed_call_runs_the_training_forward_only_for_a_gradient(monkeypatch, 
     with scope(), pytest.raises(Forward):
         fa.attention_varlen(q, x, x, torch.tensor([0, 5]), 0.3, 7, 2.0, sink)
     assert asked == [(0.3, 7, 2.0, True, mode == "grad" and leaves != "none")]
+    assert fixed == [mode == "grad" and leaves == "q"]  # a sink that is not trained is said to be fixed

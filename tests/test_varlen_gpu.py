@@ -536,3 +536,27 @@ def test_without_grad_mode_the_call_is_the_plain_forward(D, Hq, Hkv):
         assert not o.requires_grad and torch.equal(o, want)
     o = fa.attention_varlen(q, k, v, cu, window=90, sink=sk)
     assert not o.requires_grad and torch.equal(o, want)
+
+
+@pytest.mark.parametrize("W,C", [(0, 0.0), (90, 50.0)])
+@pytest.mark.parametrize("D,Hq,Hkv", [(64, 3, 3), (128, 4, 2), (256, 2, 1)])
+def test_a_sink_that_is_not_trained(D, Hq, Hkv, W, C):
+    # the forward is the plain one (P in one term: its bits), the other gradients are those of the same
+    # o, lse and residual, and no dsink is formed
+    q, k, v, dO, sk, cu = make("bf16", [130, 300, 7], 5, Hq, Hkv, D, C, True, False)
+    x = [t.clone().requires_grad_() for t in (q, k, v)]
+    o = fa.attention_varlen(*x, cu, window=W, softcap=C, sink=sk)
+    got = torch.autograd.grad(o, x, dO)
+    assert torch.equal(o, fa.attention_varlen_fwd(q, k, v, cu, window=W, softcap=C, sink=sk)[0])
+    o, lse, o_res = fa.attention_varlen_fwd(q, k, v, cu, window=W, softcap=C, sink=sk, return_residual=True,
+                                            sink_fixed=True)
+    want = fa.attention_varlen_bwd(q, k, v, o, lse, dO, cu, window=W, softcap=C, o_res=o_res)
+    assert torch.equal(got[1], want[1]) and torch.equal(got[2], want[2])
+    check_close("dq", got[0], want[0].double().cpu().numpy(), "bf16")
+    assert not bool(o[-5:].any())  # the rows behind the last sequence are cleared as ever
+    # a trained sink alone: the split forward, and its gradient
+    s = sk.clone().requires_grad_()
+    (ds,) = torch.autograd.grad(fa.attention_varlen(q, k, v, cu, window=W, softcap=C, sink=s), s, dO)
+    o, lse, o_res = fa.attention_varlen_fwd(q, k, v, cu, window=W, softcap=C, sink=sk, return_residual=True)
+    assert torch.equal(ds, fa.attention_varlen_bwd(q, k, v, o, lse, dO, cu, window=W, softcap=C, sink=sk, o_res=o_res)[3])
+    assert fa.forge_attn_check() == fa.FORGE_OK
