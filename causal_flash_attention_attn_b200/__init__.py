@@ -729,11 +729,12 @@ def _attention_varlen_function():
 
         class ForgeAttentionVarlen(torch.autograd.Function):
             @staticmethod
-            def forward(ctx, q, k, v, cu_seqlens, sink, scale, window, softcap):
+            def forward(ctx, q, k, v, cu_seqlens, sink, scale, window, softcap, residual):
                 # a sink that requires no gradient: no second term of P, no dsink
                 trained = sink if ctx.needs_input_grad[4] else None
-                o, lse, o_res = attention_varlen_fwd(q, k, v, cu_seqlens, scale, window, softcap, sink=sink,
-                                                     return_residual=True, sink_fixed=trained is None)
+                o, lse, *rest = attention_varlen_fwd(q, k, v, cu_seqlens, scale, window, softcap, sink=sink,
+                                                     return_residual=residual, sink_fixed=trained is None)
+                o_res = rest[0] if residual else None
                 ctx.save_for_backward(q, k, v, o, o_res, lse, cu_seqlens, trained)
                 rows, Hq, D = q.shape
                 ctx.args = (scale, window, softcap, rows, Hq, k.shape[1], D,
@@ -750,24 +751,28 @@ def _attention_varlen_function():
                 if dO.data_ptr() % 16:  # a part of another tensor's gradient may start anywhere
                     dO = dO.clone()
                 dq, dk, dv, dsink = _varlen_bwd(q, k, v, o, o_res, lse, dO, cu_seqlens, sink, *ctx.args)
-                return dq, dk, dv, None, dsink, None, None, None
+                return dq, dk, dv, None, dsink, None, None, None, None
 
         _attention_varlen_fn = ForgeAttentionVarlen
     return _attention_varlen_fn
 
 
-def attention_varlen(q, k, v, cu_seqlens, scale=None, window=0, softcap=0.0, sink=None):
+def attention_varlen(q, k, v, cu_seqlens, scale=None, window=0, softcap=0.0, sink=None, residual=True):
     """attention_varlen_fwd with autograd: o, and gradients for q, k, v (and sink, if it requires one)
-    through the library's backward (once: there are no second derivatives). The lengths must not change between the
-    forward and its backward. Capture a forward together with its backward, on one stream, while no
-    graph of an earlier call on the same leaves is alive."""
+    through the library's backward (once: there are no second derivatives). In bf16 a second tensor
+    of o's size, its rounding residual, is kept for the backward; residual=False does without (less
+    memory and traffic, as `attention`), and then dq, dk and dsink carry o's rounding, which shows
+    where rows attend to few keys. The lengths must not change between the forward and its backward.
+    Capture a forward together with its backward, on one stream, while no graph of an earlier call on
+    the same leaves is alive."""
     import torch
     # (a Function's forward cannot tell: inside it grad mode is off, and needs_input_grad says only
     # which inputs require one)
     if not (torch.is_grad_enabled() and any(x is not None and x.requires_grad for x in (q, k, v, sink))):
         return attention_varlen_fwd(q, k, v, cu_seqlens, scale, window, softcap, sink=sink)[0]
     scale = 1.0 / math.sqrt(q.shape[-1]) if scale is None else float(scale)
-    return _attention_varlen_function().apply(q, k, v, cu_seqlens, sink, scale, int(window), float(softcap))
+    return _attention_varlen_function().apply(q, k, v, cu_seqlens, sink, scale, int(window), float(softcap),
+                                              bool(residual))
 
 
 # ---------------------------------------------------------------- paged cache

@@ -560,3 +560,27 @@ def test_a_sink_that_is_not_trained(D, Hq, Hkv, W, C):
     o, lse, o_res = fa.attention_varlen_fwd(q, k, v, cu, window=W, softcap=C, sink=sk, return_residual=True)
     assert torch.equal(ds, fa.attention_varlen_bwd(q, k, v, o, lse, dO, cu, window=W, softcap=C, sink=sk, o_res=o_res)[3])
     assert fa.forge_attn_check() == fa.FORGE_OK
+
+
+@pytest.mark.parametrize("with_sink", [False, True])
+def test_training_without_the_residual(with_sink):
+    # the backward gets no o_res (the plain call's gradients), and the graph keeps one tensor of o's size less
+    q, k, v, dO, sk, cu = make("bf16", [700, 300], 0, 8, 2, 128, 0.0, with_sink, False)
+    x = [t.clone().requires_grad_() for t in (q, k, v, sk) if t is not None]
+    held = []
+    for residual in (True, False):
+        torch.cuda.synchronize()
+        before = torch.cuda.memory_allocated()
+        o = fa.attention_varlen(*x[:3], cu, sink=x[3] if with_sink else None, residual=residual)
+        held.append(torch.cuda.memory_allocated() - before)
+        if residual:
+            del o
+    assert held[0] - held[1] == o.numel() * 2
+    got = torch.autograd.grad(o, x, dO)
+    po, lse = fa.attention_varlen_fwd(q, k, v, cu, sink=sk)
+    want = fa.attention_varlen_bwd(q, k, v, po, lse, dO, cu, sink=sk)
+    assert torch.equal(o, po) and torch.equal(got[1], want[1]) and torch.equal(got[2], want[2])
+    check_close("dq", got[0], want[0].double().cpu().numpy(), "bf16")
+    if with_sink:
+        assert torch.equal(got[3], want[3])
+    assert fa.forge_attn_check() == fa.FORGE_OK
