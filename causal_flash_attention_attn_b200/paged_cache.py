@@ -94,7 +94,8 @@ class PagedCache:
     def extend(self, seqs, counts, stream=None):
         """Make room for counts[i] more tokens of seqs[i] (each sequence once). A partly filled last page
         that is shared is copied first, in every layer. Returns the old lengths: the positions to append
-        at. All or nothing: MemoryError if the free pages do not suffice."""
+        at. All or nothing: MemoryError if the free pages do not suffice, and if a copy fails the books stay
+        as they were."""
         seqs, counts = list(seqs), list(counts)
         if len(seqs) != len(counts) or len(set(seqs)) != len(seqs):
             raise ValueError("PagedCache.extend: one count for each sequence, each sequence once")
@@ -113,19 +114,19 @@ class PagedCache:
                     shared.append(s)
         if need + len(shared) > len(self._free):
             raise MemoryError(f"PagedCache: {need + len(shared)} pages needed, {len(self._free)} free")
-        moves = []
+        # the copies come first: they touch free pages only, and may fail
+        copies = heapq.nsmallest(len(shared), self._free)
+        self._copy([(self._pages[s][-1], page) for s, page in zip(shared, copies)], stream)
         for s in shared:
-            old, page = self._pages[s][-1], self._take()
-            self._pages[s][-1] = page
+            old = self._pages[s][-1]
+            self._pages[s][-1] = self._take()
             self._drop(old)
-            moves.append((old, page))
         starts = []
         for s, n in zip(seqs, counts):
             starts.append(self._lens[s])
             self._lens[s] += n
             while len(self._pages[s]) * ps < self._lens[s]:
                 self._pages[s].append(self._take())
-        self._copy(moves, stream)
         return starts
 
     def compact(self, stream=None):
@@ -135,12 +136,12 @@ class PagedCache:
         holes = [p for p in range(len(held)) if not self._refs[p]]
         moves = list(zip(reversed(held[len(held) - len(holes):]), holes)) if holes else []
         to = dict(moves)
+        self._copy(moves, stream)  # into free pages: if it fails, the books stay as they were
         for old, new in moves:
             self._refs[new], self._refs[old] = self._refs[old], 0
         for s, pages in self._pages.items():
             self._pages[s] = [to.get(p, p) for p in pages]
         self._free = list(range(len(held), self.num_pages))
-        self._copy(moves, stream)
         return moves
 
     def _copy(self, moves, stream):

@@ -286,3 +286,47 @@ def test_cache_refusals():
     c.free(a)
     with pytest.raises(KeyError):
         c.free(a)
+
+
+def state(c):
+    return (sorted(c._free), list(c._refs), {s: list(p) for s, p in c._pages.items()}, dict(c._lens),
+            c.k_pages.clone(), c.v_pages.clone())
+
+
+def same(a, b):
+    return a[:4] == b[:4] and torch.equal(a[4], b[4]) and torch.equal(a[5], b[5])
+
+
+class Failing(Host):
+    fail = False
+
+    def _copy(self, moves, stream):
+        if self.fail and moves:
+            raise fa.ForgeError(fa.FORGE_ERR_INVALID_ARG, "forge_attn_paged_copy")
+        super()._copy(moves, stream)
+
+
+def test_a_copy_that_fails_leaves_the_books_as_they_were():
+    pools = tuple(torch.zeros(2, 12, 1, 16, 1) for _ in range(2))
+    c = Failing(12, 1, 1, page_size=16, num_layers=2, pages=pools)
+    gone, a = c.new(), c.new()
+    c.extend([gone, a], [32, 20])
+    write(c, a, 0, range(1, 21))
+    b, d = c.fork(a), c.fork(a)
+    before = state(c)
+    c.fail = True
+    with pytest.raises(fa.ForgeError):
+        c.extend([a, b, d], [1, 30, 1])
+    assert same(state(c), before)
+    c.fail = False
+    assert c.extend([a, b, d], [1, 30, 1]) == [20, 20, 20]
+    assert read(c, b)[:20] == list(range(1, 21)) and len({c.pages(s)[1] for s in (a, b, d)}) == 3
+    c.free(gone)
+    before = state(c)
+    c.fail = True
+    with pytest.raises(fa.ForgeError):
+        c.compact()
+    assert same(state(c), before)
+    c.fail = False
+    assert c.compact() and read(c, b)[:20] == list(range(1, 21))
+    assert {p for s in (a, b, d) for p in c.pages(s)} == set(range(c.num_pages - c.free_pages))
