@@ -33,14 +33,25 @@ class PagedCache:
             raise ValueError("PagedCache: every size must be at least 1")
         if page_size % 16:
             raise ValueError(f"PagedCache: page_size must be a multiple of 16, got {page_size}")
+        import torch
         shape = (num_layers, num_pages, num_kv_heads, page_size, head_dim)
         if pages is None:
-            import torch
             dtype = torch.bfloat16 if dtype is None else dtype
+            self._check_kind(torch.device(device), dtype, head_dim)
             pages = tuple(torch.empty(shape, dtype=dtype, device=device) for _ in range(2))
-        for t in pages:
+        k, v = pages
+        for t in (k, v):
             if tuple(t.shape) != shape:
                 raise ValueError(f"PagedCache: pages of shape {tuple(t.shape)}, expected {shape}")
+            # (strides of dimensions of size 1 do not matter)
+            if any(n > 1 and s != w for n, s, w in zip(shape[2:], t.stride()[2:], (page_size * head_dim, head_dim, 1))):
+                raise ValueError(f"PagedCache: pages must be contiguous (strides {t.stride()})")
+        if (k.dtype, k.device) != (v.dtype, v.device) or (dtype is not None and k.dtype != dtype):
+            raise ValueError(f"PagedCache: pages of {k.dtype} on {k.device} and {v.dtype} on {v.device}"
+                             f"{'' if dtype is None else f', expected {dtype}'}")
+        if k.stride() != v.stride():
+            raise ValueError(f"PagedCache: pages with strides {k.stride()} and {v.stride()}, expected the same")
+        self._check_kind(k.device, k.dtype, head_dim)
         self.k_pages, self.v_pages = pages
         self.num_pages, self.page_size, self.num_layers = num_pages, page_size, num_layers
         self._free = list(range(num_pages))   # a heap: the lowest page first
@@ -48,6 +59,15 @@ class PagedCache:
         self._pages = {}                      # sequence -> its pages in order
         self._lens = {}                       # sequence -> tokens
         self._next = 0
+
+    @staticmethod
+    def _check_kind(device, dtype, head_dim):
+        """What the library's calls take: found out here, and not when a shared page is to be copied."""
+        import torch
+        if dtype not in (torch.bfloat16, torch.float32):
+            raise ValueError(f"PagedCache: unsupported dtype {dtype}")
+        if device.type == "cuda" and head_dim not in (64, 128, 256):
+            raise ValueError(f"PagedCache: head_dim must be 64, 128 or 256, got {head_dim}")
 
     # ------------------------------------------------------------------ the books
     @property

@@ -330,3 +330,25 @@ def test_a_copy_that_fails_leaves_the_books_as_they_were():
     c.fail = False
     assert c.compact() and read(c, b)[:20] == list(range(1, 21))
     assert {p for s in (a, b, d) for p in c.pages(s)} == set(range(c.num_pages - c.free_pages))
+
+
+def test_cache_refuses_pools_that_its_calls_could_not_take():
+    shape = (2, 4, 1, 16, 64)
+    ok = z(*shape)
+
+    def build(k, v, **kw):
+        return fa.PagedCache(4, 1, 64, page_size=16, num_layers=2, pages=(k, v), **kw)
+    assert build(ok, z(*shape)).num_pages == 4
+    assert build(z(4, 2, 1, 16, 64).transpose(0, 1), z(4, 2, 1, 16, 64).transpose(0, 1)).num_pages == 4  # layers inside
+    for k, v, kw, match in (
+            (ok, z(*shape, dtype=torch.float32), {}, "torch.bfloat16 on cpu and torch.float32 on cpu"),
+            (ok, z(*shape), dict(dtype=torch.float32), "expected torch.float32"),
+            (z(*shape, dtype=torch.float16), z(*shape, dtype=torch.float16), {}, "unsupported dtype"),
+            (ok, z(4, 2, 1, 16, 64).transpose(0, 1), {}, "expected the same"),
+            (z(2, 4, 1, 64, 16).transpose(3, 4), z(2, 4, 1, 64, 16).transpose(3, 4), {}, "must be contiguous")):
+        with pytest.raises(ValueError, match=match):
+            build(k, v, **kw)
+    with pytest.raises(ValueError, match="head_dim must be"):
+        fa.PagedCache(4, 1, 96)
+    with pytest.raises(ValueError, match="unsupported dtype"):
+        fa.PagedCache(4, 1, 64, dtype=torch.float16)
