@@ -89,8 +89,9 @@ class PagedCache:
 
     def fork(self, seq):
         """A new sequence with the same tokens. Shares seq's pages; nothing is copied yet."""
+        pages, length = list(self._pages[seq]), self._lens[seq]
         new = self.new()
-        self._pages[new], self._lens[new] = list(self._pages[seq]), self._lens[seq]
+        self._pages[new], self._lens[new] = pages, length
         for p in self._pages[new]:
             self._refs[p] += 1
         return new

@@ -352,3 +352,13 @@ def test_cache_refuses_pools_that_its_calls_could_not_take():
         fa.PagedCache(4, 1, 96)
     with pytest.raises(ValueError, match="unsupported dtype"):
         fa.PagedCache(4, 1, 64, dtype=torch.float16)
+
+
+def test_fork_of_an_unknown_sequence_changes_nothing():
+    c = make()
+    a = c.new()
+    c.extend([a], [5])
+    before = state(c)
+    with pytest.raises(KeyError):
+        c.fork(77)
+    assert same(state(c), before) and c.new() == a + 1
