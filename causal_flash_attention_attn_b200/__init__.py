@@ -21,6 +21,7 @@ import contextlib
 import ctypes
 import functools
 import math
+import operator
 import os
 
 __all__ = [
@@ -893,7 +894,13 @@ def _host_ints(what, name, x):
         if x.dtype == torch.int64 and x.numel() and (int(x.min()) < 0 or int(x.max()) >= 1 << 31):
             raise ValueError(f"{what}: {name} has a page number out of range")
         return x.to(torch.int32).contiguous()
-    return torch.tensor(list(x), dtype=torch.int32)
+    try:
+        pages = [operator.index(i) for i in x]
+    except TypeError:
+        raise ValueError(f"{what}: {name} must be a list of page numbers") from None
+    if pages and (min(pages) < -1 << 31 or max(pages) >= 1 << 31):
+        raise ValueError(f"{what}: {name} has a page number out of range")
+    return torch.tensor(pages, dtype=torch.int32)
 
 
 def paged_copy(k_pages, v_pages, src, dst, stream=None):

@@ -362,3 +362,14 @@ def test_fork_of_an_unknown_sequence_changes_nothing():
     with pytest.raises(KeyError):
         c.fork(77)
     assert same(state(c), before) and c.new() == a + 1
+
+
+@pytest.mark.parametrize("src,match", [([0.5], "list of page numbers"), ([2.0], "list of page numbers"), (["1"], "list of page"),
+                                       ([1 << 33], "out of range"), ([-1 << 40], "out of range")])
+def test_paged_copy_takes_whole_page_numbers_only(src, match):
+    with pytest.raises(ValueError, match=match):
+        fa.paged_copy(POOL, POOL, src, [0])
+    with pytest.raises(ValueError, match=match):
+        fa.paged_copy(POOL, POOL, [0], src)
+    with pytest.raises(ValueError, match="must be a CUDA tensor"):  # integers of any kind get on to the next check
+        fa.paged_copy(POOL, POOL, [torch.tensor(1), 2], iter([True, 3]))
