@@ -4,6 +4,7 @@ through the library's kernels (paged_append, paged_copy, attention_decode_paged)
 from __future__ import annotations
 
 import heapq
+from array import array
 
 
 class PagedCache:
@@ -16,12 +17,17 @@ class PagedCache:
             cache.append(layer, k[layer], v[layer], [a], starts, cu_seqlens)
         b = cache.fork(a)                             # shares a's pages
         ...
-        o, lse = cache.decode(layer, q, [a, b])
+        starts = cache.extend([a, b], [1, 1])         # a step: one token each
+        now = cache.tables([a, b])                    # once, for all layers
+        for layer in range(2):
+            cache.append(layer, k[layer], v[layer], [a, b], starts, tables=now)
+            o, lse = cache.decode(layer, q[layer], [a, b], tables=now)
 
     A page is shared by the forks of a sequence until one of them writes into it: extend() then
     gives that sequence a copy (its last, partly filled page only, in every layer). free() and compact()
-    return pages and close the gaps. Page tables are built on the host; tables() copies them
-    to the device.
+    return pages and close the gaps. Page tables are built on the host; tables() sends them to the
+    device, and append() and decode() do it themselves where they are given none. No call waits for the
+    device.
 
     k_pages, v_pages: [num_layers, num_pages, num_kv_heads, page_size, head_dim]; they may be given
     (pages=(k, v)) instead of being allocated.
@@ -171,14 +177,38 @@ class PagedCache:
             paged_copy(self.k_pages, self.v_pages, [a for a, _ in moves], [b for _, b in moves], stream=stream)
 
     # ------------------------------------------------------------------ on the device
-    def tables(self, seqs):
-        """(page_table int32 [len(seqs), width], seq_lens int32 [len(seqs)]) on the pools' device."""
-        import torch
+    def tables(self, seqs, stream=None):
+        """(page_table int32 [len(seqs), width], seq_lens int32 [len(seqs)]) on the pools' device, for append()
+        and decode() of every layer. Valid until the books change (extend, fork, free, compact)."""
+        seqs = list(seqs)
+        rows, width = self._rows(seqs)
+        rows.extend(self._lens[s] for s in seqs)
+        with self._on(stream):
+            t = self._send(rows)
+        return t[:len(seqs) * width].view(len(seqs), width), t[len(seqs) * width:]
+
+    def _rows(self, seqs):
+        """The page table's rows one after the other, and their width."""
         width = max([1] + [len(self._pages[s]) for s in seqs])
-        rows = [self._pages[s] + [0] * (width - len(self._pages[s])) for s in seqs]
+        rows = array("i")
+        for s in seqs:
+            pages = self._pages[s]
+            rows.extend(pages)
+            rows.extend([0] * (width - len(pages)))
+        return rows, width
+
+    def _send(self, ints):
+        """An array of ints as an int32 tensor on the pools' device: through pinned memory, so that
+        the host does not wait for the stream. (torch gives the pinned block away again only when the copy is done.)"""
+        import torch
         device = self.k_pages.device
-        return (torch.tensor(rows, dtype=torch.int32).to(device),
-                torch.tensor([self._lens[s] for s in seqs], dtype=torch.int32).to(device))
+        host = torch.frombuffer(ints, dtype=torch.int32) if len(ints) else torch.empty(0, dtype=torch.int32)
+        if device.type != "cuda":
+            return host.clone()
+        if torch.cuda.is_current_stream_capturing():
+            raise RuntimeError("PagedCache: a graph that is captured would send this moment's tables for ever: build them "
+                               "before, with tables(), and give them to append() and decode()")
+        return torch.empty(len(ints), dtype=torch.int32, pin_memory=True).copy_(host).to(device, non_blocking=True)
 
     def _on(self, stream):
         """The scope in which a call's tables are made: they belong to the stream that reads them, or
@@ -186,18 +216,36 @@ class PagedCache:
         from . import _NOTHING, _scope
         return _NOTHING if stream is None else _scope(self.k_pages.device, stream)
 
-    def append(self, layer, k, v, seqs, starts, cu_seqlens=None, stream=None):
-        """Write new tokens of one layer at the positions that extend() returned (paged_append)."""
+    @staticmethod
+    def _given(what, seqs, tables):
+        if seqs is not None and len(seqs) != tables[0].shape[0]:
+            raise ValueError(f"PagedCache.{what}: tables of {tables[0].shape[0]} sequences for {len(seqs)}")
+        return tables
+
+    def append(self, layer, k, v, seqs, starts, cu_seqlens=None, stream=None, tables=None):
+        """Write new tokens of one layer at the positions that extend() returned (paged_append). tables: what
+        tables(seqs) returned, so that nothing is built and sent again for another layer (seqs may be None
+        then); starts may be an int32 device tensor."""
         import torch
         from . import paged_append
+        ready = isinstance(starts, torch.Tensor) and starts.device == self.k_pages.device and starts.dtype == torch.int32
         with self._on(stream):
-            starts = torch.tensor(list(starts), dtype=torch.int32).to(self.k_pages.device)
-            table = self.tables(seqs)[0]
+            if tables is not None:
+                table = self._given("append", seqs, tables)[0]
+                starts = starts if ready else self._send(array("i", starts))
+            else:
+                seqs = list(seqs)
+                rows, width = self._rows(seqs)
+                at = len(rows)
+                if not ready:
+                    rows.extend(starts)
+                t = self._send(rows)
+                table, starts = t[:at].view(len(seqs), width), starts if ready else t[at:]
         paged_append(k, v, self.k_pages[layer], self.v_pages[layer], table, starts, cu_seqlens, stream)
 
-    def decode(self, layer, q, seqs, stream=None, **options):
-        """attention_decode_paged of one new query per sequence; options: scale, window, softcap, sink."""
+    def decode(self, layer, q, seqs, stream=None, tables=None, **options):
+        """attention_decode_paged of one new query per sequence; tables as in append(); options: scale, window,
+        softcap, sink."""
         from . import attention_decode_paged
-        with self._on(stream):
-            table, lens = self.tables(seqs)
+        table, lens = self.tables(seqs, stream) if tables is None else self._given("decode", seqs, tables)
         return attention_decode_paged(q, self.k_pages[layer], self.v_pages[layer], table, lens, stream=stream, **options)

@@ -449,3 +449,84 @@ def test_append_takes_empty_sequences_and_rows_behind_the_last(cu):
     for b in range(n):
         want[b, 0, :cu[b + 1] - cu[b]] = k[cu[b]:cu[b + 1], 0]
     assert torch.equal(kp, want) and torch.equal(vp, -want)
+
+
+def test_cache_calls_do_not_wait_for_the_device():
+    Hkv, D, seqs_n = 2, 64, 3
+    cache = fa.PagedCache(64, Hkv, D, page_size=16, num_layers=2, device=DEV)
+    seqs = [cache.new() for _ in range(seqs_n)]
+    k = torch.randn(60, Hkv, D, device=DEV).bfloat16()
+    q = torch.randn(seqs_n + 1, 4, D, device=DEV).bfloat16()
+    cu = torch.tensor([0, 20, 40, 60], dtype=torch.int32, device=DEV)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    torch.cuda.set_sync_debug_mode("error")
+    try:
+        starts = cache.extend(seqs, [20] * 3)
+        cache.append(0, k, k, seqs, starts, cu)
+        cache.append(1, k, k, seqs, starts, cu)
+        seqs.append(cache.fork(seqs[1]))
+        starts = cache.extend(seqs, [1] * 4)
+        now = cache.tables(seqs)
+        for layer in range(2):
+            cache.append(layer, k[:4], k[:4], seqs, starts, tables=now)
+            o, lse = cache.decode(layer, q, seqs, tables=now)
+        o2, lse2 = cache.decode(1, q, seqs)
+        side.wait_stream(torch.cuda.current_stream())
+        o3, lse3 = cache.decode(1, q, seqs, stream=side)
+        cache.free(seqs.pop(0))
+        assert cache.compact()
+    finally:
+        torch.cuda.set_sync_debug_mode("default")
+    torch.cuda.synchronize()
+    assert torch.equal(o, o2) and torch.equal(lse, lse2) and torch.equal(o, o3) and torch.equal(lse, lse3)
+    assert fa.forge_attn_check() == fa.FORGE_OK
+
+
+def test_a_captured_step_of_the_cache_follows_its_tables():
+    # one graph for a step of two layers; before each replay the new step's tables, starts and tokens are
+    # copied into the tensors that the graph reads. A second cache takes the same steps without a graph.
+    L, Hq, Hkv, D, n, steps = 2, 4, 2, 64, 3, 40
+    caches = [fa.PagedCache(40, Hkv, D, page_size=16, num_layers=L, device=DEV) for _ in range(2)]
+    for c in caches:
+        c.k_pages.zero_(), c.v_pages.zero_()
+    seqs = [[c.new() for _ in range(n)] for c in caches]
+    g = torch.Generator(device=DEV).manual_seed(8)
+    width = 4
+    table = torch.zeros(n, width, dtype=torch.int32, device=DEV)
+    lens, starts = (torch.zeros(n, dtype=torch.int32, device=DEV) for _ in range(2))
+    new = torch.zeros(L, n, Hq + 2 * Hkv, D, device=DEV, dtype=torch.bfloat16)
+
+    def step(c, s, at, tables):
+        out = []
+        for layer in range(L):
+            q, k, v = new[layer, :, :Hq], new[layer, :, Hq:Hq + Hkv], new[layer, :, Hq + Hkv:]
+            c.append(layer, k, v, s, at, tables=tables)
+            out += c.decode(layer, q.contiguous(), s, tables=tables)
+        return out
+    graph = torch.cuda.CUDAGraph()
+    pool_before = caches[0].k_pages.clone()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        got = step(caches[0], seqs[0], starts, (table, lens))
+    assert torch.equal(caches[0].k_pages, pool_before)
+    with pytest.raises(RuntimeError, match="build them before"):
+        with torch.cuda.graph(torch.cuda.CUDAGraph()):
+            caches[1].decode(0, new[0, :, :Hq].contiguous(), seqs[1])
+    for i in range(steps):
+        new.copy_(torch.randn(new.shape, generator=g, device=DEV))
+        at = [c.extend(s, [1] * n) for c, s in zip(caches, seqs)]
+        t, length = caches[0].tables(seqs[0])
+        table[:, :t.shape[1]] = t
+        lens.copy_(length)
+        starts.copy_(length - 1)
+        graph.replay()
+        want = step(caches[1], seqs[1], at[1], None)
+        for a, b in zip(got, want):
+            assert torch.equal(a, b), i
+        if i == 17:
+            for c, s in zip(caches, seqs):
+                c.free(s[0])
+                s[0] = c.fork(s[1])
+    assert torch.equal(caches[0].k_pages, caches[1].k_pages) and torch.equal(caches[0].v_pages, caches[1].v_pages)
+    assert fa.forge_attn_check() == fa.FORGE_OK

@@ -373,3 +373,34 @@ def test_paged_copy_takes_whole_page_numbers_only(src, match):
         fa.paged_copy(POOL, POOL, [0], src)
     with pytest.raises(ValueError, match="must be a CUDA tensor"):  # integers of any kind get on to the next check
         fa.paged_copy(POOL, POOL, [torch.tensor(1), 2], iter([True, 3]))
+
+
+def test_cache_tables_are_the_books_and_serve_every_layer(monkeypatch):
+    c = make()
+    a, b, e = c.new(), c.new(), c.new()
+    c.extend([a, b], [20, 40])
+    table, lens = c.tables(iter([b, e, a]))
+    assert table.tolist() == [c.pages(b), [0] * 3, c.pages(a) + [0]] and lens.tolist() == [40, 0, 20]
+    assert table.dtype == lens.dtype == torch.int32 and table.is_contiguous() and lens.is_contiguous()
+    assert c.tables([])[0].shape == (0, 1) and c.tables([])[1].shape == (0,)
+    got = []
+    monkeypatch.setattr(fa, "paged_append", lambda k, v, kp, vp, table, starts, cu, stream: got.append((table, starts)))
+    monkeypatch.setattr(fa, "attention_decode_paged", lambda q, kp, vp, table, lens, stream=None, **o: got.append((table, lens)))
+    # given tables are what the library gets, without being built again
+    given, device_starts = (table, lens), torch.tensor([1, 2, 3], dtype=torch.int32)
+    monkeypatch.setattr(c, "_rows", lambda seqs: pytest.fail("built again"))
+    c.append(0, None, None, [b, e, a], device_starts, tables=given)
+    c.append(1, None, None, None, [1, 2, 3], tables=given)
+    c.decode(1, None, [b, e, a], tables=given)
+    assert got[0][0] is table and got[0][1] is device_starts and got[1][0] is table and got[2] == given
+    assert got[1][1].tolist() == [1, 2, 3] and got[1][1].dtype == torch.int32
+    with pytest.raises(ValueError, match="tables of 3 sequences for 2"):
+        c.decode(0, None, [a, b], tables=given)
+    with pytest.raises(ValueError, match="tables of 3 sequences for 1"):
+        c.append(0, None, None, [a], [0], tables=given)
+    monkeypatch.undo()
+    # and without, the books of the call's moment
+    monkeypatch.setattr(fa, "paged_append", lambda k, v, kp, vp, table, starts, cu, stream: got.append((table, starts)))
+    for starts in ([20, 40], device_starts[:2]):
+        c.append(0, None, None, iter([a, b]), starts)
+        assert got[-1][0].tolist() == [c.pages(a) + [0], c.pages(b)] and got[-1][1].tolist() == list(starts)
