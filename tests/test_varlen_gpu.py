@@ -584,3 +584,36 @@ def test_training_without_the_residual(with_sink):
     if with_sink:
         assert torch.equal(got[3], want[3])
     assert fa.forge_attn_check() == fa.FORGE_OK
+
+
+# every compiled variant of the bf16 kernels that the cases above leave out: with and without a cap (scores of
+# standard deviation 4: a cap of 5 takes the exponential tanh, 50 the polynomial one), a window and a sink
+VARIANTS = [
+    ("d64_cap", "bf16", [300, 1, 129, 64], 3, 4, 2, 64, 0, 5.0, False, True),
+    ("d64_cap50", "bf16", [257, 128, 40], 0, 3, 3, 64, 0, 50.0, False, False),
+    ("d64_win_cap", "bf16", [385, 31, 200], 0, 4, 1, 64, 77, 50.0, False, True),
+    ("d64_cap_sink", "bf16", [300, 0, 129], 0, 4, 2, 64, 0, 5.0, True, False),
+    ("d64_win_cap_sink", "bf16", [300, 65], 2, 4, 2, 64, 90, 50.0, True, False),
+    ("d64_win_sink", "bf16", [300, 65], 2, 4, 2, 64, 90, 0.0, True, False),
+    ("d128_cap", "bf16", [300, 1, 129, 64], 3, 4, 2, 128, 0, 5.0, False, True),
+    ("d128_cap50", "bf16", [513, 128, 40], 0, 3, 3, 128, 0, 50.0, False, False),
+    ("d128_win_cap", "bf16", [385, 31, 200], 0, 4, 1, 128, 77, 50.0, False, True),
+    ("d128_sink", "bf16", [300, 0, 129, 600], 0, 4, 2, 128, 0, 0.0, True, False),
+    ("d128_win_sink", "bf16", [300, 65], 2, 7, 1, 128, 90, 0.0, True, False),
+    ("d128_cap_sink", "bf16", [300, 130], 0, 4, 2, 128, 0, 50.0, True, False),
+    ("d256_cap", "bf16", [300, 129, 64], 3, 4, 2, 256, 0, 5.0, False, True),
+    ("d256_win", "bf16", [300, 129, 64], 0, 2, 2, 256, 100, 0.0, False, False),
+    ("d256_sink", "bf16", [300, 0, 129], 0, 4, 2, 256, 0, 0.0, True, False),
+    ("f32_d64_win_cap_sink", "f32", [150, 0, 65], 3, 4, 2, 64, 40, 50.0, True, True),
+    ("f32_d128_cap_sink", "f32", [150, 33], 0, 4, 1, 128, 0, 5.0, True, False),
+]
+
+
+@pytest.mark.parametrize("case", VARIANTS, ids=[c[0] for c in VARIANTS])
+def test_variants_match_oracle_per_sequence(case):
+    test_matches_oracle_per_sequence(case)
+
+
+@pytest.mark.parametrize("case", [c for c in VARIANTS if c[1] == "bf16"], ids=[c[0] for c in VARIANTS if c[1] == "bf16"])
+def test_variants_with_the_residual(case):
+    test_the_residual_of_o_takes_its_rounding_out_of_the_gradients(case)
