@@ -198,6 +198,14 @@ struct FwdParams {
     bool for_dsink;  // VAR: the backward will form dsink from this o and o_res
 };
 
+// Bit c: key k0 + c is visible to query qi.
+__device__ __forceinline__ uint32_t visible32(int qi, int k0, int W) {
+    const int hi = qi - k0, lo = hi - W;  // lo < c <= hi
+    uint32_t vm = hi < 0 ? 0u : (hi >= 31 ? ~0u : (~0u >> (31 - hi)));
+    if (W > 0) vm &= lo < 0 ? ~0u : (lo >= 31 ? 0u : (~0u << (lo + 1)));
+    return vm;
+}
+
 // 32 f32 values of o times f, as bf16 pairs (hi), and the residuals' pairs (lo)
 __device__ __forceinline__ void o_pairs32(const uint32_t (&o)[32], float f, uint32_t (&hi)[16], uint32_t (&lo)[16]) {
 #pragma unroll
@@ -429,16 +437,19 @@ __global__ void __launch_bounds__(320, 1)
             const bool need_mask = (kt0 + C::BN - 1 > q0) || (W > 0 && kt0 <= q0 + C::BM - 1 - W);
             if (VAR && cap) {
                 // the warp's scores choose the tanh's form together: masked ones and those of rows
-                // past the end, which may hold another sequence's values, have no say in it
-                if (need_mask || q0 + C::BM > T) {
+                // past the end, which may hold another sequence's values, have no say in it (bit
+                // masks: with comparisons as below, 88 instead of 74 us on 3000 + 905 + 191 rows)
+                if (need_mask) {
 #pragma unroll
-                    for (int c = 0; c < 64; c++) {
-                        const int kj = k0 + c;
-                        if (!(kj <= qi && (W == 0 || kj > qi - W) && qi < T)) s[c >> 5][c & 31] = 0u;
+                    for (int h = 0; h < 2; h++) {
+                        const uint32_t vm = visible32(qi, k0 + 32 * h, W);
+#pragma unroll
+                        for (int c = 0; c < 32; c++)
+                            if (!((vm >> c) & 1u)) s[h][c] = 0u;
                     }
                 }
-                cap_scores(s[0], p.cap_in, p.cap_out);
-                cap_scores(s[1], p.cap_in, p.cap_out);
+                cap_scores(s[0], p.cap_in, p.cap_out, qi < T);
+                cap_scores(s[1], p.cap_in, p.cap_out, qi < T);
             } else if (cap) {
 #pragma unroll
                 for (int c = 0; c < 64; c++) {

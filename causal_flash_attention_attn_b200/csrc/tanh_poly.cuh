@@ -6,7 +6,10 @@
 // 50): for |y| <= 3/4, tanh(y) = y P(y^2) with P of degree 5, minimax in relative error
 // (Remez exchange; coefficients and their f32 error, 1.6e-7, from gen_tanh_poly.py), nine packed
 // f32x2 operations a pair. A warp takes it for a group of scores when none of its lanes
-// has one beyond 3/4, and tanh_via_ex2 for the whole group otherwise.
+// has one beyond 3/4, and tanh_via_ex2 for the whole group otherwise. Scores that may belong to
+// another sequence are kept out of that choice, so that its values never reach a result: the
+// callers set masked ones to 0, and lanes whose row lies past the sequence's end have no vote (what
+// comes out of a score beyond the limit there is not used).
 #pragma once
 
 #include "sm100.cuh"
@@ -26,20 +29,20 @@ __device__ __forceinline__ uint64_t tanh_poly2(uint64_t y2) {
     return f2_mul(p, y2);
 }
 
-// Whether every lane's N raw scores, times `in` (positive), are within the limit. A NaN
-// does not count: it comes out as NaN either way.
+// Whether the N raw scores of every lane with a vote, times `in` (positive), are within the
+// limit. A NaN does not count: it comes out as NaN either way.
 template <int N>
-__device__ __forceinline__ bool tanh_poly_fits(const uint32_t (&s)[N], float in) {
+__device__ __forceinline__ bool tanh_poly_fits(const uint32_t (&s)[N], float in, bool votes = true) {
     float m = 0.0f;
 #pragma unroll
     for (int c = 0; c < N; c += 2) m = fmax3(m, fabsf(__uint_as_float(s[c])), fabsf(__uint_as_float(s[c + 1])));
-    return __all_sync(0xffffffffu, m * in <= kTanhPolyLimit);
+    return __all_sync(0xffffffffu, m * in <= kTanhPolyLimit || !votes);
 }
 
 // s = out * tanh(in * s) for N raw scores
 template <int N>
-__device__ __forceinline__ void cap_scores(uint32_t (&s)[N], float in, float out) {
-    if (tanh_poly_fits<N>(s, in)) {
+__device__ __forceinline__ void cap_scores(uint32_t (&s)[N], float in, float out, bool votes) {
+    if (tanh_poly_fits<N>(s, in, votes)) {
         const uint64_t in2 = f2_make(in, in), out2 = f2_make(out, out);
 #pragma unroll
         for (int c = 0; c < N; c += 2) {

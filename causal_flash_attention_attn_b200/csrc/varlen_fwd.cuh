@@ -460,13 +460,12 @@ __global__ void __launch_bounds__(640, 1)
                         // the warp's scores choose the tanh's form together: masked ones and
                         // those of rows past the end, which may hold another sequence's values,
                         // have no say in it
-                        if ((dead | part) || r0 + 31 >= I.T) {
-                            const uint32_t keep = qi < I.T ? vm : 0u;
+                        if (dead | part) {
 #pragma unroll
                             for (int c = 0; c < 32; c++)
-                                if (!((keep >> c) & 1u)) s[c] = 0u;
+                                if (!((vm >> c) & 1u)) s[c] = 0u;
                         }
-                        cap_scores(s, p.cap_in, p.cap_out);
+                        cap_scores(s, p.cap_in, p.cap_out, qi < I.T);
                     }
                     if (dead | part) {
 #pragma unroll
