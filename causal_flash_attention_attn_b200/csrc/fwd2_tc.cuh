@@ -501,7 +501,10 @@ __global__ void __launch_bounds__(384, 1)
                 l = l * factor + ((r0_ + r1) + (r2 + r3));
             }
             // (a wait that ran out: the tile's warps leave together, behind their barrier below)
-            if (ok) ok = mbar_wait_warp(bar(C::B_O_FINAL + x), (uint32_t)(pass & 1), abort_flag);
+            if (!ok || !mbar_wait_warp(bar(C::B_O_FINAL + x), (uint32_t)(pass & 1), abort_flag)) {
+                ok = named_barrier_all(1 + x, 128, false);
+                break;
+            }
             tc_fence_after();
             // Stage this tile's O (bf16) in its Q buffer, which every MMA of the
             // item has finished reading once O_FINAL fired, in the 128-byte-swizzled
@@ -536,7 +539,7 @@ __global__ void __launch_bounds__(384, 1)
             __syncwarp();
             if (lane == 0) mbar_arrive(bar(C::B_O_EMPTY + x));
             if (has) fence_proxy_async_smem();
-            if (!(ok = named_barrier_all(1 + x, 128, ok))) break;
+            if (!(ok = named_barrier_all(1 + x, 128, true))) break;
             if (has) {
                 if (row == 0) {
                     for (int cb = 0; cb < C::NCB; cb++) tma_store_3d(&tmO, sO + cb * C::CB, cb * 64, q0, I.bh);

@@ -421,7 +421,10 @@ __global__ void __launch_bounds__(320, 1)
             const int buf = u & 1;
             const int k0 = (lo + u) * C::BN + hf * 64;  // first key of this half
             // (a wait that ran out: both warps of the rows leave behind their next barrier)
-            if (ok) ok = mbar_wait_warp(bar(C::B_S_FULL + buf), (uint32_t)((u >> 1) & 1), abort_flag);
+            if (!mbar_wait_warp(bar(C::B_S_FULL + buf), (uint32_t)((u >> 1) & 1), abort_flag)) {
+                ok = named_barrier_all(pair_bar, 64, false);
+                break;
+            }
             tc_fence_after();
             const uint32_t tS = tmem + lane_base + (buf ? C::COL_S1 : C::COL_S0);
             uint32_t s[2][32];
@@ -471,7 +474,7 @@ __global__ void __launch_bounds__(320, 1)
             // the row max over both halves: exchange through shared memory (both
             // halves have read all their scores, so P may go over S after this)
             xmax[(buf * 2 + hf) * 128 + row] = mh;
-            if (!(ok = named_barrier_all(pair_bar, 64, ok))) break;
+            if (!(ok = named_barrier_all(pair_bar, 64, true))) break;
             float mx = fmaxf(mh, xmax[(buf * 2 + (hf ^ 1)) * 128 + row]);
             if (!cap) mx *= p.scale_log2;
             mraw = fmaxf(mraw, mx);
@@ -480,7 +483,10 @@ __global__ void __launch_bounds__(320, 1)
             const float factor = moved ? ex2_approx(m - m_new) : 1.0f;
             if (__any_sync(0xffffffffu, moved && u > 0)) {
                 // rescale this half's O columns once PV of the previous tile has landed
-                ok = mbar_wait_warp(bar(C::B_O_READY), (uint32_t)((u - 1) & 1), abort_flag);
+                if (!mbar_wait_warp(bar(C::B_O_READY), (uint32_t)((u - 1) & 1), abort_flag)) {
+                    ok = u + 1 < n && named_barrier_all(pair_bar, 64, false);
+                    break;
+                }
                 tc_fence_after();
                 const float f = (moved && u > 0) ? factor : 1.0f;
 #pragma unroll 1
@@ -525,9 +531,11 @@ __global__ void __launch_bounds__(320, 1)
                 const int end = T - (lo + u) * C::BN;
                 if (end < C::BN) {
                     const int load = n > 1 ? min(2 * u + 2, n + u) : 1;
-                    if (ok)
-                        ok = mbar_wait_warp(bar(C::B_KV_FULL + load % C::NSTAGE), (uint32_t)((load / C::NSTAGE) & 1),
-                                            abort_flag);
+                    if (!mbar_wait_warp(bar(C::B_KV_FULL + load % C::NSTAGE), (uint32_t)((load / C::NSTAGE) & 1),
+                                        abort_flag)) {
+                        ok = u + 1 < n && named_barrier_all(pair_bar, 64, false);
+                        break;
+                    }
                     zero_tail_rows<C::BN, C::NCBV, 256>(sKV + (uint32_t)(load % C::NSTAGE) * C::SLOT, C::CB, end,
                                                         (int)threadIdx.x);
                     fence_proxy_async_smem();

@@ -428,7 +428,10 @@ __global__ void __launch_bounds__(640, 1)
             float l = p.sink && hf == 0 ? 1.0f : 0.0f;  // the sink's 1 counts once
             for (int j = lox; has && j <= hix; j++, cnt++) {
                 const int k0 = j * C::BN + 64 * hf;  // first key of this half
-                if (ok) ok = mbar_wait_warp(bar(C::B_S_FULL + x), (uint32_t)(cnt & 1), abort_flag);
+                if (!mbar_wait_warp(bar(C::B_S_FULL + x), (uint32_t)(cnt & 1), abort_flag)) {
+                    ok = named_barrier_all(pair_bar, 64, false);
+                    break;
+                }
                 tc_fence_after();
                 // classes of the two 32-key chunks for this warp's 32 rows (warp-uniform):
                 // bit q of `dead` = no key of chunk q is visible to any of the rows, bit q
@@ -499,7 +502,7 @@ __global__ void __launch_bounds__(640, 1)
                 // behind the next barrier.
                 float *xm = xmax + (x * 2 + (cnt & 1)) * 256 + row;
                 xm[128 * hf] = best;
-                if (!(ok = named_barrier_all(pair_bar, 64, ok))) break;
+                if (!(ok = named_barrier_all(pair_bar, 64, true))) break;
                 best = fmaxf(best, xm[128 * (hf ^ 1)]);
                 if constexpr (!CAP) best *= p.scale_log2;
                 const float m_new = (best > m + 8.0f) ? best : m;
@@ -535,8 +538,12 @@ __global__ void __launch_bounds__(640, 1)
                 const int end = I.T - j * C::BN;
                 if (end < C::BN) {
                     const int slotV = slot0 + 2 * (j - I.lo) + 1;
-                    ok = mbar_wait_warp(bar(C::B_KV_FULL + slotV % C::NSTAGE), (uint32_t)((slotV / C::NSTAGE) & 1),
-                                        abort_flag);
+                    if (!mbar_wait_warp(bar(C::B_KV_FULL + slotV % C::NSTAGE), (uint32_t)((slotV / C::NSTAGE) & 1),
+                                        abort_flag)) {
+                        // (behind the last tile the pair's next barrier is the one below)
+                        ok = j < hix && named_barrier_all(pair_bar, 64, false);
+                        break;
+                    }
                     zero_tail_rows<128, C::NCB, 256>(sKV + (uint32_t)(slotV % C::NSTAGE) * C::TILE, C::CB, end, t);
                     fence_proxy_async_smem();
                 }

@@ -41,6 +41,8 @@ def test_the_groups_answer_is_acted_upon(path):
     calls = len(re.findall(r"\bnamed_barrier_all\(", text))
     used = (len(re.findall(r"if \(!(?:\(ok = )?named_barrier_all\([^;]*?\)\)?\) break;", text)) +
             len(re.findall(r"\bok = named_barrier_all\([^;]*\);\s*(?:l \+=[^;]*;\s*)?if \(ok\)", text)) +
+            # (a warp whose own wait ran out)
+            len(re.findall(r"\bok = (?:u \+ 1 < n && |j < hix && )?named_barrier_all\([^;]*, false\);\s*break;", text)) +
             # (the pair's answer, carried to the tile's barrier)
             len(re.findall(r"ok = named_barrier_all\(pair_bar, 64, ok\);(?:(?!named_barrier|mbar_wait).)*"
                            r"if \(!named_barrier_all\(tile_bar, 256, ok\)\) break;", text, flags=re.S)))
