@@ -141,12 +141,16 @@ class PagedCache:
                     shared.append(s)
         if need + len(shared) > len(self._free):
             raise MemoryError(f"PagedCache: {need + len(shared)} pages needed, {len(self._free)} free")
-        # the copies come first: they touch free pages only, and may fail
-        copies = heapq.nsmallest(len(shared), self._free)
-        self._copy([(self._pages[s][-1], page) for s, page in zip(shared, copies)], stream)
-        for s in shared:
-            old = self._pages[s][-1]
-            self._pages[s][-1] = self._take()
+        # the copies come first: they write free pages only, and may fail
+        copies = [heapq.heappop(self._free) for _ in shared]
+        try:
+            self._copy([(self._pages[s][-1], page) for s, page in zip(shared, copies)], stream)
+        except BaseException:
+            for page in copies:
+                heapq.heappush(self._free, page)
+            raise
+        for s, page in zip(shared, copies):
+            old, self._pages[s][-1], self._refs[page] = self._pages[s][-1], page, 1
             self._drop(old)
         starts = []
         for s, n in zip(seqs, counts):
