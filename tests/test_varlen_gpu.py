@@ -614,3 +614,35 @@ def test_variants_match_oracle_per_sequence(case):
 @pytest.mark.parametrize("case", [c for c in VARIANTS if c[1] == "bf16"], ids=[c[0] for c in VARIANTS if c[1] == "bf16"])
 def test_variants_with_the_residual(case):
     test_the_residual_of_o_takes_its_rounding_out_of_the_gradients(case)
+
+
+@pytest.mark.parametrize("dtype,Hq,Hkv,D", [("bf16", 32, 2, 128), ("bf16", 64, 1, 64), ("bf16", 16, 1, 256), ("f32", 64, 1, 64)])
+def test_rows_whose_offsets_pass_32_bits(dtype, Hq, Hkv, D):
+    # q, o, dO and dq of more than 2^32 elements, in 8200 short sequences: the last ones are what they are in
+    # a call of their own, bit for bit, but for dk and dv (bf16) of the one of 300 rows: its first key tile has
+    # three query tiles, and in the small call, where a CTA's share is less than that, it is cut into parts
+    # (of two tiles at least, so that no other one is), whose sums add up in another order before they are rounded
+    lens = [128] * 8190 + [77, 128, 1, 300, 129, 64, 0, 200, 33, 128]
+    total = sum(lens)
+    tail = sum(lens[8190:])
+    assert total * Hq * D > 1 << 32
+    g = torch.Generator(device=DEV).manual_seed(4)
+    q, dO = (torch.randn(total, Hq, D, generator=g, device=DEV, dtype=TDT[dtype]) for _ in range(2))
+    k, v = (torch.randn(total, Hkv, D, generator=g, device=DEV, dtype=TDT[dtype]) for _ in range(2))
+    cu = torch.tensor([0] + list(np.cumsum(lens)), dtype=torch.int32, device=DEV)
+
+    def both(q, k, v, dO, cu):
+        o, lse, o_res = fa.attention_varlen_fwd(q, k, v, cu, return_residual=True)
+        return (o, lse.t(), *fa.attention_varlen_bwd(q, k, v, o, lse, dO, cu, o_res=o_res))
+    got = [x[-tail:].clone() for x in both(q, k, v, dO, cu)]
+    assert fa.forge_attn_check() == fa.FORGE_OK
+    q, k, v, dO = (x[-tail:].clone() for x in (q, k, v, dO))
+    torch.cuda.empty_cache()
+    want = both(q, k, v, dO, (cu[8190:] - cu[8190]).contiguous())
+    at = torch.ones(tail, dtype=torch.bool, device=DEV)
+    at[77 + 128 + 1:][:300] = dtype == "f32"
+    for i in (0, 1, 3, 4) if dtype == "bf16" else range(5):
+        rows = slice(None) if i < 2 else at
+        assert torch.equal(got[i][rows], want[i][rows]), i
+        check_close(str(i), got[i], want[i].double().cpu().numpy(), dtype)
+    check_close("dq", got[2], want[2].double().cpu().numpy(), dtype)
