@@ -350,7 +350,7 @@ __global__ void __launch_bounds__(384, 1)
                     // tile B's warps have left the item before even where this one gives them
                     // nothing to do (no PV waits for them then): a wait by parity must not fall
                     // two phases behind
-                    if (!I.hasB && pass > 0 &&
+                    if (hi1 < 0 && pass > 0 &&
                         !(ok = mbar_wait(bar(C::B_O_EMPTY + 1), (uint32_t)((pass - 1) & 1), abort_flag)))
                         break;
                     // O_FINAL fires once every MMA of the item (and before) has completed

@@ -82,7 +82,8 @@ def test_the_model_finds_the_lost_phase_without_the_wait():
 @pytest.mark.parametrize("name", ["varlen_fwd.cuh", "fwd2_tc.cuh"])
 def test_the_kernels_wait_before_the_last_commit(name):
     text = re.sub(r"//.*", "", open(os.path.join(CSRC, name)).read())
+    assert "hi1 = I.hasB ? I.tB : -1;" in text
     issuer = text[text.index("warp == C::W_MMA) {\n" if name == "varlen_fwd.cuh" else "issue_pv"):]
-    assert re.search(r"if \(!I\.hasB && pass > 0 &&\s*!\(ok = mbar_wait(_warp)?\(bar\(C::B_O_EMPTY \+ 1\), "
+    assert re.search(r"if \((?:!I\.hasB|hi1 < 0) && pass > 0 &&\s*!\(ok = mbar_wait(_warp)?\(bar\(C::B_O_EMPTY \+ 1\), "
                      r"\(uint32_t\)\(\(pass - 1\) & 1\), abort_flag\)\)\)\s*break;\s*"
                      r"(if \(lead\) \{\s*)?tc_commit\(bar\(C::B_O_FINAL \+ 0\)\);", issuer)
