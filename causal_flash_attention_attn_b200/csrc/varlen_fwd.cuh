@@ -13,9 +13,9 @@
 // Then the products pace the tile pair, and how they are issued matters (see the MMA issuer).
 // P is handed over in two chunks, the first 32 keys of both halves and the other 32, so that
 // half of P V runs under the second chunk's exponentials.
-// 16,384 tokens, 32 / 8 heads, D 128, window 4096: two softmax warpgroups 775 us, four 764,
-// with the products issued by an elected lane 700, with P in two chunks 687 (1.04 PFLOP/s of
-// the entries needed). A tile's chain is now, in cycles: row maximum 440, exchange 250,
+// 16,384 tokens, 32 / 8 heads, D 128, window 4096, at 1965 MHz: two softmax warpgroups 775 us, four
+// 764, with the products issued by an elected lane 700, with P in two chunks 687, now 689-694
+// (1.03 PFLOP/s of the entries needed); back to back, at 1000 W and 1695 MHz, 786. A tile's chain is now, in cycles: row maximum 440, exchange 250,
 // exponentials 1250, store and hand-off 400, products 1024, commit 400, with the tensor cores
 // busy for 2048 of 3800 a pair. Forming the first chunk's exponentials before the other half's
 // maximum is there, and again if it moved a row, measured slower (687 -> 728: spills).
@@ -29,8 +29,9 @@
 // PV_x(j), so that a softmax warp that sees S_x(j+1) may rescale O_x.
 //
 // Rows of the next sequence that a sequence's last tiles bring along are kept out: K's by the
-// causal mask, V's by zeroing them in shared memory (the softmax warps of the last tile, before
-// they hand its P to the MMA warp), O's by storing that tile row by row.
+// causal mask (and out of the choice of the cap's tanh, see tanh_poly.cuh), V's by zeroing them in
+// shared memory (the softmax warps of the last tile, before they hand its P to the MMA warp),
+// O's by storing that tile row by row.
 //
 // SPLIT: O += P V with P as two bf16 terms (P lo beside P hi in S's columns), so that
 // O, and with its residual the backward's Delta, are accurate to ~2^-17 instead of

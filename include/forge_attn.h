@@ -252,8 +252,8 @@ forge_status forge_attn_decode(const void *q, const void *k_cache, const void *v
  *  - q_stride, k_stride, v_stride: elements between two rows (>= heads * D, a multiple
  *    of 16 bytes), so that q, k and v may be parts of one projection's output. o, dO,
  *    dq, dk, dv and lse are dense.
- *  - Rows at or behind cu_seqlens[num_seqs] are not read. Outputs there are left as they
- *    were (flags = 0), or set to zero, lse to -inf (FORGE_VARLEN_CLEAR_TAIL).
+ *  - What rows at or behind cu_seqlens[num_seqs] hold (NaN included) does not matter. Outputs there
+ *    are left as they were (flags = 0), or set to zero, lse to -inf (FORGE_VARLEN_CLEAR_TAIL).
  *  - The lengths are read on the device: nothing synchronises, and a captured call
  *    follows the lengths that cu_seqlens holds at each replay. Lengths that do not ascend from
  *    0, or that pass `rows`, are reported as FORGE_ERR_INVALID_ARG by the next
@@ -272,7 +272,8 @@ forge_status forge_attn_decode(const void *q, const void *k_cache, const void *v
  *    limits of the dense calls with B = 1, T = rows.
  * workspace: 256-byte aligned device memory of at least the given size, overwritten:
  * the schedule, and in the backward Delta and (bf16) an f32 dq accumulator whose sequences
- * are padded to 128 rows. dq (bf16) is summed with f32 atomics whose order differs
+ * are padded to 128 rows, and f32 partial sums of key tiles that are cut along their queries (at
+ * most about 39 MB at D = 64, 80 MB at 128 and 256). dq (bf16) is summed with f32 atomics whose order differs
  * between calls; o, lse, dk, dv and everything in f32 are the same on every call. The backward
  * takes o and lse as forge_attn_varlen_fwd wrote them.
  */
