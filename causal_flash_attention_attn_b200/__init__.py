@@ -261,11 +261,12 @@ def forge_attn_varlen_fwd_workspace_size(num_seqs, rows, Hq, Hkv, D, dtype) -> i
 
 
 def forge_attn_varlen_fwd(q, k, v, o, o_res, lse, cu_seqlens, num_seqs, rows, Hq, Hkv, D, q_stride, k_stride, v_stride,
-                          scale, window, softcap, sink, flags, dtype, workspace, workspace_bytes,
+                          scale, window, softcap, sink, clear_tail, dtype, workspace, workspace_bytes,
                           stream=None) -> int:
+    """clear_tail: the C function's flags (FORGE_VARLEN_CLEAR_TAIL, FORGE_VARLEN_SINK_FIXED)."""
     return library().forge_attn_varlen_fwd(_ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(o_res), _ptr(lse),
                                            _ptr(cu_seqlens), num_seqs, rows, Hq, Hkv, D, int(q_stride), int(k_stride), int(v_stride), float(scale),
-                                           int(window), float(softcap), _ptr(sink), int(flags), int(dtype),
+                                           int(window), float(softcap), _ptr(sink), int(clear_tail), int(dtype),
                                            _ptr(workspace), int(workspace_bytes), _stream(stream))
 
 
@@ -274,12 +275,13 @@ def forge_attn_varlen_bwd_workspace_size(num_seqs, rows, Hq, Hkv, D, dtype) -> i
 
 
 def forge_attn_varlen_bwd(q, k, v, o, o_res, lse, dO, dq, dk, dv, cu_seqlens, num_seqs, rows, Hq, Hkv, D, q_stride, k_stride,
-                          v_stride, scale, window, softcap, sink, dsink, flags, dtype, workspace, workspace_bytes,
+                          v_stride, scale, window, softcap, sink, dsink, clear_tail, dtype, workspace, workspace_bytes,
                           stream=None) -> int:
+    """clear_tail: the C function's flags (FORGE_VARLEN_CLEAR_TAIL)."""
     return library().forge_attn_varlen_bwd(_ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(o_res), _ptr(lse), _ptr(dO), _ptr(dq), _ptr(dk),
                                            _ptr(dv), _ptr(cu_seqlens), num_seqs, rows, Hq, Hkv, D, int(q_stride),
                                            int(k_stride), int(v_stride), float(scale), int(window), float(softcap),
-                                           _ptr(sink), _ptr(dsink), int(flags), int(dtype), _ptr(workspace),
+                                           _ptr(sink), _ptr(dsink), int(clear_tail), int(dtype), _ptr(workspace),
                                            int(workspace_bytes), _stream(stream))
 
 
@@ -656,8 +658,8 @@ def attention_varlen_fwd(q, k, v, cu_seqlens, scale=None, window=0, softcap=0.0,
     may lie apart), cu_seqlens int32 [num_seqs + 1] on the device, from 0. Returns (o [rows,Hq,D], lse
     [Hq,rows]), or (o, lse, o_res) with return_residual: o's rounding residual for the backward (None in
     f32), and with a sink P in two terms for dsink, unless sink_fixed says that no gradient of the sink
-    will be asked for. Rows behind the last sequence get zeros, lse -inf there. Nothing synchronises; bad cu_seqlens
-    are reported by forge_attn_check."""
+    will be asked for. Rows behind the last sequence get zeros, lse -inf there. Nothing synchronises; bad
+    cu_seqlens are reported by forge_attn_check."""
     import torch
     what = "attention_varlen_fwd"
     rows, Hq, Hkv, D, (qs, ks, vs) = (_is_packed(q, k, v, cu_seqlens, sink) or
@@ -683,8 +685,8 @@ def attention_varlen_fwd(q, k, v, cu_seqlens, scale=None, window=0, softcap=0.0,
 def attention_varlen_bwd(q, k, v, o, lse, dO, cu_seqlens, scale=None, window=0, softcap=0.0, stream=None, *,
                          sink=None, o_res=None):
     """Backward of attention_varlen_fwd (its o and lse, and o_res if it returned one; dO contiguous).
-    Returns (dq, dk, dv), or (dq, dk, dv, dsink [Hq]) with a sink (which is needed for dsink only); zeros in the rows behind the last
-    sequence."""
+    Returns (dq, dk, dv), or (dq, dk, dv, dsink [Hq]) with a sink (which only dsink needs); zeros in the rows
+    behind the last sequence."""
     import torch
     what = "attention_varlen_bwd"
     rows, Hq, Hkv, D, (qs, ks, vs) = (_is_packed(q, k, v, cu_seqlens, sink) or

@@ -58,7 +58,7 @@ class PagedCache:
         if k.stride() != v.stride():
             raise ValueError(f"PagedCache: pages with strides {k.stride()} and {v.stride()}, expected the same")
         self._check_kind(k.device, k.dtype, head_dim)
-        self.k_pages, self.v_pages = pages
+        self.k_pages, self.v_pages = k, v
         self.num_pages, self.page_size, self.num_layers = num_pages, page_size, num_layers
         self._free = list(range(num_pages))   # a heap: the lowest page first
         self._refs = [0] * num_pages
@@ -183,7 +183,8 @@ class PagedCache:
     # ------------------------------------------------------------------ on the device
     def tables(self, seqs, stream=None):
         """(page_table int32 [len(seqs), width], seq_lens int32 [len(seqs)]) on the pools' device, for append()
-        and decode() of every layer. Valid until the books change (extend, fork, free, compact)."""
+        and decode() of every layer. Valid until the books change (extend, fork, free, compact). They are made on
+        `stream` (the current one), for calls on that stream."""
         seqs = list(seqs)
         rows, width = self._rows(seqs)
         rows.extend(self._lens[s] for s in seqs)
@@ -203,7 +204,8 @@ class PagedCache:
 
     def _send(self, ints):
         """An array of ints as an int32 tensor on the pools' device: through pinned memory, so that
-        the host does not wait for the stream. (torch gives the pinned block away again only when the copy is done.)"""
+        the host does not wait for the stream. (torch gives the pinned block away again only when the
+        copy is done.)"""
         import torch
         device = self.k_pages.device
         host = torch.frombuffer(ints, dtype=torch.int32) if len(ints) else torch.empty(0, dtype=torch.int32)
@@ -229,7 +231,7 @@ class PagedCache:
     def append(self, layer, k, v, seqs, starts, cu_seqlens=None, stream=None, tables=None):
         """Write new tokens of one layer at the positions that extend() returned (paged_append). tables: what
         tables(seqs) returned, so that nothing is built and sent again for another layer (seqs may be None
-        then); starts may be an int32 device tensor."""
+        then). starts: a list, or an int32 tensor on the pools' device, which is taken as it is."""
         import torch
         from . import paged_append
         ready = isinstance(starts, torch.Tensor) and starts.device == self.k_pages.device and starts.dtype == torch.int32

@@ -273,9 +273,9 @@ forge_status forge_attn_decode(const void *q, const void *k_cache, const void *v
  * workspace: 256-byte aligned device memory of at least the given size, overwritten:
  * the schedule, and in the backward Delta and (bf16) an f32 dq accumulator whose sequences
  * are padded to 128 rows, and f32 partial sums of key tiles that are cut along their queries (at
- * most about 39 MB at D = 64, 80 MB at 128 and 256). dq (bf16) is summed with f32 atomics whose order differs
- * between calls; o, lse, dk, dv and everything in f32 are the same on every call. The backward
- * takes o and lse as forge_attn_varlen_fwd wrote them.
+ * most about 39 MB at D = 64, 80 MB at 128 and 256). dq (bf16) is summed with f32 atomics whose
+ * order differs between calls; o, lse, dk, dv and everything in f32 are the same on every call.
+ * The backward takes o and lse as forge_attn_varlen_fwd wrote them.
  */
 enum {
     FORGE_VARLEN_CLEAR_TAIL = 1,     /* (any flags but the ones below count as this one) */

@@ -404,3 +404,12 @@ def test_cache_tables_are_the_books_and_serve_every_layer(monkeypatch):
     for starts in ([20, 40], device_starts[:2]):
         c.append(0, None, None, iter([a, b]), starts)
         assert got[-1][0].tolist() == [c.pages(a) + [0], c.pages(b)] and got[-1][1].tolist() == list(starts)
+
+
+def test_the_raw_calls_keep_their_keyword_and_the_cache_takes_any_pair():
+    import inspect
+    for fn in (fa.forge_attn_varlen_fwd, fa.forge_attn_varlen_bwd):
+        assert "clear_tail" in inspect.signature(fn).parameters
+    pools = iter((z(1, 4, 1, 16, 64), z(1, 4, 1, 16, 64)))
+    c = fa.PagedCache(4, 1, 64, page_size=16, pages=pools)
+    assert c.k_pages.shape == c.v_pages.shape == (1, 4, 1, 16, 64)
